@@ -60,7 +60,9 @@ enum qlora_status {
   QLORA_ERR_WORKSPACE = 5, /* workspace NULL or smaller than required       */
   QLORA_ERR_ALPHA = 6,     /* alpha is not finite                           */
   QLORA_ERR_ALIAS = 7,     /* an output overlaps an input                   */
-  QLORA_ERR_HIP = 8        /* a HIP runtime call or kernel launch failed    */
+  QLORA_ERR_HIP = 8,       /* a HIP runtime call or kernel launch failed    */
+  QLORA_ERR_TYPE = 9       /* an element type or loss kind is not one of the
+                              listed                                        */
 };
 
 #define QLORA_NF4_BLOCK 64   /* weights per first-level block constant      */
@@ -361,6 +363,154 @@ int qlora_forward_multi(const uint16_t *X, int64_t M, const qlora_nf4_t *W0, int
 int qlora_adam_step(uint16_t *P, float *W, const uint16_t *G, float *m, float *v, int64_t n,
                     float lr, float beta1, float beta2, float eps, float weight_decay,
                     int64_t step, void *stream);
+
+/*
+ * Element types of the logits (qlora_token_logprobs and the calls after it).
+ */
+enum qlora_dtype { QLORA_BF16 = 0, QLORA_F32 = 1 };
+
+/*
+ * qlora_token_logprobs, qlora_token_logprobs_backward -- the log-probability
+ * of each token's label under the logits of a head, and its gradient.  The
+ * head may be an adapted linear (qlora_forward with d = the vocabulary): the
+ * gradient written here is then the dY of its qlora_backward, and the
+ * reference policy of a preference or policy loss is the same weight with
+ * r = 0.  For token t with label y = labels[t] and tau = inv_temperature:
+ *
+ *   logp[t] = tau z_y - ln sum_v exp(tau z_v)          if 0 <= y < V
+ *   logp[t] = 0                                        otherwise (not counted)
+ *   dlogits[t, v] = dlogp[t] tau ([v == y] - p_v)      (0 when not counted)
+ *
+ *   logits   device, T rows of V elements of type dtype; row t starts at
+ *            element t*ld (ld >= V), any start that is a multiple of the
+ *            element's size.
+ *   labels   device, T int32.
+ *   logp     device, T fp32, written.
+ *   stats    device, T x 2 fp32, written (may be NULL in the forward): what
+ *            the backward needs of each row.
+ *   dlogp    device, T fp32.  With a label's cross-entropy this is -1/n.
+ *   dlogits  device, T rows of ldd elements (ldd >= V) of type dtype, all of
+ *            them written: columns V .. ldd-1 get zeros (a head padded to
+ *            whole tiles takes its dY whole).  May be the logits themselves
+ *            (same pointer and ld == ldd); any other overlap is
+ *            QLORA_ERR_ALIAS.
+ *
+ * A token that is not counted, or whose dlogp is 0, has zero gradient
+ * whatever its logits hold (they are not read).  Values of -inf are masked
+ * words (probability 0); a row with a NaN, +inf or nothing but -inf gives
+ * NaN.  Sums are fp32 in a fixed order: results are deterministic.
+ *
+ * T >= 0 (T == 0 is a no-op), 1 <= V <= ld < 2^30, no limit of 2^31 on T*ld;
+ * fp32 and int32 arrays are 4-byte aligned; inv_temperature is positive and
+ * finite (QLORA_ERR_ALPHA otherwise).
+ */
+int qlora_token_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                         const int32_t *labels, float inv_temperature, float *logp, float *stats,
+                         void *stream);
+int qlora_token_logprobs_backward(const float *dlogp, const void *logits, int32_t dtype, int64_t T,
+                                  int64_t V, int64_t ld, const int32_t *labels,
+                                  float inv_temperature, const float *stats, void *dlogits,
+                                  int64_t ldd, void *stream);
+
+/*
+ * qlora_preference_loss -- loss of P pairs of sequences, the first of a pair
+ * preferred over the second, from their tokens' log-probabilities, with the
+ * gradient in them.  cu_seqlens (device, 2P + 1 int32, non-decreasing) holds
+ * the offsets of the sequences: s = 0 .. P-1 are the chosen ones and P ..
+ * 2P-1 the rejected ones, sequence s being tokens cu[s] .. cu[s+1]-1 (it may
+ * be empty).  Over a sequence's counted tokens (0 <= label < V)
+ *
+ *   l_s = sum (logp[t] - ref_logp[t])     (average != 0: divided by their
+ *                                          number, at least 1)
+ *   h   = beta (l_p - l_{P+p}) - margin
+ *
+ *   QLORA_PREF_SIGMOID   loss = (1-e) softplus(-h) + e softplus(h),
+ *                        e = label_smoothing
+ *   QLORA_PREF_HINGE     loss = max(0, 1 - h)
+ *   QLORA_PREF_SQUARED   loss = ((h - 1/2) / beta)^2
+ *
+ *   ref_logp device, T fp32, or NULL (no reference).
+ *   weight   device, P fp32, or NULL (ones): pair p's weight in dlogp.
+ *   loss     device, P fp32, written (unweighted).
+ *   reward   device, 2P fp32, written: beta l_s.  May be NULL.
+ *   dlogp    device, T fp32, written: d(sum_p weight[p] loss[p]) / d logp;
+ *            0 for tokens that are not counted or in no sequence.  May be
+ *            NULL (evaluation).
+ *
+ * Sums are fp64.  Offsets are clamped to [0, T]; offsets that decrease leave
+ * dlogp unspecified where sequences overlap or leave gaps.
+ *
+ * P >= 0 (P == 0 is a no-op), P < 2^20, 0 <= T < 2^31; beta > 0 and finite, label_smoothing
+ * in [0, 1/2], margin finite (QLORA_ERR_ALPHA otherwise).
+ */
+enum qlora_preference { QLORA_PREF_SIGMOID = 0, QLORA_PREF_HINGE = 1, QLORA_PREF_SQUARED = 2 };
+int qlora_preference_loss(const float *logp, const float *ref_logp, const int32_t *labels, int64_t T,
+                          int64_t V, const int32_t *cu_seqlens, int64_t P, int32_t kind,
+                          int32_t average, float beta, float label_smoothing, float margin,
+                          const float *weight, float *loss, float *reward, float *dlogp,
+                          void *stream);
+
+/*
+ * qlora_policy_loss -- clipped policy loss with a KL term per token, from the
+ * logits, and its gradient in them in the same call.  With lp the label's
+ * log-probability (as in qlora_token_logprobs), r = exp(lp - old_logp[t]),
+ * A = advantages[t] and x = ref_logp[t] - lp:
+ *
+ *   loss[t] = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
+ *             + kl_coef kl[t],      kl[t] = exp(x) - x - 1
+ *   dlogits = d(sum_t weight[t] loss[t]) / d logits
+ *
+ * and 0 for tokens that are not counted.
+ *
+ *   old_logp device, T fp32, or NULL: the policy itself (r = 1).
+ *   ref_logp device, T fp32, or NULL: no KL term (kl is then 0).
+ *   weight   device, T fp32, or NULL (ones): 1/n of a token's mean, say.
+ *   loss, logp  device, T fp32, written.   kl  T fp32, written, or NULL.
+ *   dlogits, ldd as in qlora_token_logprobs_backward; NULL: no gradient.
+ *
+ * logits, labels, T, V, ld, dtype and inv_temperature as in
+ * qlora_token_logprobs.  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0,
+ * all finite (QLORA_ERR_ALPHA otherwise).
+ */
+int qlora_policy_loss(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                      const int32_t *labels, float inv_temperature, const float *advantages,
+                      const float *old_logp, const float *ref_logp, const float *weight,
+                      float clip_low, float clip_high, float kl_coef, float *loss, float *kl,
+                      float *logp, void *dlogits, int64_t ldd, void *stream);
+
+/*
+ * qlora_muon_step -- one step of momentum with an orthogonalised update
+ * (Newton-Schulz iteration, as in the Muon optimiser) on nmat adapter factors
+ * of rows x cols each, stacked without gaps (the A of several sections or
+ * layers, or their B), with an fp32 master copy.  Per matrix:
+ *
+ *   m = momentum m + g
+ *   u = g + momentum m (nesterov != 0) or m
+ *   X = u / (|u|_F + eps)
+ *   ns_steps times:  X = a X + (b G + c G^2) X,  G = X X^T
+ *   W = (1 - lr weight_decay) W - lr scale X
+ *   P = bf16(W)
+ *
+ *   P, W, G, m  as in qlora_adam_step, without v: nmat*rows*cols elements
+ *          each (W and m in any memory the GPU addresses).
+ *   coef   HOST array of 3*ns_steps floats, (a, b, c) of each step; NULL
+ *          takes (3.4445, -4.7750, 2.0315) for every step, the coefficients
+ *          published with the optimiser.
+ *   ws     device workspace of qlora_muon_workspace_bytes(nmat, rows, cols).
+ *
+ * The iteration runs on the min(rows, cols)-square Gram matrix in fp64, so
+ * that side is at most 64 (QLORA_ERR_RANK).  Non-finite gradients give
+ * non-finite weights in their own matrix only.
+ * 1 <= ns_steps <= 16, 0 <= nmat <= 65535 (nmat == 0 is a no-op), rows and
+ * cols >= 1, fewer than 2^31 elements in all (QLORA_ERR_SHAPE); all pointers
+ * 16-byte aligned and disjoint; momentum in [0, 1), lr and weight_decay >= 0,
+ * eps > 0, all of them and scale and coef finite (QLORA_ERR_ALPHA otherwise).
+ */
+size_t qlora_muon_workspace_bytes(int64_t nmat, int64_t rows, int64_t cols);
+int qlora_muon_step(uint16_t *P, float *W, const uint16_t *G, float *m, int64_t nmat, int64_t rows,
+                    int64_t cols, float lr, float momentum, int32_t nesterov, float weight_decay,
+                    float scale, float eps, int32_t ns_steps, const float *coef, void *ws,
+                    size_t ws_bytes, void *stream);
 
 /*
  * lora_merge -- deploy-time merge W = bf16_rne(w~ + s B A), d x k bf16

@@ -12,6 +12,9 @@ The calls mirror include/qlora.h:
 * ``backward(dY, X, w, A, B, alpha)``  -> ``dX, dA, dB``
 * ``merge(w, A, B, alpha)``            -> bf16 ``W``
 * ``unmerge(W, A, B, alpha)``          -> bf16 ``W0``
+* ``token_logprobs(logits, labels)``   -> fp32 ``logp`` (and row statistics)
+* ``preference_loss(logp, ...)``, ``policy_loss(logits, ...)`` -> losses and gradients
+* ``adam_step``, ``muon_step``         -> the adapters' optimiser steps
 """
 
 from __future__ import annotations
@@ -74,6 +77,16 @@ _sigs = {
     "qlora_forward_multi": (ctypes.c_int, [_vp, _i64, _P, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _vp,
                                            _sz, _vp]),
     "qlora_adam_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _f32, _f32, _f32, _i64, _vp]),
+    "qlora_token_logprobs": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _vp]),
+    "qlora_token_logprobs_backward": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _i64,
+                                                     _vp]),
+    "qlora_preference_loss": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _f32, _f32, _f32, _vp,
+                                             _vp, _vp, _vp, _vp]),
+    "qlora_policy_loss": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _vp, _vp, _f32, _f32, _f32,
+                                         _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qlora_muon_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "qlora_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _f32, _i32, _f32, _f32, _f32, _i32,
+                                       ctypes.POINTER(ctypes.c_float), _vp, _sz, _vp]),
     "lora_merge": (ctypes.c_int, [_P, _vp, _vp, _i32, _f32, _vp, _vp]),
     "lora_unmerge": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _vp]),
     "qlora_timing_enable": (ctypes.c_int, [ctypes.c_int]),
@@ -90,7 +103,7 @@ for _name, (_res, _args) in _sigs.items():
 EXPORTED = tuple(_sigs)
 STATUS = {0: "QLORA_OK", 1: "QLORA_ERR_NULL", 2: "QLORA_ERR_SHAPE", 3: "QLORA_ERR_RANK",
           4: "QLORA_ERR_ALIGN", 5: "QLORA_ERR_WORKSPACE", 6: "QLORA_ERR_ALPHA",
-          7: "QLORA_ERR_ALIAS", 8: "QLORA_ERR_HIP"}
+          7: "QLORA_ERR_ALIAS", 8: "QLORA_ERR_HIP", 9: "QLORA_ERR_TYPE"}
 
 
 class QloraError(RuntimeError):
@@ -389,6 +402,183 @@ def adam_step(P: torch.Tensor, W: torch.Tensor, G: torch.Tensor, m: torch.Tensor
                                 int(step), _stream(P.device)), "qlora_adam_step")
 
 
+# ------------------------------------------------ losses on the logits ----
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+
+
+def _on_gpu(t: torch.Tensor):
+    if t.device.type != "cuda":
+        raise ValueError("the tensors have to be on a GPU")
+    return t.device
+
+
+def _rows(logits: torch.Tensor):
+    """(T, V, row stride) of logits whose rows are contiguous."""
+    if logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise TypeError("logits are a T x V tensor of bfloat16 or float32")
+    T, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of one token have to be contiguous")
+    return T, V, (logits.stride(0) if T > 1 else V)
+
+
+def _per(name: str, t, n: int, dtype, device):
+    """Pointer of an optional contiguous vector of n values on ``device``."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} is a contiguous vector of {n} {dtype} on {device}")
+    return t.data_ptr()
+
+
+def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
+    """The tensor that receives dlogits and its row stride.  Rows are written
+    to their whole stride, so the storage has to hold them."""
+    if out is None:
+        # a padded head's gradient keeps the padding (as zeros), with rows
+        # that start where the logits' rows do
+        ldd = ld if ld - V < 256 else V
+        return torch.empty((T, ldd), dtype=logits.dtype, device=logits.device)[:, :V], ldd
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out has the shape, type and device of the logits")
+    if V > 1 and out.stride(1) != 1:
+        raise ValueError("the gradient of one token has to be contiguous")
+    ldd = out.stride(0) if T > 1 else V
+    room = out.untyped_storage().nbytes() // out.element_size() - out.storage_offset()
+    if T * ldd > room:
+        raise ValueError("out's last row ends before its stride: the rows are written whole")
+    return out, ldd
+
+
+def token_logprobs(logits: torch.Tensor, labels: torch.Tensor, inv_temperature: float = 1.0,
+                   save_stats: bool = False):
+    """Log-probability of each token's label (fp32 [T]) under T x V logits
+    (bf16 or fp32; rows may be a slice of a wider matrix).  A label (int32)
+    outside [0, V) gives 0.  With ``save_stats`` also returns the rows'
+    statistics for ``token_logprobs_backward``."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    y = _per("labels", labels, T, torch.int32, dev)
+    logp = torch.empty(T, dtype=torch.float32, device=_on_gpu(logits))
+    stats = torch.empty((T, 2), dtype=torch.float32, device=dev) if save_stats else None
+    _check(_lib.qlora_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature),
+                                     logp.data_ptr(), _ptr(stats), _stream(dev)), "qlora_token_logprobs")
+    return (logp, stats) if save_stats else logp
+
+
+def token_logprobs_backward(dlogp: torch.Tensor, logits: torch.Tensor, labels: torch.Tensor, stats: torch.Tensor,
+                            inv_temperature: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient in the logits for ``dlogp`` = d loss / d logp (fp32 [T]).
+    ``out`` may be the logits themselves.  Rows of ``out`` are written to
+    their whole stride: of a slice ``dY[:, :V]`` the columns from V on get
+    zeros, so dY is ready for the head's backward."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    g = _per("dlogp", dlogp, T, torch.float32, dev)
+    y = _per("labels", labels, T, torch.int32, dev)
+    if stats.shape != (T, 2):
+        raise ValueError("stats are the T x 2 values that token_logprobs returned")
+    s = _per("stats", stats.view(-1), 2 * T, torch.float32, dev)
+    out, ldd = _grad_rows(logits, out, T, V, ld)
+    _on_gpu(logits)
+    _check(_lib.qlora_token_logprobs_backward(g, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y,
+                                              float(inv_temperature), s, out.data_ptr(), ldd, _stream(dev)),
+           "qlora_token_logprobs_backward")
+    return out
+
+
+def preference_loss(logp: torch.Tensor, labels: torch.Tensor, vocab: int, cu_seqlens: torch.Tensor, beta: float,
+                    ref_logp: torch.Tensor | None = None, kind: str = "sigmoid", average: bool = False,
+                    label_smoothing: float = 0.0, margin: float = 0.0, weight: torch.Tensor | None = None,
+                    need_grad: bool = True):
+    """(loss [P], reward [2P], dlogp [T]) of P pairs of sequences at offsets
+    ``cu_seqlens`` (int32 [2P + 1]; the P chosen ones first, then the P
+    rejected ones), from the tokens' log-probabilities under the policy and,
+    optionally, a reference.  ``kind`` is "sigmoid", "hinge" or "squared";
+    ``weight`` [P] weights the pairs in dlogp.  dlogp is None without
+    ``need_grad``."""
+    if kind not in _KINDS:
+        raise ValueError(f"kind is one of {sorted(_KINDS)}")
+    if logp.dim() != 1 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 != 1:
+        raise ValueError("logp is a vector and cu_seqlens holds 2P + 1 offsets")
+    T, P, dev = logp.shape[0], cu_seqlens.shape[0] // 2, logp.device
+    lp = _per("logp", logp, T, torch.float32, dev)
+    y = _per("labels", labels, T, torch.int32, dev)
+    cu = _per("cu_seqlens", cu_seqlens, 2 * P + 1, torch.int32, dev)
+    ref = _per("ref_logp", ref_logp, T, torch.float32, dev)
+    wt = _per("weight", weight, P, torch.float32, dev)
+    loss = torch.empty(P, dtype=torch.float32, device=_on_gpu(logp))
+    reward = torch.empty(2 * P, dtype=torch.float32, device=dev)
+    dlogp = None
+    if need_grad:  # without a pair there is no loss and nothing is launched
+        dlogp = (torch.empty if P else torch.zeros)(T, dtype=torch.float32, device=dev)
+    _check(_lib.qlora_preference_loss(lp, ref, y, T, int(vocab), cu, P, _KINDS[kind], int(average), float(beta),
+                                      float(label_smoothing), float(margin), wt, loss.data_ptr(), reward.data_ptr(),
+                                      _ptr(dlogp), _stream(dev)), "qlora_preference_loss")
+    return loss, reward, dlogp
+
+
+def policy_loss(logits: torch.Tensor, labels: torch.Tensor, advantages: torch.Tensor,
+                old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None,
+                weight: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, inv_temperature: float = 1.0, need_grad: bool = True,
+                out: torch.Tensor | None = None):
+    """(loss [T], kl [T], logp [T], dlogits) of the clipped policy loss with a
+    KL term, per token; dlogits is the gradient of sum(weight * loss) and is
+    None without ``need_grad``.  ``out`` as in ``token_logprobs_backward``
+    (it may be the logits)."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    y = _per("labels", labels, T, torch.int32, dev)
+    vec = [_per(n, t, T, torch.float32, dev) for n, t in (("advantages", advantages), ("old_logp", old_logp),
+                                                          ("ref_logp", ref_logp), ("weight", weight))]
+    loss, kl, logp = (torch.empty(T, dtype=torch.float32, device=_on_gpu(logits)) for _ in range(3))
+    dlogits, ldd = _grad_rows(logits, out, T, V, ld) if need_grad else (None, 0)
+    _check(_lib.qlora_policy_loss(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature), *vec,
+                                  float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), kl.data_ptr(),
+                                  logp.data_ptr(), _ptr(dlogits), ldd, _stream(dev)), "qlora_policy_loss")
+    return loss, kl, logp, dlogits
+
+
+def muon_step(P: torch.Tensor, W: torch.Tensor, G: torch.Tensor, m: torch.Tensor, lr: float, momentum: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, ns_steps: int = 5, scale: float | None = None,
+              coefficients=None, eps: float = 1e-7) -> None:
+    """One step of momentum with an orthogonalised update on one adapter
+    factor (rows x cols) or a stack of them (n x rows x cols, as the A or B
+    of several sections): W and m (fp32) in place, P = bf16(W); G bf16
+    gradients.  ``scale`` is the update's size in units of lr, by default
+    sqrt(max(1, rows / cols)); ``coefficients`` is one (a, b, c) for every
+    step or a sequence of ns_steps of them."""
+    if W.dim() not in (2, 3):
+        raise ValueError("W is rows x cols or n x rows x cols")
+    rows, cols = W.shape[-2:]
+    nmat = W.shape[0] if W.dim() == 3 else 1
+    for name, t, dtype in (("P", P, torch.bfloat16), ("W", W, torch.float32), ("G", G, torch.bfloat16),
+                           ("m", m, torch.float32)):
+        if t.dtype != dtype or t.shape != W.shape or not t.is_contiguous():
+            raise ValueError(f"{name} is contiguous, {dtype}, of shape {tuple(W.shape)}")
+    if scale is None:
+        scale = max(1.0, rows / max(1, cols)) ** 0.5
+    coef = None
+    if coefficients is not None:
+        c = [list(t) for t in coefficients] if isinstance(coefficients[0], (list, tuple)) \
+            else [list(coefficients)] * ns_steps
+        if len(c) != ns_steps or any(len(t) != 3 for t in c):
+            raise ValueError("coefficients: (a, b, c), or ns_steps of them")
+        coef = (ctypes.c_float * (3 * ns_steps))(*[v for t in c for v in t])
+    dev = _on_gpu(P)
+    # like adam_step's, the fp32 state may be paged out to pinned host memory
+    if G.device != dev or any(t.device != dev and not t.is_pinned() for t in (W, m)):
+        raise ValueError(f"P and G have to be on one GPU ({dev}), W and m there or in pinned host memory")
+    ws = _workspace(_lib.qlora_muon_workspace_bytes(nmat, rows, cols), dev)
+    _check(_lib.qlora_muon_step(P.data_ptr(), W.data_ptr(), G.data_ptr(), m.data_ptr(), nmat, rows, cols, float(lr),
+                                float(momentum), int(nesterov), float(weight_decay), float(scale), float(eps),
+                                int(ns_steps), coef, _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)),
+           "qlora_muon_step")
+
+
 def merge(w: NF4Weight, A=None, B=None, alpha: float = 0.0, out=None) -> torch.Tensor:
     """W = bf16(w~ + (alpha/r) B A), d x k bf16 (one section at a time:
     ``merge(w.section(p), A_p, B_p, alpha)``)."""
@@ -418,7 +608,8 @@ class kernel_timing:
     NAMES = ("quant_blocks", "quant_group_sums", "quant_mean", "quant_dq", "merge", "unmerge",
              "prep_adapters", "lora_proj", "lora_proj_finish", "token_reduce",
              "token_reduce_finish", "fwd_decode", "fwd_decode_finish", "fwd_rich", "dx", "drop_input", "adam",
-             "fwd_sum_splits", "dx_sum_splits")
+             "fwd_sum_splits", "dx_sum_splits", "logprob", "logprob_grad", "preference", "policy", "muon_gram",
+             "muon_poly", "muon_apply")
 
     def __enter__(self):
         _check(_lib.qlora_timing_reset(), "qlora_timing_reset")
@@ -444,4 +635,5 @@ class kernel_timing:
 
 __all__ = ["kernel_timing", "NF4Weight", "QloraError", "quantize", "forward", "backward", "merge", "unmerge",
            "quantize_sections", "forward_sections", "backward_sections", "forward_multi", "forward_dropout",
-           "backward_dropout", "backward_noalloc", "adam_step", "nf4_levels", "nf4_sizes", "lib", "EXPORTED", "LIB_PATH"]
+           "backward_dropout", "backward_noalloc", "adam_step", "token_logprobs", "token_logprobs_backward",
+           "preference_loss", "policy_loss", "muon_step", "nf4_levels", "nf4_sizes", "lib", "EXPORTED", "LIB_PATH"]

@@ -276,6 +276,25 @@ static int scratch_for_stream(hipStream_t stream, void** out) {
   return QLORA_OK;
 }
 
+// ----------------------------------------------------------- regions ----
+
+struct Region {
+  const void* p;
+  size_t n;
+};
+
+// No output may overlap an input or another output (null regions never do).
+template <int NO, int NI>
+static bool any_alias(const Region (&out)[NO], const Region (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
 }  // namespace qlora
 
 using namespace qlora;
@@ -293,6 +312,7 @@ const char* qlora_status_string(int status) {
     case QLORA_ERR_ALPHA: return "alpha is not finite";
     case QLORA_ERR_ALIAS: return "an output overlaps an input";
     case QLORA_ERR_HIP: return "HIP runtime or kernel launch failure";
+    case QLORA_ERR_TYPE: return "element type or loss kind is not one of the listed";
     default: return "unknown status";
   }
 }
@@ -682,6 +702,168 @@ int qlora_adam_step(uint16_t* P, float* W, const uint16_t* G, float* m, float* v
       if (overlaps(pp[i], pn[i], pp[j], pn[j])) return QLORA_ERR_ALIAS;
   return hip_status(launch_adam(W, G, m, v, P, n, lr, beta1, beta2, eps, weight_decay, step,
                                 reinterpret_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------- losses on the logits --
+
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+constexpr int64_t kMaxCols = (int64_t)1 << 30;  // row strides: column indexes and their strides fit 32 bits
+
+// logits (T rows of V, stride ld) and labels
+static int check_logits(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* labels,
+                        float tau) {
+  if (dtype != QLORA_BF16 && dtype != QLORA_F32) return QLORA_ERR_TYPE;
+  if (T < 0 || T >= kMaxElems || V < 1 || ld < V || ld >= kMaxCols) return QLORA_ERR_SHAPE;
+  if (!(tau > 0.0f) || !std::isfinite(tau)) return QLORA_ERR_ALPHA;
+  if (T == 0) return QLORA_OK;
+  if (logits == nullptr || labels == nullptr) return QLORA_ERR_NULL;
+  if (((uintptr_t)logits & (dtype == QLORA_F32 ? 3u : 1u)) != 0 || !aligned4(labels)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+// Bytes from the first element of the first row to the last of the last.
+static size_t rows_bytes(int32_t dtype, int64_t T, int64_t cols, int64_t ld) {
+  return (size_t)((T - 1) * ld + cols) * (dtype == QLORA_F32 ? 4 : 2);
+}
+
+// dlogits: T whole rows of ldd; the logits themselves or apart from them.
+static int check_dlogits(const void* dlogits, int64_t ldd, const void* logits, int32_t dtype, int64_t T, int64_t V,
+                         int64_t ld) {
+  if (ldd < V || ldd >= kMaxCols) return QLORA_ERR_SHAPE;
+  if (((uintptr_t)dlogits & (dtype == QLORA_F32 ? 3u : 1u)) != 0) return QLORA_ERR_ALIGN;
+  if (dlogits == logits && ldd == ld) return QLORA_OK;
+  return overlaps(dlogits, rows_bytes(dtype, T, ldd, ldd), logits, rows_bytes(dtype, T, V, ld)) ? QLORA_ERR_ALIAS
+                                                                                              : QLORA_OK;
+}
+
+int qlora_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* labels,
+                         float inv_temperature, float* logp, float* stats, void* stream) {
+  if (int s = check_logits(logits, dtype, T, V, ld, labels, inv_temperature)) return s;
+  if (T == 0) return QLORA_OK;
+  if (logp == nullptr) return QLORA_ERR_NULL;
+  if (!aligned4(logp) || !aligned4(stats)) return QLORA_ERR_ALIGN;
+  const size_t tb = (size_t)T * 4;
+  const Region out[2] = {{logp, tb}, {stats, 2 * tb}};
+  const Region in[2] = {{logits, rows_bytes(dtype, T, V, ld)}, {labels, tb}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_logprob(logits, dtype, T, (int)V, ld, labels, inv_temperature, logp, stats,
+                                   reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_token_logprobs_backward(const float* dlogp, const void* logits, int32_t dtype, int64_t T, int64_t V,
+                                  int64_t ld, const int32_t* labels, float inv_temperature, const float* stats,
+                                  void* dlogits, int64_t ldd, void* stream) {
+  if (int s = check_logits(logits, dtype, T, V, ld, labels, inv_temperature)) return s;
+  if (T == 0) return QLORA_OK;
+  if (dlogp == nullptr || stats == nullptr || dlogits == nullptr) return QLORA_ERR_NULL;
+  if (!aligned4(dlogp) || !aligned4(stats)) return QLORA_ERR_ALIGN;
+  if (int s = check_dlogits(dlogits, ldd, logits, dtype, T, V, ld)) return s;
+  const size_t tb = (size_t)T * 4;
+  const Region out[1] = {{dlogits, rows_bytes(dtype, T, ldd, ldd)}};
+  const Region in[3] = {{dlogp, tb}, {labels, tb}, {stats, 2 * tb}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_logprob_grad(logits, dtype, T, (int)V, ld, labels, inv_temperature, stats, dlogp, dlogits,
+                                        ldd, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_preference_loss(const float* logp, const float* ref_logp, const int32_t* labels, int64_t T, int64_t V,
+                          const int32_t* cu_seqlens, int64_t P, int32_t kind, int32_t average, float beta,
+                          float label_smoothing, float margin, const float* weight, float* loss, float* reward,
+                          float* dlogp, void* stream) {
+  if (kind != QLORA_PREF_SIGMOID && kind != QLORA_PREF_HINGE && kind != QLORA_PREF_SQUARED) return QLORA_ERR_TYPE;
+  if (T < 0 || T >= kMaxElems || V < 1 || V >= kMaxCols || P < 0 || P >= ((int64_t)1 << 20)) return QLORA_ERR_SHAPE;
+  if (!(beta > 0.0f) || !std::isfinite(beta) || !(label_smoothing >= 0.0f && label_smoothing <= 0.5f) ||
+      !std::isfinite(margin))
+    return QLORA_ERR_ALPHA;
+  if (P == 0) return QLORA_OK;
+  if (cu_seqlens == nullptr || loss == nullptr) return QLORA_ERR_NULL;
+  if (T > 0 && (logp == nullptr || labels == nullptr)) return QLORA_ERR_NULL;
+  if (!aligned4(logp) || !aligned4(ref_logp) || !aligned4(labels) || !aligned4(cu_seqlens) || !aligned4(weight) ||
+      !aligned4(loss) || !aligned4(reward) || !aligned4(dlogp))
+    return QLORA_ERR_ALIGN;
+  const size_t tb = (size_t)T * 4, pb = (size_t)P * 4;
+  const Region out[3] = {{loss, pb}, {reward, 2 * pb}, {dlogp, tb}};
+  const Region in[5] = {{logp, tb}, {ref_logp, tb}, {labels, tb}, {cu_seqlens, 2 * pb + 4}, {weight, pb}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_preference(logp, ref_logp, labels, T, (int)V, cu_seqlens, P, kind, average, beta,
+                                      label_smoothing, margin, weight, loss, reward, dlogp,
+                                      reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* labels,
+                      float inv_temperature, const float* advantages, const float* old_logp, const float* ref_logp,
+                      const float* weight, float clip_low, float clip_high, float kl_coef, float* loss, float* kl,
+                      float* logp, void* dlogits, int64_t ldd, void* stream) {
+  if (int s = check_logits(logits, dtype, T, V, ld, labels, inv_temperature)) return s;
+  if (!(clip_low >= 0.0f && clip_low <= 1.0f) || !(clip_high >= 0.0f) || !std::isfinite(clip_high) ||
+      !(kl_coef >= 0.0f) || !std::isfinite(kl_coef))
+    return QLORA_ERR_ALPHA;
+  if (T == 0) return QLORA_OK;
+  if (advantages == nullptr || loss == nullptr || logp == nullptr) return QLORA_ERR_NULL;
+  if (!aligned4(advantages) || !aligned4(old_logp) || !aligned4(ref_logp) || !aligned4(weight) || !aligned4(loss) ||
+      !aligned4(kl) || !aligned4(logp))
+    return QLORA_ERR_ALIGN;
+  const size_t tb = (size_t)T * 4, zb = rows_bytes(dtype, T, V, ld);
+  size_t db = 0;
+  if (dlogits != nullptr) {
+    if (int s = check_dlogits(dlogits, ldd, logits, dtype, T, V, ld)) return s;
+    db = rows_bytes(dtype, T, ldd, ldd);
+  }
+  const Region out[3] = {{loss, tb}, {kl, tb}, {logp, tb}};
+  const Region in[7] = {{logits, zb}, {labels, tb}, {advantages, tb}, {old_logp, tb}, {ref_logp, tb}, {weight, tb},
+                        {dlogits, db}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  for (int i = 1; i < 6; ++i)
+    if (overlaps(dlogits, db, in[i].p, in[i].n)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_policy(logits, dtype, T, (int)V, ld, labels, inv_temperature, advantages, old_logp,
+                                  ref_logp, weight, clip_low, clip_high, kl_coef, loss, kl, logp, dlogits, ldd,
+                                  reinterpret_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------- orthogonalised update ----
+
+static int check_muon_shape(int64_t nmat, int64_t rows, int64_t cols) {
+  if (nmat < 0 || nmat > 65535 || rows < 1 || cols < 1 || rows >= kMaxElems || cols >= kMaxElems)
+    return QLORA_ERR_SHAPE;
+  if ((rows < cols ? rows : cols) > kMaxRank) return QLORA_ERR_RANK;
+  if (rows * cols >= kMaxElems || nmat * (rows * cols) >= kMaxElems) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+size_t qlora_muon_workspace_bytes(int64_t nmat, int64_t rows, int64_t cols) {
+  if (nmat == 0 || check_muon_shape(nmat, rows, cols)) return 0;
+  return muon_ws_bytes(nmat, rows, cols);
+}
+
+int qlora_muon_step(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t nmat, int64_t rows, int64_t cols,
+                    float lr, float momentum, int32_t nesterov, float weight_decay, float scale, float eps,
+                    int32_t ns_steps, const float* coef, void* ws, size_t ws_bytes, void* stream) {
+  if (int s = check_muon_shape(nmat, rows, cols)) return s;
+  if (ns_steps < 1 || ns_steps > kMaxMuonSteps) return QLORA_ERR_SHAPE;
+  if (!(lr >= 0.0f) || !std::isfinite(lr) || !(momentum >= 0.0f && momentum < 1.0f) || !(weight_decay >= 0.0f) ||
+      !std::isfinite(weight_decay) || !std::isfinite(scale) || !(eps > 0.0f) || !std::isfinite(eps))
+    return QLORA_ERR_ALPHA;
+  MuonCoef co;
+  co.n = ns_steps;
+  const float usual[3] = {3.4445f, -4.7750f, 2.0315f};
+  for (int i = 0; i < kMaxMuonSteps; ++i)
+    for (int q = 0; q < 3; ++q) {
+      const float v = i >= ns_steps ? 0.0f : (coef != nullptr ? coef[3 * i + q] : usual[q]);
+      if (!std::isfinite(v)) return QLORA_ERR_ALPHA;
+      co.c[i][q] = v;
+    }
+  if (nmat == 0) return QLORA_OK;
+  if (P == nullptr || W == nullptr || G == nullptr || m == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(P) || !aligned16(W) || !aligned16(G) || !aligned16(m) || !aligned16(ws)) return QLORA_ERR_ALIGN;
+  const size_t need = muon_ws_bytes(nmat, rows, cols);
+  if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  const size_t n = (size_t)(nmat * rows * cols);
+  const Region out[4] = {{P, n * 2}, {W, n * 4}, {m, n * 4}, {ws, need}};
+  const Region in[1] = {{G, n * 2}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_muon(P, W, G, m, nmat, rows, cols, lr, momentum, nesterov, weight_decay, scale, eps, co,
+                                ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
 static int merge_common(const qlora_nf4_t* W0, const uint16_t* Win, int64_t d, int64_t k,

@@ -147,6 +147,39 @@ size_t dx_ws_bytes(int M, int d, int k);
 hipError_t launch_adam(float* W, const uint16_t* G, float* m, float* v, uint16_t* P, int64_t n, float lr,
                        float b1, float b2, float eps, float wd, int64_t step, hipStream_t st);
 
+// loss.hip: logits are T rows of V (stride ld elements), fp32 (f32 != 0) or
+// bf16; tau is the inverse temperature.  A token whose label lies outside
+// [0, V) does not count: log-probability 0 and no gradient.
+// stats (T x 2, optional): row maximum and log2 of the exponentials' sum.
+hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
+                          float* logp, float* stats, hipStream_t st);
+// dlogits = dlogp d logp / d logits: T whole rows of ldd elements (zeros
+// past column V); may be the logits themselves.
+hipError_t launch_logprob_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels,
+                               float tau, const float* stats, const float* dlogp, void* dlogits, int64_t ldd,
+                               hipStream_t st);
+// Clipped policy loss per token and, with dlogits, its gradient.
+hipError_t launch_policy(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
+                         const float* adv, const float* old_logp, const float* ref_logp, const float* weight,
+                         float clip_low, float clip_high, float kl_coef, float* loss, float* kl, float* logp,
+                         void* dlogits, int64_t ldd, hipStream_t st);
+// Preference loss of P pairs of sequences (offsets cu, 2P + 1 entries).
+hipError_t launch_preference(const float* logp, const float* ref_logp, const int32_t* labels, int64_t T, int V,
+                             const int32_t* cu, int64_t P, int kind, int average, float beta, float smoothing,
+                             float margin, const float* weight, float* loss, float* reward, float* dlogp,
+                             hipStream_t st);
+
+// muon.hip: momentum, orthogonalised update and weights of nmat matrices.
+constexpr int kMaxMuonSteps = 16;
+struct MuonCoef {
+  int n;
+  double c[kMaxMuonSteps][3];
+};
+size_t muon_ws_bytes(int64_t nmat, int64_t rows, int64_t cols);
+hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t nmat, int64_t rows, int64_t cols,
+                       float lr, float momentum, int nesterov, float wd, float scale, float eps, const MuonCoef& co,
+                       void* ws, hipStream_t st);
+
 // Tile height forced through the environment (QLORA_TILE=128 or 256) for
 // tests of each variant on small shapes; 0 = choose by shape.
 inline int tile_override() {

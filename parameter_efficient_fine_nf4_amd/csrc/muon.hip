@@ -29,7 +29,6 @@
 namespace qlora {
 
 constexpr int kMuThreads = 256;
-constexpr int kMuTile = 64;  // long positions per LDS tile
 
 struct MuShape {
   int64_t nmat, rows, cols;
@@ -44,174 +43,585 @@ static MuShape mu_shape(int64_t nmat, int64_t rows, int64_t cols) {
   return s;
 }
 
-__device__ __forceinline__ int64_t mu_at(const MuShape& s, int i, int64_t j) {
-  return s.tall ? j * s.S + i : i * s.L + j;
-}
-
 __device__ __forceinline__ float mu_momentum(float m, float g, float mu) { return __fadd_rn(__fmul_rn(mu, m), g); }
 __device__ __forceinline__ float mu_update(float m, float g, float mu, int nesterov) {
   return nesterov ? __fadd_rn(g, __fmul_rn(mu, m)) : m;
 }
 
-// Pass 1: m <- mu m + g, and one fp64 partial of u u^T per (matrix, split).
-__global__ __launch_bounds__(kMuThreads) void k_muon_gram(const uint16_t* __restrict__ G, float* __restrict__ M,
-                                                          MuShape s, float mu, int nesterov, int splits,
-                                                          double* __restrict__ part) {
-  __shared__ float tile[kMuTile][65];
+typedef __attribute__((ext_vector_type(4))) double f64x4;
+
+__device__ __forceinline__ f64x4 mfma_f64(double a, double b, f64x4 c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// N consecutive values at element alignment (rows of odd lengths start
+// anywhere).  VEC: one vector access; otherwise one by one, where only the
+// first n exist (a load repeats the last of them, so that no load depends on a
+// branch; n >= 1 at an address the caller has clamped into the matrix).
+template <int N>
+struct Vec {
+  typedef float __attribute__((ext_vector_type(N), aligned(4))) F;
+  typedef uint16_t __attribute__((ext_vector_type(N), aligned(2))) H;
+};
+template <>
+struct Vec<1> {
+  typedef float F;
+  typedef uint16_t H;
+};
+// N bf16 values, two to a register.
+template <int N>
+struct Halves {
+  uint32_t w[(N + 1) / 2];
+  __device__ __forceinline__ float f32(int i) const { return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
+};
+__device__ __forceinline__ int clamp_at(int i, int n) { return i < n ? i : (n > 1 ? n - 1 : 0); }
+
+template <bool VEC, int N>
+__device__ __forceinline__ void load_f(const float* p, int n, float (&v)[N]) {
+  if constexpr (VEC) {
+    const typename Vec<N>::F x = *reinterpret_cast<const typename Vec<N>::F*>(p);
+    __builtin_memcpy(v, &x, N * 4);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[clamp_at(i, n)];
+  }
+}
+template <bool VEC, int N>
+__device__ __forceinline__ void load_h(const uint16_t* p, int n, Halves<N>& v) {
+  if constexpr (VEC) {
+    const typename Vec<N>::H x = *reinterpret_cast<const typename Vec<N>::H*>(p);
+    v.w[(N - 1) / 2] = 0;
+    __builtin_memcpy(v.w, &x, N * 2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < (N + 1) / 2; ++i)
+      v.w[i] = (uint32_t)p[clamp_at(2 * i, n)] | (uint32_t)p[clamp_at(2 * i + 1, n)] << 16;
+  }
+}
+template <bool VEC, int N>
+__device__ __forceinline__ void store_f(float* p, int n, const float (&v)[N]) {
+  if constexpr (VEC) {
+    if (n > 0) {
+      typename Vec<N>::F x;
+      __builtin_memcpy(&x, v, N * 4);
+      *reinterpret_cast<typename Vec<N>::F*>(p) = x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+template <bool VEC, int N>
+__device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[N]) {
+  uint32_t h[(N + 1) / 2];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) h[i / 2] = pack_bf16x2(v[i], i + 1 < N ? v[i + 1 < N ? i + 1 : i] : 0.0f);
+  if constexpr (VEC) {
+    if (n > 0) {
+      typename Vec<N>::H x;
+      __builtin_memcpy(&x, h, N * 2);
+      *reinterpret_cast<typename Vec<N>::H*>(p) = x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
+  }
+}
+__device__ __forceinline__ int room(int64_t end, int64_t at) {  // elements from `at` on, capped to an int
+  const int64_t n = end - at;
+  return n > 64 ? 64 : (n < 0 ? 0 : (int)n);
+}
+__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// The Gram matrix and everything made of it are symmetric: of the NT x NT
+// tiles of 16 x 16 only those (t, t2) with t <= t2 are formed, numbered u.
+constexpr int mu_tiles(int nt) { return nt * (nt + 1) / 2; }
+
+// -------------------------------------------------------------- pass 1 ----
+//
+// m <- mu m + g, and one fp64 partial of u u^T per (matrix, split), as the
+// tiles' MFMA accumulators (16 x 16 x 4: operand lane l holds index l % 16 of
+// position l / 16; the same registers are both operands).  A wave takes 32
+// long positions at a time, 8 per lane; the order of the positions inside an
+// MFMA does not matter to the sum, so each lane loads consecutive values:
+//
+//   not tall: 8 positions of row 16 t + l % 16 (a row's 32 are a 128-byte
+//             line of m), tile index i of t is row 16 t + i;
+//   tall:     NT consecutive short indexes of 8 long positions 4 apart, tile
+//             index i of t is NT i + t (k_muon_poly undoes the order).
+template <int NT, bool TALL>
+struct GramLoad {
+  static constexpr int A = TALL ? 8 : NT, B = TALL ? NT : 8;  // A vectors of B consecutive values
+  float m[A][B];
+  Halves<B> g[A];
+
+  // where vector a of a lane starts (clamped into the matrix), and how many
+  // of its values exist.  VEC: all positions of the step exist and, tall, S
+  // is a multiple of NT, so a vector exists whole or not at all.
+  template <bool VEC>
+  static __device__ __forceinline__ int64_t at(const MuShape& s, int64_t j0, int lane, int a) {
+    if (TALL) {
+      const int i = NT * (lane & 15), last = VEC ? s.S - NT : s.S - 1;
+      const int64_t j = j0 + 4 * a;
+      const int64_t row = VEC ? j * s.S + lane / 16 * s.S : min64(j + lane / 16, s.L - 1) * s.S;
+      return row + (i < last ? i : last);
+    }
+    const int i = 16 * a + (lane & 15), j = 8 * (lane / 16);
+    if (a < NT - 1 && VEC) return (16 * a * s.L + j0) + (lane & 15) * s.L + j;
+    return (i < s.S ? i : s.S - 1) * s.L + (VEC ? j0 + j : min64(j0 + j, s.L - 1));
+  }
+  template <bool VEC>
+  static __device__ __forceinline__ int count(const MuShape& s, int64_t j0, int lane, int a) {
+    if (TALL) {
+      const int n = s.S - NT * (lane & 15);
+      return (VEC || j0 + lane / 16 + 4 * a < s.L) && n > 0 ? n : 0;
+    }
+    if (16 * a + (lane & 15) >= s.S) return 0;
+    return VEC ? 8 : room(s.L, j0 + 8 * (lane / 16));
+  }
+  template <bool VEC>
+  __device__ __forceinline__ void load(const uint16_t* G, const float* M, const MuShape& s, int64_t j0, int lane) {
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+      const int n = count<VEC>(s, j0, lane, a);
+      load_f<VEC, B>(M + at<VEC>(s, j0, lane, a), n, m[a]);
+      load_h<VEC, B>(G + at<VEC>(s, j0, lane, a), n, g[a]);
+    }
+  }
+  // m <- mu m + g; the tiles' sums take u.
+  template <bool VEC>
+  __device__ __forceinline__ void use(float* M, const MuShape& s, int64_t j0, int lane, float mu, int nesterov,
+                                      f64x4 (&acc)[mu_tiles(NT)]) {
+    float v[A][B];
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+      const int n = count<VEC>(s, j0, lane, a);
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        m[a][b] = mu_momentum(m[a][b], g[a].f32(b), mu);
+        v[a][b] = (VEC ? n > 0 : b < n) ? mu_update(m[a][b], g[a].f32(b), mu, nesterov) : 0.0f;
+      }
+      store_f<VEC, B>(M + at<VEC>(s, j0, lane, a), n, m[a]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      double d[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) d[t] = (double)(TALL ? v[TALL ? c : 0][TALL ? t : 0] : v[TALL ? 0 : t][TALL ? 0 : c]);
+#pragma unroll
+      for (int t2 = 0; t2 < NT; ++t2)
+#pragma unroll
+        for (int t = 0; t <= t2; ++t) acc[mu_tiles(t2) + t] = mfma_f64(d[t], d[t2], acc[mu_tiles(t2) + t]);
+    }
+  }
+};
+
+template <int NT, bool TALL>
+__global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __restrict__ Gs, float* __restrict__ Ms,
+                                                             MuShape s, float mu, int nesterov, int splits,
+                                                             double* __restrict__ part) {
+  constexpr int U = mu_tiles(NT);
+  __shared__ double red[4][U * 256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = blockIdx.x / splits;
-  const int split = blockIdx.x % splits;
-  const int64_t base = mat * s.rows * s.cols;
-  const int S = s.S, SS = S * S;
-  double acc[16];
+  const uint16_t* G = Gs + mat * s.rows * s.cols;
+  float* M = Ms + mat * s.rows * s.cols;
+  const int64_t stride = (int64_t)splits * 128;
+  f64x4 acc[U];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.0;
-  for (int64_t j0 = (int64_t)split * kMuTile; j0 < s.L; j0 += (int64_t)splits * kMuTile) {
-    for (int e = threadIdx.x; e < kMuTile * S; e += kMuThreads) {
-      const int jj = s.tall ? e / S : e % kMuTile, i = s.tall ? e % S : e / kMuTile;
-      float u = 0.0f;
-      if (j0 + jj < s.L) {
-        const int64_t at = base + mu_at(s, i, j0 + jj);
-        const float g = bf16_to_f32(G[at]);
-        const float m = mu_momentum(M[at], g, mu);
-        M[at] = m;
-        u = mu_update(m, g, mu, nesterov);
-      }
-      tile[jj][i] = u;
+  for (int u = 0; u < U; ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
+  int64_t j0 = (int64_t)(blockIdx.x % splits) * 128 + wave * 32;
+  // whole steps, the next one's loads in flight over the sums of this one;
+  // then the long axis's end (every step, of a tall factor with odd S)
+  if (!TALL || s.S % NT == 0) {
+    GramLoad<NT, TALL> x, next;
+    if (j0 + 32 <= s.L) x.template load<true>(G, M, s, j0, lane);
+    for (; j0 + 32 <= s.L; j0 += stride) {
+      if (j0 + stride + 32 <= s.L) next.template load<true>(G, M, s, j0 + stride, lane);
+      x.template use<true>(M, s, j0, lane, mu, nesterov, acc);
+      x = next;
     }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int at = e * kMuThreads + threadIdx.x;
-      if (at < SS) {
-        const int i = at / S, k = at % S;
-        for (int jj = 0; jj < kMuTile; ++jj) acc[e] += (double)tile[jj][i] * (double)tile[jj][k];
-      }
-    }
-    __syncthreads();
+  }
+#pragma unroll 1
+  for (; j0 < s.L; j0 += stride) {
+    GramLoad<NT, TALL> x;
+    x.template load<false>(G, M, s, j0, lane);
+    x.template use<false>(M, s, j0, lane, mu, nesterov, acc);
   }
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int at = e * kMuThreads + threadIdx.x;
-    if (at < SS) part[(size_t)blockIdx.x * SS + at] = acc[e];
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[wave][u * 256 + q * 64 + lane] = acc[u][q];
+  __syncthreads();
+  double* out = part + (size_t)blockIdx.x * U * 256;
+  for (int e = threadIdx.x; e < U * 256; e += kMuThreads) out[e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+}
+
+// ---------------------------------------------------- S x S iteration ----
+//
+// One matrix per work-group, on fp64 MFMA tiles with the four matrices G, P,
+// Q, R in LDS, padded with zeros to N = 16 NT.  All of them are polynomials in
+// G_0, so they are symmetric and commute: an operand's fragment (lane l: index
+// l % 16, k = l / 16) is read as row k, sixteen consecutive doubles, for
+// either side, and a tile is written both as it is and transposed.  Element
+// (k, i) lies at column i ^ (k % 16), and for even NT in the other 16-column
+// half for odd k (N = 16 and 48 put odd rows into the other half of the LDS
+// banks by themselves): then the two rows that a half-wave reads or writes,
+// and the two columns it writes transposed, meet no bank twice.
+//
+// D of the instruction: lane l, register q holds row l / 16 + 4 q, column
+// l % 16.
+//
+// Per step: P from G G; then P Q and P G, which read the same matrices, in one
+// phase; then (P G) P.  The last step needs no G.
+template <int NT>
+struct PolyLds {
+  static constexpr int N = 16 * NT;
+  static __device__ __forceinline__ int at(int k, int i) {
+    return k * N + (i ^ (NT % 2 == 0 ? (k & 15) | ((k & 1) << 4) : k & 15));
+  }
+};
+
+// The tiles are dealt to the four waves in turn.  A wave whose turn is past
+// the last tile repeats tile (0, 0) and does not write it, so that the
+// products have no branch in them.
+template <int NT>
+constexpr int kPolyTiles = (mu_tiles(NT) + 3) / 4;
+
+struct PolyTile {
+  int u, t, t2;
+  bool own;
+};
+template <int NT>
+__device__ __forceinline__ PolyTile poly_tile(int e) {
+  int u = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) + 4 * e;
+  const bool own = u < mu_tiles(NT);
+  u = own ? u : 0;
+  const int t2 = (u >= 1) + (u >= 3) + (u >= 6);
+  return PolyTile{u, u - t2 * (t2 + 1) / 2, t2, own};
+}
+
+template <int NT>
+__device__ __forceinline__ void poly_mul(const double* x, const double* y, f64x4 (&acc)[kPolyTiles<NT>]) {
+  const int lane = threadIdx.x & 63;
+  int xo[kPolyTiles<NT>], yo[kPolyTiles<NT>];  // row lane / 16; row + 4 k differs in bits 2 and 3 of the column
+#pragma unroll
+  for (int e = 0; e < kPolyTiles<NT>; ++e) {
+    const PolyTile p = poly_tile<NT>(e);
+    xo[e] = PolyLds<NT>::at(lane / 16, 16 * p.t + (lane & 15));
+    yo[e] = PolyLds<NT>::at(lane / 16, 16 * p.t2 + (lane & 15));
+    acc[e] = f64x4{0.0, 0.0, 0.0, 0.0};
+  }
+#pragma unroll
+  for (int k = 0; k < 4 * NT; ++k)
+#pragma unroll
+    for (int e = 0; e < kPolyTiles<NT>; ++e)
+      acc[e] = mfma_f64(x[(xo[e] ^ (4 * (k & 3))) + k * 64 * NT], y[(yo[e] ^ (4 * (k & 3))) + k * 64 * NT], acc[e]);
+}
+
+// f(e, q, i, k) for every element (i, k) of the wave's tiles.
+template <int NT, typename F>
+__device__ __forceinline__ void poly_each(F f) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int e = 0; e < kPolyTiles<NT>; ++e) {
+    const PolyTile p = poly_tile<NT>(e);
+    if (p.own) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f(e, q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15));
+    }
   }
 }
 
-// The S x S iteration of one matrix: Q / (|u| + eps), rounded to fp32.
-__global__ __launch_bounds__(kMuThreads) void k_muon_poly(const double* __restrict__ part, int splits, int S,
-                                                          MuonCoef co, float eps, float* __restrict__ Qout) {
-  __shared__ double G[64 * 65], P[64 * 65], Q[64 * 65], R[64 * 65];
-  const int SS = S * S, ld = 65;
-  const double* src = part + (size_t)blockIdx.x * splits * SS;
-  for (int at = threadIdx.x; at < SS; at += kMuThreads) {
-    double sum = 0.0;
-    for (int k = 0; k < splits; ++k) sum += src[(size_t)k * SS + at];
-    G[(at / S) * ld + at % S] = sum;
-    Q[(at / S) * ld + at % S] = at / S == at % S ? 1.0 : 0.0;
+template <int NT>
+__device__ __forceinline__ void poly_put(double* m, int i, int k, double v) {
+  m[PolyLds<NT>::at(i, k)] = v;
+  if ((i ^ k) >> 4) m[PolyLds<NT>::at(k, i)] = v;
+}
+
+// part -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
+template <int NT, bool TALL>
+__global__ __launch_bounds__(kMuThreads) void k_muon_poly(const double* __restrict__ part, int splits, MuonCoef co,
+                                                          float eps, float* __restrict__ Qout) {
+  using At = PolyLds<NT>;
+  constexpr int N = At::N, U = mu_tiles(NT);
+  __shared__ double G[N * N], P[N * N], Q[N * N], R[N * N];
+  const int lane = threadIdx.x & 63;
+  const double* src = part + (size_t)blockIdx.x * splits * U * 256;
+#pragma unroll
+  for (int e = 0; e < kPolyTiles<NT>; ++e) {
+    const PolyTile p = poly_tile<NT>(e);
+    if (p.own) {
+      double sum[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+      for (int k = 0; k < splits; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[q] += src[(size_t)k * U * 256 + p.u * 256 + q * 64 + lane];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) poly_put<NT>(G, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
+    }
   }
   __syncthreads();
   double trace = 0.0;
-  for (int i = 0; i < S; ++i) trace += G[i * ld + i];
+  for (int i = 0; i < N; ++i) trace += G[At::at(i, i)];
   const double inv = 1.0 / (sqrt(trace) + (double)eps);
   __syncthreads();
-  for (int at = threadIdx.x; at < SS; at += kMuThreads) G[(at / S) * ld + at % S] *= inv * inv;
+  for (int e = threadIdx.x; e < N * N; e += kMuThreads) G[e] *= inv * inv;
   __syncthreads();
-  // out = x y (all of them commute and are symmetric)
-  auto mul = [&](const double* x, const double* y, double* out) {
-    for (int at = threadIdx.x; at < SS; at += kMuThreads) {
-      const int i = at / S, k = at % S;
-      double sum = 0.0;
-      for (int q = 0; q < S; ++q) sum = fma(x[i * ld + q], y[q * ld + k], sum);
-      out[i * ld + k] = sum;
-    }
-    __syncthreads();
-  };
+  f64x4 a0[kPolyTiles<NT>], a1[kPolyTiles<NT>];
+#pragma unroll 1
   for (int n = 0; n < co.n; ++n) {
-    mul(G, G, P);
-    for (int at = threadIdx.x; at < SS; at += kMuThreads) {
-      const int i = at / S, k = at % S;
-      P[i * ld + k] = (i == k ? co.c[n][0] : 0.0) + co.c[n][1] * G[i * ld + k] + co.c[n][2] * P[i * ld + k];
+    const double ca = co.c[n][0], cb = co.c[n][1], cc = co.c[n][2];
+    const bool last = n + 1 == co.n;
+    poly_mul<NT>(G, G, a0);
+    poly_each<NT>([&](int e, int q, int i, int k) {
+      const double p = fma(cc, a0[e][q], fma(cb, G[At::at(i, k)], i == k ? ca : 0.0));
+      poly_put<NT>(P, i, k, p);
+      if (n == 0) poly_put<NT>(Q, i, k, p);
+    });
+    __syncthreads();
+    if (n > 0) poly_mul<NT>(P, Q, a0);
+    if (!last) {
+      poly_mul<NT>(P, G, a1);
+      poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(R, i, k, a1[e][q]); });
     }
     __syncthreads();
-    mul(P, Q, R);
-    for (int at = threadIdx.x; at < SS; at += kMuThreads) Q[(at / S) * ld + at % S] = R[(at / S) * ld + at % S];
-    __syncthreads();
-    if (n + 1 < co.n) {
-      mul(P, G, R);
-      mul(R, P, G);
+    if (n > 0) poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(Q, i, k, a0[e][q]); });
+    if (!last) {
+      poly_mul<NT>(R, P, a1);
+      poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(G, i, k, a1[e][q]); });
     }
+    __syncthreads();
   }
-  for (int at = threadIdx.x; at < SS; at += kMuThreads)
-    Qout[(size_t)blockIdx.x * SS + at] = (float)(Q[(at / S) * ld + at % S] * inv);
+  // tile index (t, i) -> the short index it stands for
+  auto of = [](int e) { return TALL ? (e % NT) * 16 + e / NT : e; };
+  float* out = Qout + (size_t)blockIdx.x * N * N;
+  for (int e = threadIdx.x; e < N * N; e += kMuThreads) out[e] = (float)(Q[At::at(of(e / N), of(e % N))] * inv);
 }
 
-// Pass 2: X = Q u, the weights and their bf16 copy.
-__global__ __launch_bounds__(kMuThreads) void k_muon_apply(const uint16_t* __restrict__ G,
-                                                           const float* __restrict__ M, MuShape s, float mu,
-                                                           int nesterov, int splits, const float* __restrict__ Qin,
-                                                           float decay, float step, float* __restrict__ W,
-                                                           uint16_t* __restrict__ P) {
-  __shared__ float tile[kMuTile][65];
-  __shared__ float Q[64 * 65];
-  const int64_t mat = blockIdx.x / splits;
-  const int split = blockIdx.x % splits;
-  const int64_t base = mat * s.rows * s.cols;
-  const int S = s.S;
-  for (int at = threadIdx.x; at < S * S; at += kMuThreads) Q[(at / S) * 65 + at % S] = Qin[(size_t)mat * S * S + at];
-  for (int64_t j0 = (int64_t)split * kMuTile; j0 < s.L; j0 += (int64_t)splits * kMuTile) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kMuTile * S; e += kMuThreads) {
-      const int jj = s.tall ? e / S : e % kMuTile, i = s.tall ? e % S : e / kMuTile;
-      float u = 0.0f;
-      if (j0 + jj < s.L) {
-        const int64_t at = base + mu_at(s, i, j0 + jj);
-        u = mu_update(M[at], bf16_to_f32(G[at]), mu, nesterov);
-      }
-      tile[jj][i] = u;
+// -------------------------------------------------------------- pass 2 ----
+//
+// X = Q u on fp32 MFMA tiles (16 x 16 x 4: A[i][k] lane l: i = l % 16, k = l /
+// 16; D lane l, register q: row 4 (l / 16) + q, column l % 16), the weights
+// and their bf16 copy.  Q is the A operand, held in registers over all of a
+// wave's steps; rows of D are short indexes, columns long positions.  As in
+// pass 1 lanes load consecutive values and the order inside an MFMA follows:
+//
+//   not tall: lane l has C positions C (l % 16) + c of row k = 4 s + l / 16,
+//             and D gives it the same C positions of rows 16 t + 4 (l / 16) + q;
+//   tall:     lane l has short indexes 16 s + 4 (l / 16) + c of position l % 16,
+//             so that k of MFMA (s, c) is 16 s + 4 (l / 16) + c, and D gives it
+//             short indexes 16 t + 4 (l / 16) + q of that position.
+template <int NT, bool TALL>
+struct ApplyShape {
+  // positions per lane (not tall) or 16-position groups per step (tall): as
+  // much in flight as the registers hold beside NT^2 * 4 of Q
+  static constexpr int C = TALL ? 4 : (NT >= 3 ? 2 : 4);
+  static constexpr int kGroups = TALL ? (NT == 1 ? 4 : NT == 2 ? 2 : 1) : 1;
+  static constexpr int kStep = TALL ? 16 * kGroups : 16 * C;
+};
+
+struct ApplyArgs {
+  const uint16_t* G;
+  const float* M;
+  float* W;
+  uint16_t* P;
+  float mu, decay, step;
+  int nesterov;
+};
+
+__device__ __forceinline__ float mu_weight(const ApplyArgs& a, float w, float x) {
+  return __fsub_rn(__fmul_rn(w, a.decay), __fmul_rn(a.step, x));
+}
+
+// VEC: all positions of the step exist and, tall, S is a multiple of 4.
+// Loads of rows or short indexes past S are clamped into the matrix: as u they
+// meet the zeros of Q, as weights they are not stored.
+template <int NT, bool VEC>
+__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int64_t j0, int lane,
+                                           const float (&qf)[NT][4 * NT]) {
+  constexpr int K = ApplyShape<NT, true>::kGroups;
+  float m[K][NT][4], w[K][NT][4];
+  Halves<4> g[K][NT];
+  auto at = [&](int a, int t) {
+    const int i = 16 * t + 4 * (lane / 16), last = VEC ? s.S - 4 : s.S - 1;
+    if (VEC) return (j0 + 16 * a) * s.S + (lane & 15) * s.S + (t < NT - 1 ? i : (i < last ? i : last));
+    return min64(j0 + 16 * a + (lane & 15), s.L - 1) * s.S + (i < last ? i : last);
+  };
+  auto count = [&](int a, int t) {
+    const int n = s.S - 16 * t - 4 * (lane / 16);
+    return VEC || j0 + 16 * a + (lane & 15) < s.L ? n : 0;
+  };
+#pragma unroll
+  for (int a = 0; a < K; ++a)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      load_f<VEC, 4>(p.M + at(a, t), count(a, t), m[a][t]);
+      load_h<VEC, 4>(p.G + at(a, t), count(a, t), g[a][t]);
+      load_f<VEC, 4>(p.W + at(a, t), count(a, t), w[a][t]);
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < kMuTile * S; e += kMuThreads) {
-      const int jj = s.tall ? e / S : e % kMuTile, i = s.tall ? e % S : e / kMuTile;
-      if (j0 + jj >= s.L) continue;
-      float x = 0.0f;
-      for (int k = 0; k < S; ++k) x = fmaf(Q[i * 65 + k], tile[jj][k], x);
-      const int64_t at = base + mu_at(s, i, j0 + jj);
-      const float w = __fsub_rn(__fmul_rn(W[at], decay), __fmul_rn(step, x));
-      W[at] = w;
-      P[at] = (uint16_t)pack_bf16x2(w, 0.0f);
+#pragma unroll
+  for (int a = 0; a < K; ++a) {
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < 4 * NT; ++k) {
+      const float u = mu_update(m[a][k / 4][k % 4], g[a][k / 4].f32(k % 4), p.mu, p.nesterov);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t] = mfma_f32(qf[t][k], u, acc[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[t][q]);
+      store_f<VEC, 4>(p.W + at(a, t), count(a, t), w[a][t]);
+      store_bf16<VEC, 4>(p.P + at(a, t), count(a, t), w[a][t]);
     }
   }
 }
 
-// Work-groups per matrix: about four per CU over the stack, each with at
-// least one tile.
-static int mu_splits(const MuShape& s) {
-  const int64_t tiles = (s.L + kMuTile - 1) / kMuTile;
-  int64_t n = (1024 + s.nmat - 1) / s.nmat;
-  if (n > tiles) n = tiles;
+template <int NT, bool VEC>
+__device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s, int64_t j0, int lane,
+                                           const float (&qf)[NT][4 * NT]) {
+  constexpr int C = ApplyShape<NT, false>::C;
+  const int64_t j = VEC ? j0 + C * (lane & 15) : min64(j0 + C * (lane & 15), s.L - 1);
+  const int nj = VEC ? C : room(s.L, j0 + C * (lane & 15));
+  float m[4 * NT][C], w[NT][4][C];
+  Halves<C> g[4 * NT];
+  // rows that exist are a uniform offset plus the lane's; only the last tile
+  // of 16 can go past S
+  auto at = [&](int first, int of_lane) {
+    if (first < 16 * (NT - 1)) return first * s.L + (of_lane * s.L + j);
+    const int i = first + of_lane;
+    return (i < s.S ? i : s.S - 1) * s.L + j;
+  };
+#pragma unroll
+  for (int k = 0; k < 4 * NT; ++k) {
+    load_f<VEC, C>(p.M + at(4 * k, lane / 16), nj, m[k]);
+    load_h<VEC, C>(p.G + at(4 * k, lane / 16), nj, g[k]);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load_f<VEC, C>(p.W + at(16 * t + q, 4 * (lane / 16)), nj, w[t][q]);
+  f32x4 acc[NT][C];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 4 * NT; ++k)
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float u = mu_update(m[k][c], g[k].f32(c), p.mu, p.nesterov);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][c] = mfma_f32(qf[t][k], u, acc[t][c]);
+    }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = 16 * t + 4 * (lane / 16) + q < s.S ? nj : 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) w[t][q][c] = mu_weight(p, w[t][q][c], acc[t][c][q]);
+      store_f<VEC, C>(p.W + at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+      store_bf16<VEC, C>(p.P + at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+    }
+}
+
+template <int NT, bool TALL>
+__global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs p, MuShape s, int splits,
+                                                              const float* __restrict__ Qin) {
+  constexpr int N = 16 * NT, kStep = ApplyShape<NT, TALL>::kStep;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t mat = blockIdx.x / splits, base = mat * s.rows * s.cols;
+  p.G += base;
+  p.M += base;
+  p.W += base;
+  p.P += base;
+  const float* Q = Qin + (size_t)mat * N * N;
+  float qf[NT][4 * NT];  // MFMA step 4 s + c (tall) or s
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < 4 * NT; ++k)
+      qf[t][k] = Q[(16 * t + (lane & 15)) * N + (TALL ? 16 * (k / 4) + 4 * (lane / 16) + k % 4 : 4 * k + lane / 16)];
+  const int64_t stride = (int64_t)splits * 4 * kStep;
+  int64_t j0 = ((int64_t)(blockIdx.x % splits) * 4 + wave) * kStep;
+  if (!TALL || s.S % 4 == 0) {
+#pragma unroll 1
+    for (; j0 + kStep <= s.L; j0 += stride) {
+      if constexpr (TALL)
+        apply_tall<NT, true>(p, s, j0, lane, qf);
+      else
+        apply_wide<NT, true>(p, s, j0, lane, qf);
+    }
+  }
+#pragma unroll 1
+  for (; j0 < s.L; j0 += stride) {
+    if constexpr (TALL)
+      apply_tall<NT, false>(p, s, j0, lane, qf);
+    else
+      apply_wide<NT, false>(p, s, j0, lane, qf);
+  }
+}
+
+// ----------------------------------------------------------- launchers ----
+
+static int mu_nt(const MuShape& s) { return (s.S + 15) / 16; }
+
+// Work-groups per matrix: about two per CU over the stack, each with at
+// least `per` long positions.
+static int mu_splits(const MuShape& s, int per) {
+  const int64_t most = (s.L + per - 1) / per;
+  int64_t n = (512 + s.nmat - 1) / s.nmat;
+  if (n > most) n = most;
   return (int)(n < 1 ? 1 : n);
 }
+static int gram_splits(const MuShape& s) { return mu_splits(s, 256); }
 
 static size_t mu_part_bytes(const MuShape& s) {
-  return (size_t)align_up((int64_t)((size_t)s.nmat * mu_splits(s) * s.S * s.S * sizeof(double)), 256);
+  return (size_t)s.nmat * gram_splits(s) * mu_tiles(mu_nt(s)) * 256 * sizeof(double);
 }
 
 size_t muon_ws_bytes(int64_t nmat, int64_t rows, int64_t cols) {
   const MuShape s = mu_shape(nmat, rows, cols);
-  return mu_part_bytes(s) + (size_t)nmat * s.S * s.S * sizeof(float);
+  const size_t n = 16 * (size_t)mu_nt(s);
+  return mu_part_bytes(s) + (size_t)nmat * n * n * sizeof(float);
+}
+
+template <int NT, bool TALL>
+static void muon_kernels(uint16_t* P, float* W, const uint16_t* G, float* m, const MuShape& s, float momentum,
+                         int nesterov, float decay, float step, float eps, const MuonCoef& co, double* part, float* Q,
+                         hipStream_t st) {
+  const int gs = gram_splits(s), as = mu_splits(s, 4 * ApplyShape<NT, TALL>::kStep);
+  const dim3 block(kMuThreads);
+  QLORA_LAUNCH("muon_gram", st, (k_muon_gram<NT, TALL>), dim3((unsigned)(s.nmat * gs)), block, 0, st, G, m, s,
+               momentum, nesterov, gs, part);
+  QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), block, 0, st, part, gs, co, eps, Q);
+  QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL>), dim3((unsigned)(s.nmat * as)), block, 0, st,
+               ApplyArgs{G, m, W, P, momentum, decay, step, nesterov}, s, as, Q);
 }
 
 hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t nmat, int64_t rows, int64_t cols,
                        float lr, float momentum, int nesterov, float wd, float scale, float eps, const MuonCoef& co,
                        void* ws, hipStream_t st) {
   const MuShape s = mu_shape(nmat, rows, cols);
-  const int splits = mu_splits(s);
   double* part = reinterpret_cast<double*>(ws);
   float* Q = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + mu_part_bytes(s));
-  const dim3 grid((unsigned)(nmat * splits)), block(kMuThreads);
-  QLORA_LAUNCH("muon_gram", st, k_muon_gram, grid, block, 0, st, G, m, s, momentum, nesterov, splits, part);
-  QLORA_LAUNCH("muon_poly", st, k_muon_poly, dim3((unsigned)nmat), block, 0, st, part, splits, s.S, co, eps, Q);
-  QLORA_LAUNCH("muon_apply", st, k_muon_apply, grid, block, 0, st, G, m, s, momentum, nesterov, splits, Q,
-               (float)(1.0 - (double)lr * wd), (float)((double)lr * scale), W, P);
+  const float decay = (float)(1.0 - (double)lr * wd), step = (float)((double)lr * scale);
+  using Fn = void (*)(uint16_t*, float*, const uint16_t*, float*, const MuShape&, float, int, float, float, float,
+                      const MuonCoef&, double*, float*, hipStream_t);
+  static const Fn table[2][4] = {
+      {muon_kernels<1, false>, muon_kernels<2, false>, muon_kernels<3, false>, muon_kernels<4, false>},
+      {muon_kernels<1, true>, muon_kernels<2, true>, muon_kernels<3, true>, muon_kernels<4, true>}};
+  table[s.tall][mu_nt(s) - 1](P, W, G, m, s, momentum, nesterov, decay, step, eps, co, part, Q, st);
   return hipGetLastError();
 }
 

@@ -502,7 +502,8 @@ int qlora_policy_loss(const void *logits, int32_t dtype, int64_t T, int64_t V, i
  * that side is at most 64 (QLORA_ERR_RANK).  Non-finite gradients give
  * non-finite weights in their own matrix only.
  * 1 <= ns_steps <= 16, 0 <= nmat <= 65535 (nmat == 0 is a no-op), rows and
- * cols >= 1, fewer than 2^31 elements in all (QLORA_ERR_SHAPE); all pointers
+ * cols >= 1, fewer than 2^29 elements a matrix and 2^31 in all
+ * (QLORA_ERR_SHAPE); all pointers
  * 16-byte aligned and disjoint; momentum in [0, 1), lr and weight_decay >= 0,
  * eps > 0, all of them and scale and coef finite (QLORA_ERR_ALPHA otherwise).
  */

@@ -827,7 +827,7 @@ static int check_muon_shape(int64_t nmat, int64_t rows, int64_t cols) {
   if (nmat < 0 || nmat > 65535 || rows < 1 || cols < 1 || rows >= kMaxElems || cols >= kMaxElems)
     return QLORA_ERR_SHAPE;
   if ((rows < cols ? rows : cols) > kMaxRank) return QLORA_ERR_RANK;
-  if (rows * cols >= kMaxElems || nmat * (rows * cols) >= kMaxElems) return QLORA_ERR_SHAPE;
+  if (rows * cols >= ((int64_t)1 << 29) || nmat * (rows * cols) >= kMaxElems) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 

@@ -22,6 +22,7 @@
 // G as s^2, which fp32 loses below 3e-4 of the largest, while the iteration
 // amplifies it by a^n (485 for the usual five steps).
 #include <cmath>
+#include <type_traits>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -32,14 +33,13 @@ constexpr int kMuThreads = 256;
 
 struct MuShape {
   int64_t nmat, rows, cols;
-  int S, tall;   // short side; rows > cols
-  int64_t L;     // long side
+  int S, L, tall;  // short and long side; rows > cols
 };
 
 static MuShape mu_shape(int64_t nmat, int64_t rows, int64_t cols) {
-  MuShape s{nmat, rows, cols, 0, rows > cols, 0};
+  MuShape s{nmat, rows, cols, 0, 0, rows > cols};
   s.S = (int)(s.tall ? cols : rows);
-  s.L = s.tall ? rows : cols;
+  s.L = (int)(s.tall ? rows : cols);
   return s;
 }
 
@@ -79,44 +79,55 @@ struct Halves {
 };
 __device__ __forceinline__ int clamp_at(int i, int n) { return i < n ? i : (n > 1 ? n - 1 : 0); }
 
+// An access is a wave-uniform base (scalar registers) plus a lane's 32-bit
+// offset in elements: row and step go into the base, so that the many rows of
+// a step in flight take no vector registers for addresses.  A matrix has
+// fewer than 2^29 elements.
+template <typename T, typename E>
+__device__ __forceinline__ T& lane_at(E* base, uint32_t at) {
+  typedef typename std::conditional<std::is_const<E>::value, const char, char>::type B;
+  return *reinterpret_cast<T*>(reinterpret_cast<B*>(base) + at * (uint32_t)sizeof(E));
+}
+
 template <bool VEC, int N>
-__device__ __forceinline__ void load_f(const float* p, int n, float (&v)[N]) {
+__device__ __forceinline__ void load_f(const float* p, uint32_t at, int n, float (&v)[N]) {
   if constexpr (VEC) {
-    const typename Vec<N>::F x = *reinterpret_cast<const typename Vec<N>::F*>(p);
+    const typename Vec<N>::F x = lane_at<const typename Vec<N>::F>(p, at);
     __builtin_memcpy(v, &x, N * 4);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = p[clamp_at(i, n)];
+    for (int i = 0; i < N; ++i) v[i] = lane_at<const float>(p, at + clamp_at(i, n));
   }
 }
 template <bool VEC, int N>
-__device__ __forceinline__ void load_h(const uint16_t* p, int n, Halves<N>& v) {
+__device__ __forceinline__ void load_h(const uint16_t* p, uint32_t at, int n, Halves<N>& v) {
   if constexpr (VEC) {
-    const typename Vec<N>::H x = *reinterpret_cast<const typename Vec<N>::H*>(p);
+    const typename Vec<N>::H x = lane_at<const typename Vec<N>::H>(p, at);
     v.w[(N - 1) / 2] = 0;
     __builtin_memcpy(v.w, &x, N * 2);
   } else {
 #pragma unroll
     for (int i = 0; i < (N + 1) / 2; ++i)
-      v.w[i] = (uint32_t)p[clamp_at(2 * i, n)] | (uint32_t)p[clamp_at(2 * i + 1, n)] << 16;
+      v.w[i] = (uint32_t)lane_at<const uint16_t>(p, at + clamp_at(2 * i, n)) |
+               (uint32_t)lane_at<const uint16_t>(p, at + clamp_at(2 * i + 1, n)) << 16;
   }
 }
 template <bool VEC, int N>
-__device__ __forceinline__ void store_f(float* p, int n, const float (&v)[N]) {
+__device__ __forceinline__ void store_f(float* p, uint32_t at, int n, const float (&v)[N]) {
   if constexpr (VEC) {
     if (n > 0) {
       typename Vec<N>::F x;
       __builtin_memcpy(&x, v, N * 4);
-      *reinterpret_cast<typename Vec<N>::F*>(p) = x;
+      lane_at<typename Vec<N>::F>(p, at) = x;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = v[i];
+      if (i < n) lane_at<float>(p, at + i) = v[i];
   }
 }
 template <bool VEC, int N>
-__device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[N]) {
+__device__ __forceinline__ void store_bf16(uint16_t* p, uint32_t at, int n, const float (&v)[N]) {
   uint32_t h[(N + 1) / 2];
 #pragma unroll
   for (int i = 0; i < N; i += 2) h[i / 2] = pack_bf16x2(v[i], i + 1 < N ? v[i + 1 < N ? i + 1 : i] : 0.0f);
@@ -124,23 +135,39 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, int n, const float (&v)[
     if (n > 0) {
       typename Vec<N>::H x;
       __builtin_memcpy(&x, h, N * 2);
-      *reinterpret_cast<typename Vec<N>::H*>(p) = x;
+      lane_at<typename Vec<N>::H>(p, at) = x;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
+      if (i < n) lane_at<uint16_t>(p, at + i) = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
   }
 }
-__device__ __forceinline__ int room(int64_t end, int64_t at) {  // elements from `at` on, capped to an int
-  const int64_t n = end - at;
-  return n > 64 ? 64 : (n < 0 ? 0 : (int)n);
-}
-__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int room(int end, int at) { return at < end ? end - at : 0; }
 
 // The Gram matrix and everything made of it are symmetric: of the NT x NT
 // tiles of 16 x 16 only those (t, t2) with t <= t2 are formed, numbered u.
 constexpr int mu_tiles(int nt) { return nt * (nt + 1) / 2; }
+
+// The whole steps of one wave over a matrix's long axis: the waves of all its
+// work-groups take neighbouring steps in turn.  Each matrix starts at its own
+// place (and goes round): rows of a power of two of bytes would otherwise put
+// every work-group of a stack on the same memory channels at the same time.
+// What is left of the axis (all of it where no step is whole) comes after, in
+// steps from `rest` on.
+struct Steps {
+  int i, n, first, rest, stride, step;
+  __device__ __forceinline__ Steps(const MuShape& s, int64_t mat, int wave, int waves, int step_, bool vec)
+      : i(wave), n(vec ? s.L / step_ : 0), stride(waves), step(step_) {
+    first = (int)(mat * n / s.nmat);
+    // (past the axis for every wave but the one whose turn it is; L + step
+    // fits an int as a matrix has fewer than 2^29 elements)
+    rest = n * step < s.L ? (int)min((int64_t)s.L, ((int64_t)n + (i + stride - n % stride) % stride) * step) : s.L;
+  }
+  __device__ __forceinline__ bool valid() const { return i < n; }
+  __device__ __forceinline__ bool next_valid() const { return i + stride < n; }
+  __device__ __forceinline__ int j0(int at) const { return (first + at < n ? first + at : first + at - n) * step; }
+};
 
 // -------------------------------------------------------------- pass 1 ----
 //
@@ -160,23 +187,26 @@ struct GramLoad {
   float m[A][B];
   Halves<B> g[A];
 
-  // where vector a of a lane starts (clamped into the matrix), and how many
-  // of its values exist.  VEC: all positions of the step exist and, tall, S
-  // is a multiple of NT, so a vector exists whole or not at all.
+  // Vector a of a lane starts at base(a) + lane_at(a) (clamped into the
+  // matrix) and has count(a) values.  VEC: all positions of the step exist
+  // and, tall, S is a multiple of NT, so a vector exists whole or not at all.
   template <bool VEC>
-  static __device__ __forceinline__ int64_t at(const MuShape& s, int64_t j0, int lane, int a) {
-    if (TALL) {
-      const int i = NT * (lane & 15), last = VEC ? s.S - NT : s.S - 1;
-      const int64_t j = j0 + 4 * a;
-      const int64_t row = VEC ? j * s.S + lane / 16 * s.S : min64(j + lane / 16, s.L - 1) * s.S;
-      return row + (i < last ? i : last);
-    }
-    const int i = 16 * a + (lane & 15), j = 8 * (lane / 16);
-    if (a < NT - 1 && VEC) return (16 * a * s.L + j0) + (lane & 15) * s.L + j;
-    return (i < s.S ? i : s.S - 1) * s.L + (VEC ? j0 + j : min64(j0 + j, s.L - 1));
+  static __device__ __forceinline__ int base(const MuShape& s, int j0, int a) {
+    if (TALL) return VEC ? (j0 + 4 * a) * s.S : 0;
+    return VEC ? 16 * a * s.L + j0 : 0;
   }
   template <bool VEC>
-  static __device__ __forceinline__ int count(const MuShape& s, int64_t j0, int lane, int a) {
+  static __device__ __forceinline__ uint32_t lane_part(const MuShape& s, int j0, int lane, int a) {
+    if (TALL) {
+      const int i = NT * (lane & 15), last = VEC ? s.S - NT : s.S - 1, j = j0 + 4 * a + lane / 16;
+      return (VEC ? lane / 16 : (j < s.L ? j : s.L - 1)) * s.S + (i < last ? i : last);
+    }
+    const int i = 16 * a + (lane & 15), j = j0 + 8 * (lane / 16);
+    if (VEC) return ((a < NT - 1 || i < s.S ? i : s.S - 1) - 16 * a) * s.L + 8 * (lane / 16);
+    return (i < s.S ? i : s.S - 1) * s.L + (j < s.L ? j : s.L - 1);
+  }
+  template <bool VEC>
+  static __device__ __forceinline__ int count(const MuShape& s, int j0, int lane, int a) {
     if (TALL) {
       const int n = s.S - NT * (lane & 15);
       return (VEC || j0 + lane / 16 + 4 * a < s.L) && n > 0 ? n : 0;
@@ -185,17 +215,17 @@ struct GramLoad {
     return VEC ? 8 : room(s.L, j0 + 8 * (lane / 16));
   }
   template <bool VEC>
-  __device__ __forceinline__ void load(const uint16_t* G, const float* M, const MuShape& s, int64_t j0, int lane) {
+  __device__ __forceinline__ void load(const uint16_t* G, const float* M, const MuShape& s, int j0, int lane) {
 #pragma unroll
     for (int a = 0; a < A; ++a) {
-      const int n = count<VEC>(s, j0, lane, a);
-      load_f<VEC, B>(M + at<VEC>(s, j0, lane, a), n, m[a]);
-      load_h<VEC, B>(G + at<VEC>(s, j0, lane, a), n, g[a]);
+      const int n = count<VEC>(s, j0, lane, a), first = base<VEC>(s, j0, a);
+      load_f<VEC, B>(M + first, lane_part<VEC>(s, j0, lane, a), n, m[a]);
+      load_h<VEC, B>(G + first, lane_part<VEC>(s, j0, lane, a), n, g[a]);
     }
   }
   // m <- mu m + g; the tiles' sums take u.
   template <bool VEC>
-  __device__ __forceinline__ void use(float* M, const MuShape& s, int64_t j0, int lane, float mu, int nesterov,
+  __device__ __forceinline__ void use(float* M, const MuShape& s, int j0, int lane, float mu, int nesterov,
                                       f64x4 (&acc)[mu_tiles(NT)]) {
     float v[A][B];
 #pragma unroll
@@ -206,7 +236,7 @@ struct GramLoad {
         m[a][b] = mu_momentum(m[a][b], g[a].f32(b), mu);
         v[a][b] = (VEC ? n > 0 : b < n) ? mu_update(m[a][b], g[a].f32(b), mu, nesterov) : 0.0f;
       }
-      store_f<VEC, B>(M + at<VEC>(s, j0, lane, a), n, m[a]);
+      store_f<VEC, B>(M + base<VEC>(s, j0, a), lane_part<VEC>(s, j0, lane, a), n, m[a]);
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -231,27 +261,26 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __r
   const int64_t mat = blockIdx.x / splits;
   const uint16_t* G = Gs + mat * s.rows * s.cols;
   float* M = Ms + mat * s.rows * s.cols;
-  const int64_t stride = (int64_t)splits * 128;
   f64x4 acc[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
-  int64_t j0 = (int64_t)(blockIdx.x % splits) * 128 + wave * 32;
-  // whole steps, the next one's loads in flight over the sums of this one;
-  // then the long axis's end (every step, of a tall factor with odd S)
-  if (!TALL || s.S % NT == 0) {
+  // a whole step's loads go out over the sums of the one before (no step is
+  // whole in a tall factor whose S is not a multiple of NT)
+  Steps at(s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, 32, !TALL || s.S % NT == 0);
+  {
     GramLoad<NT, TALL> x, next;
-    if (j0 + 32 <= s.L) x.template load<true>(G, M, s, j0, lane);
-    for (; j0 + 32 <= s.L; j0 += stride) {
-      if (j0 + stride + 32 <= s.L) next.template load<true>(G, M, s, j0 + stride, lane);
-      x.template use<true>(M, s, j0, lane, mu, nesterov, acc);
+    if (at.valid()) x.template load<true>(G, M, s, at.j0(at.i), lane);
+    for (; at.valid(); at.i += at.stride) {
+      if (at.next_valid()) next.template load<true>(G, M, s, at.j0(at.i + at.stride), lane);
+      x.template use<true>(M, s, at.j0(at.i), lane, mu, nesterov, acc);
       x = next;
     }
   }
 #pragma unroll 1
-  for (; j0 < s.L; j0 += stride) {
+  for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * 32) {
     GramLoad<NT, TALL> x;
-    x.template load<false>(G, M, s, j0, lane);
-    x.template use<false>(M, s, j0, lane, mu, nesterov, acc);
+    x.template load<false>(G, M, s, (int)j0, lane);
+    x.template use<false>(M, s, (int)j0, lane, mu, nesterov, acc);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -408,9 +437,9 @@ __global__ __launch_bounds__(kMuThreads) void k_muon_poly(const double* __restri
 //
 // X = Q u on fp32 MFMA tiles (16 x 16 x 4: A[i][k] lane l: i = l % 16, k = l /
 // 16; D lane l, register q: row 4 (l / 16) + q, column l % 16), the weights
-// and their bf16 copy.  Q is the A operand, held in registers over all of a
-// wave's steps; rows of D are short indexes, columns long positions.  As in
-// pass 1 lanes load consecutive values and the order inside an MFMA follows:
+// and their bf16 copy.  Q is the A operand; rows of D are short indexes,
+// columns long positions.  As in pass 1 lanes load consecutive values and the
+// order inside an MFMA follows:
 //
 //   not tall: lane l has C positions C (l % 16) + c of row k = 4 s + l / 16,
 //             and D gives it the same C positions of rows 16 t + 4 (l / 16) + q;
@@ -420,7 +449,7 @@ __global__ __launch_bounds__(kMuThreads) void k_muon_poly(const double* __restri
 template <int NT, bool TALL>
 struct ApplyShape {
   // positions per lane (not tall) or 16-position groups per step (tall): as
-  // much in flight as the registers hold beside NT^2 * 4 of Q
+  // much in flight as two waves' share of the registers holds
   static constexpr int C = TALL ? 4 : (NT >= 3 ? 2 : 4);
   static constexpr int kGroups = TALL ? (NT == 1 ? 4 : NT == 2 ? 2 : 1) : 1;
   static constexpr int kStep = TALL ? 16 * kGroups : 16 * C;
@@ -443,15 +472,16 @@ __device__ __forceinline__ float mu_weight(const ApplyArgs& a, float w, float x)
 // Loads of rows or short indexes past S are clamped into the matrix: as u they
 // meet the zeros of Q, as weights they are not stored.
 template <int NT, bool VEC>
-__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int64_t j0, int lane,
+__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane,
                                            const float (&qf)[NT][4 * NT]) {
   constexpr int K = ApplyShape<NT, true>::kGroups;
   float m[K][NT][4], w[K][NT][4];
   Halves<4> g[K][NT];
-  auto at = [&](int a, int t) {
-    const int i = 16 * t + 4 * (lane / 16), last = VEC ? s.S - 4 : s.S - 1;
-    if (VEC) return (j0 + 16 * a) * s.S + (lane & 15) * s.S + (t < NT - 1 ? i : (i < last ? i : last));
-    return min64(j0 + 16 * a + (lane & 15), s.L - 1) * s.S + (i < last ? i : last);
+  auto base = [&](int a, int t) { return VEC ? (j0 + 16 * a) * s.S + 16 * t : 0; };
+  auto at = [&](int a, int t) -> uint32_t {
+    const int i = 16 * t + 4 * (lane / 16), last = VEC ? s.S - 4 : s.S - 1, j = j0 + 16 * a + (lane & 15);
+    if (VEC) return (lane & 15) * s.S + (t < NT - 1 || i < last ? i : last) - 16 * t;
+    return (j < s.L ? j : s.L - 1) * s.S + (i < last ? i : last);
   };
   auto count = [&](int a, int t) {
     const int n = s.S - 16 * t - 4 * (lane / 16);
@@ -461,10 +491,11 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
   for (int a = 0; a < K; ++a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      load_f<VEC, 4>(p.M + at(a, t), count(a, t), m[a][t]);
-      load_h<VEC, 4>(p.G + at(a, t), count(a, t), g[a][t]);
-      load_f<VEC, 4>(p.W + at(a, t), count(a, t), w[a][t]);
+      load_f<VEC, 4>(p.M + base(a, t), at(a, t), count(a, t), m[a][t]);
+      load_h<VEC, 4>(p.G + base(a, t), at(a, t), count(a, t), g[a][t]);
+      load_f<VEC, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
+  if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);  // all of the step's loads go out first
 #pragma unroll
   for (int a = 0; a < K; ++a) {
     f32x4 acc[NT];
@@ -480,49 +511,64 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[t][q]);
-      store_f<VEC, 4>(p.W + at(a, t), count(a, t), w[a][t]);
-      store_bf16<VEC, 4>(p.P + at(a, t), count(a, t), w[a][t]);
+      store_f<VEC, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
+      store_bf16<VEC, 4>(p.P + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
   }
 }
 
+// Q in LDS (64 x 64 of it would take the registers of the loads in flight):
+// row strides that put the four rows of an operand into four sets of banks.
+template <int NT>
+constexpr int kQRow = 16 * NT + (NT % 2 == 0 ? 16 : 0);
+
 template <int NT, bool VEC>
-__device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s, int64_t j0, int lane,
-                                           const float (&qf)[NT][4 * NT]) {
+__device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs) {
   constexpr int C = ApplyShape<NT, false>::C;
-  const int64_t j = VEC ? j0 + C * (lane & 15) : min64(j0 + C * (lane & 15), s.L - 1);
-  const int nj = VEC ? C : room(s.L, j0 + C * (lane & 15));
+  const int j = j0 + C * (lane & 15);
+  const int nj = VEC ? C : room(s.L, j), col = VEC ? C * (lane & 15) : (j < s.L ? j : s.L - 1);
   float m[4 * NT][C], w[NT][4][C];
   Halves<C> g[4 * NT];
-  // rows that exist are a uniform offset plus the lane's; only the last tile
-  // of 16 can go past S
-  auto at = [&](int first, int of_lane) {
-    if (first < 16 * (NT - 1)) return first * s.L + (of_lane * s.L + j);
-    const int i = first + of_lane;
-    return (i < s.S ? i : s.S - 1) * s.L + j;
+  // row first + of_lane: only the last tile of 16 can go past S, in its first
+  // row too (the base's row is clamped on its own, so that a lane's offset
+  // from it is never negative)
+  auto row0 = [&](int first) { return first < 16 * (NT - 1) || first < s.S ? first : s.S - 1; };
+  auto base = [&](int first) { return VEC ? row0(first) * s.L + j0 : 0; };
+  auto at = [&](int first, int of_lane) -> uint32_t {
+    if (VEC && first < 16 * (NT - 1)) return of_lane * s.L + col;
+    const int i = first + of_lane < s.S ? first + of_lane : s.S - 1;
+    return (VEC ? i - row0(first) : i) * s.L + col;
   };
 #pragma unroll
   for (int k = 0; k < 4 * NT; ++k) {
-    load_f<VEC, C>(p.M + at(4 * k, lane / 16), nj, m[k]);
-    load_h<VEC, C>(p.G + at(4 * k, lane / 16), nj, g[k]);
+    load_f<VEC, C>(p.M + base(4 * k), at(4 * k, lane / 16), nj, m[k]);
+    load_h<VEC, C>(p.G + base(4 * k), at(4 * k, lane / 16), nj, g[k]);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) load_f<VEC, C>(p.W + at(16 * t + q, 4 * (lane / 16)), nj, w[t][q]);
+    for (int q = 0; q < 4; ++q)
+      load_f<VEC, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), nj, w[t][q]);
+  // all of the step's loads go out first, and Q stays in LDS from step to step
+  if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
   f32x4 acc[NT][C];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 4 * NT; ++k)
+  for (int k = 0; k < 4 * NT; ++k) {
+    float q[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) q[t] = qs[(4 * k + lane / 16) * kQRow<NT> + 16 * t + (lane & 15)];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const float u = mu_update(m[k][c], g[k].f32(c), p.mu, p.nesterov);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t][c] = mfma_f32(qf[t][k], u, acc[t][c]);
+      for (int t = 0; t < NT; ++t) acc[t][c] = mfma_f32(q[t], u, acc[t][c]);
     }
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -530,8 +576,8 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
       const int n = 16 * t + 4 * (lane / 16) + q < s.S ? nj : 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) w[t][q][c] = mu_weight(p, w[t][q][c], acc[t][c][q]);
-      store_f<VEC, C>(p.W + at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
-      store_bf16<VEC, C>(p.P + at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+      store_f<VEC, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+      store_bf16<VEC, C>(p.P + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
     }
 }
 
@@ -546,29 +592,26 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs p, MuSha
   p.W += base;
   p.P += base;
   const float* Q = Qin + (size_t)mat * N * N;
-  float qf[NT][4 * NT];  // MFMA step 4 s + c (tall) or s
+  Steps at(s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, kStep, !TALL || s.S % 4 == 0);
+  if constexpr (TALL) {
+    float qf[NT][4 * NT];  // of MFMA step 4 s + c, over all of the wave's steps
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int k = 0; k < 4 * NT; ++k)
-      qf[t][k] = Q[(16 * t + (lane & 15)) * N + (TALL ? 16 * (k / 4) + 4 * (lane / 16) + k % 4 : 4 * k + lane / 16)];
-  const int64_t stride = (int64_t)splits * 4 * kStep;
-  int64_t j0 = ((int64_t)(blockIdx.x % splits) * 4 + wave) * kStep;
-  if (!TALL || s.S % 4 == 0) {
+      for (int k = 0; k < 4 * NT; ++k)
+        qf[t][k] = Q[(16 * t + (lane & 15)) * N + 16 * (k / 4) + 4 * (lane / 16) + k % 4];
 #pragma unroll 1
-    for (; j0 + kStep <= s.L; j0 += stride) {
-      if constexpr (TALL)
-        apply_tall<NT, true>(p, s, j0, lane, qf);
-      else
-        apply_wide<NT, true>(p, s, j0, lane, qf);
-    }
-  }
+    for (; at.valid(); at.i += at.stride) apply_tall<NT, true>(p, s, at.j0(at.i), lane, qf);
 #pragma unroll 1
-  for (; j0 < s.L; j0 += stride) {
-    if constexpr (TALL)
-      apply_tall<NT, false>(p, s, j0, lane, qf);
-    else
-      apply_wide<NT, false>(p, s, j0, lane, qf);
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) apply_tall<NT, false>(p, s, (int)j0, lane, qf);
+  } else {
+    __shared__ float qs[N * kQRow<NT>];
+    for (int e = threadIdx.x; e < N * N; e += kMuThreads) qs[e / N * kQRow<NT> + e % N] = Q[e];
+    __syncthreads();
+#pragma unroll 1
+    for (; at.valid(); at.i += at.stride) apply_wide<NT, true>(p, s, at.j0(at.i), lane, qs);
+#pragma unroll 1
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) apply_wide<NT, false>(p, s, (int)j0, lane, qs);
   }
 }
 

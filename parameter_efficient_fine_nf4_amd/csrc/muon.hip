@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __r
                                                              MuShape s, float mu, int nesterov, int splits,
                                                              double* __restrict__ part) {
   constexpr int U = mu_tiles(NT);
-  __shared__ double red[4][U * 256];
+  __shared__ double red[2][U * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = blockIdx.x / splits;
   const uint16_t* G = Gs + mat * s.rows * s.cols;
@@ -268,12 +268,11 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __r
   // whole in a tall factor whose S is not a multiple of NT)
   Steps at(s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, 32, !TALL || s.S % NT == 0);
   {
-    GramLoad<NT, TALL> x, next;
-    if (at.valid()) x.template load<true>(G, M, s, at.j0(at.i), lane);
+    GramLoad<NT, TALL> x;
+#pragma unroll 1
     for (; at.valid(); at.i += at.stride) {
-      if (at.next_valid()) next.template load<true>(G, M, s, at.j0(at.i + at.stride), lane);
+      x.template load<true>(G, M, s, at.j0(at.i), lane);
       x.template use<true>(M, s, at.j0(at.i), lane, mu, nesterov, acc);
-      x = next;
     }
   }
 #pragma unroll 1
@@ -282,13 +281,31 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __r
     x.template load<false>(G, M, s, (int)j0, lane);
     x.template use<false>(M, s, (int)j0, lane, mu, nesterov, acc);
   }
+  // the four waves' sums, pairwise: 2 and 3 hand theirs to 0 and 1, 1 to 0
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int half = 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) red[wave][u * 256 + q * 64 + lane] = acc[u][q];
-  __syncthreads();
-  double* out = part + (size_t)blockIdx.x * U * 256;
-  for (int e = threadIdx.x; e < U * 256; e += kMuThreads) out[e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[wave - half][u * 256 + q * 64 + lane] = acc[u][q];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[u][q] += red[wave][u * 256 + q * 64 + lane];
+    }
+    __syncthreads();
+  }
+  if (wave == 0) {
+    double* out = part + (size_t)blockIdx.x * U * 256;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[u * 256 + q * 64 + lane] = acc[u][q];
+  }
 }
 
 // ---------------------------------------------------- S x S iteration ----
@@ -316,54 +333,44 @@ struct PolyLds {
   }
 };
 
-// The tiles are dealt to the four waves in turn.  A wave whose turn is past
-// the last tile repeats tile (0, 0) and does not write it, so that the
-// products have no branch in them.
+// Two waves per SIMD (one would leave the matrix unit idle over its own LDS
+// traffic) share the tiles in turn; the second of two products that run in one
+// phase starts with the wave at which the first one's tiles ended.
 template <int NT>
-constexpr int kPolyTiles = (mu_tiles(NT) + 3) / 4;
+constexpr int kPolyWaves = NT == 2 ? 4 : 8;
+template <int NT>
+constexpr int kPolyTiles = (mu_tiles(NT) + kPolyWaves<NT> - 1) / kPolyWaves<NT>;
 
+// Tile e of this wave of the first (turn 0) or second product of a phase.
 struct PolyTile {
   int u, t, t2;
-  bool own;
 };
 template <int NT>
-__device__ __forceinline__ PolyTile poly_tile(int e) {
-  int u = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) + 4 * e;
-  const bool own = u < mu_tiles(NT);
-  u = own ? u : 0;
+__device__ __forceinline__ PolyTile poly_tile(int turn, int e) {
+  constexpr int W = kPolyWaves<NT>, U = mu_tiles(NT);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int u = (wave + (turn ? W - U % W : 0)) % W + W * e;
   const int t2 = (u >= 1) + (u >= 3) + (u >= 6);
-  return PolyTile{u, u - t2 * (t2 + 1) / 2, t2, own};
+  return PolyTile{u, u - t2 * (t2 + 1) / 2, t2};
 }
 
-template <int NT>
-__device__ __forceinline__ void poly_mul(const double* x, const double* y, f64x4 (&acc)[kPolyTiles<NT>]) {
-  const int lane = threadIdx.x & 63;
-  int xo[kPolyTiles<NT>], yo[kPolyTiles<NT>];  // row lane / 16; row + 4 k differs in bits 2 and 3 of the column
-#pragma unroll
-  for (int e = 0; e < kPolyTiles<NT>; ++e) {
-    const PolyTile p = poly_tile<NT>(e);
-    xo[e] = PolyLds<NT>::at(lane / 16, 16 * p.t + (lane & 15));
-    yo[e] = PolyLds<NT>::at(lane / 16, 16 * p.t2 + (lane & 15));
-    acc[e] = f64x4{0.0, 0.0, 0.0, 0.0};
-  }
-#pragma unroll
-  for (int k = 0; k < 4 * NT; ++k)
-#pragma unroll
-    for (int e = 0; e < kPolyTiles<NT>; ++e)
-      acc[e] = mfma_f64(x[(xo[e] ^ (4 * (k & 3))) + k * 64 * NT], y[(yo[e] ^ (4 * (k & 3))) + k * 64 * NT], acc[e]);
-}
-
-// f(e, q, i, k) for every element (i, k) of the wave's tiles.
+// The wave's tiles of x y, handed element by element to f(q, i, k, value).
 template <int NT, typename F>
-__device__ __forceinline__ void poly_each(F f) {
+__device__ __forceinline__ void poly_mul(int turn, const double* x, const double* y, F f) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int e = 0; e < kPolyTiles<NT>; ++e) {
-    const PolyTile p = poly_tile<NT>(e);
-    if (p.own) {
+    const PolyTile p = poly_tile<NT>(turn, e);
+    if (p.u >= mu_tiles(NT)) break;
+    // row lane / 16; row + 4 k differs in bits 2 and 3 of the column
+    const int xo = PolyLds<NT>::at(lane / 16, 16 * p.t + (lane & 15));
+    const int yo = PolyLds<NT>::at(lane / 16, 16 * p.t2 + (lane & 15));
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) f(e, q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15));
-    }
+    for (int k = 0; k < 4 * NT; ++k)
+      acc = mfma_f64(x[(xo ^ (4 * (k & 3))) + k * 64 * NT], y[(yo ^ (4 * (k & 3))) + k * 64 * NT], acc);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f(4 * e + q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), acc[q]);
   }
 }
 
@@ -373,64 +380,110 @@ __device__ __forceinline__ void poly_put(double* m, int i, int k, double v) {
   if ((i ^ k) >> 4) m[PolyLds<NT>::at(k, i)] = v;
 }
 
+// Sum of the splits' partials of tile u, in order.
+__device__ __forceinline__ f64x4 poly_sum(const double* __restrict__ src, int splits, int tiles, int u, int lane) {
+  f64x4 sum = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += src[((size_t)k * tiles + u) * 256 + q * 64 + lane];
+  return sum;
+}
+
 // part -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
 template <int NT, bool TALL>
-__global__ __launch_bounds__(kMuThreads) void k_muon_poly(const double* __restrict__ part, int splits, MuonCoef co,
-                                                          float eps, float* __restrict__ Qout) {
+__global__ __launch_bounds__(64 * kPolyWaves<NT>) void k_muon_poly(const double* __restrict__ part, int splits,
+                                                                   MuonCoef co, float eps, float* __restrict__ Qout) {
   using At = PolyLds<NT>;
-  constexpr int N = At::N, U = mu_tiles(NT);
+  constexpr int N = At::N, U = mu_tiles(NT), kThreads = 64 * kPolyWaves<NT>;
   __shared__ double G[N * N], P[N * N], Q[N * N], R[N * N];
   const int lane = threadIdx.x & 63;
   const double* src = part + (size_t)blockIdx.x * splits * U * 256;
 #pragma unroll
   for (int e = 0; e < kPolyTiles<NT>; ++e) {
-    const PolyTile p = poly_tile<NT>(e);
-    if (p.own) {
-      double sum[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-      for (int k = 0; k < splits; ++k)
+    const PolyTile p = poly_tile<NT>(0, e);
+    if (p.u >= U) break;
+    const f64x4 sum = poly_sum(src, splits, U, p.u, lane);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum[q] += src[(size_t)k * U * 256 + p.u * 256 + q * 64 + lane];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) poly_put<NT>(G, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
-    }
+    for (int q = 0; q < 4; ++q) poly_put<NT>(G, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
   }
   __syncthreads();
-  double trace = 0.0;
-  for (int i = 0; i < N; ++i) trace += G[At::at(i, i)];
+  double trace = lane < N ? G[At::at(lane, lane)] : 0.0;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) trace += __shfl_xor(trace, o, 64);
   const double inv = 1.0 / (sqrt(trace) + (double)eps);
   __syncthreads();
-  for (int e = threadIdx.x; e < N * N; e += kMuThreads) G[e] *= inv * inv;
+  for (int e = threadIdx.x; e < N * N; e += kThreads) G[e] *= inv * inv;
   __syncthreads();
-  f64x4 a0[kPolyTiles<NT>], a1[kPolyTiles<NT>];
 #pragma unroll 1
   for (int n = 0; n < co.n; ++n) {
     const double ca = co.c[n][0], cb = co.c[n][1], cc = co.c[n][2];
     const bool last = n + 1 == co.n;
-    poly_mul<NT>(G, G, a0);
-    poly_each<NT>([&](int e, int q, int i, int k) {
-      const double p = fma(cc, a0[e][q], fma(cb, G[At::at(i, k)], i == k ? ca : 0.0));
+    poly_mul<NT>(0, G, G, [&](int, int i, int k, double v) {
+      const double p = fma(cc, v, fma(cb, G[At::at(i, k)], i == k ? ca : 0.0));
       poly_put<NT>(P, i, k, p);
       if (n == 0) poly_put<NT>(Q, i, k, p);
     });
     __syncthreads();
-    if (n > 0) poly_mul<NT>(P, Q, a0);
-    if (!last) {
-      poly_mul<NT>(P, G, a1);
-      poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(R, i, k, a1[e][q]); });
-    }
+    double hold[4 * kPolyTiles<NT>];  // P Q, until every wave has read Q
+    if (n > 0) poly_mul<NT>(0, P, Q, [&](int e, int, int, double v) { hold[e] = v; });
+    if (!last) poly_mul<NT>(1, P, G, [&](int, int i, int k, double v) { poly_put<NT>(R, i, k, v); });
     __syncthreads();
-    if (n > 0) poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(Q, i, k, a0[e][q]); });
-    if (!last) {
-      poly_mul<NT>(R, P, a1);
-      poly_each<NT>([&](int e, int q, int i, int k) { poly_put<NT>(G, i, k, a1[e][q]); });
+    if (n > 0) {
+#pragma unroll
+      for (int e = 0; e < kPolyTiles<NT>; ++e) {
+        const PolyTile p = poly_tile<NT>(0, e);
+        if (p.u >= U) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          poly_put<NT>(Q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), hold[4 * e + q]);
+      }
     }
+    if (!last) poly_mul<NT>(0, R, P, [&](int, int i, int k, double v) { poly_put<NT>(G, i, k, v); });
     __syncthreads();
   }
   // tile index (t, i) -> the short index it stands for
   auto of = [](int e) { return TALL ? (e % NT) * 16 + e / NT : e; };
   float* out = Qout + (size_t)blockIdx.x * N * N;
-  for (int e = threadIdx.x; e < N * N; e += kMuThreads) out[e] = (float)(Q[At::at(of(e / N), of(e % N))] * inv);
+  for (int e = threadIdx.x; e < N * N; e += kThreads) out[e] = (float)(Q[At::at(of(e / N), of(e % N))] * inv);
+}
+
+// S <= 16: one tile, one wave, no LDS.  The accumulator's register q holds row
+// l / 16 + 4 q of column l % 16, which is just what operand step k = q of the
+// next product takes: every product feeds the next one in place.
+__device__ __forceinline__ f64x4 poly_mul16(const f64x4& x, const f64x4& y) {
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc = mfma_f64(x[k], y[k], acc);
+  return acc;
+}
+
+__global__ __launch_bounds__(64) void k_muon_poly16(const double* __restrict__ part, int splits, MuonCoef co,
+                                                    float eps, float* __restrict__ Qout) {
+  const int lane = threadIdx.x;
+  f64x4 G = poly_sum(part + (size_t)blockIdx.x * splits * 256, splits, 1, 0, lane);
+  f64x4 one;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) one[q] = lane / 16 + 4 * q == (lane & 15) ? 1.0 : 0.0;
+  double trace = 0.0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) trace += one[q] != 0.0 ? G[q] : 0.0;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) trace += __shfl_xor(trace, o, 64);
+  const double inv = 1.0 / (sqrt(trace) + (double)eps);
+  G *= inv * inv;
+  f64x4 Q = one;
+#pragma unroll 1
+  for (int n = 0; n < co.n; ++n) {
+    const f64x4 sq = poly_mul16(G, G);
+    f64x4 P;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) P[q] = fma(co.c[n][2], sq[q], fma(co.c[n][1], G[q], co.c[n][0] * one[q]));
+    Q = n > 0 ? poly_mul16(P, Q) : P;
+    if (n + 1 < co.n) G = poly_mul16(poly_mul16(P, G), P);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) Qout[(size_t)blockIdx.x * 256 + q * 64 + lane] = (float)(Q[q] * inv);
 }
 
 // -------------------------------------------------------------- pass 2 ----
@@ -619,15 +672,15 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs p, MuSha
 
 static int mu_nt(const MuShape& s) { return (s.S + 15) / 16; }
 
-// Work-groups per matrix: about two per CU over the stack, each with at
+// Work-groups per matrix: `all` over the stack (a few per CU), each with at
 // least `per` long positions.
-static int mu_splits(const MuShape& s, int per) {
-  const int64_t most = (s.L + per - 1) / per;
-  int64_t n = (512 + s.nmat - 1) / s.nmat;
+static int mu_splits(const MuShape& s, int all, int per) {
+  const int64_t most = ((int64_t)s.L + per - 1) / per;
+  int64_t n = (all + s.nmat - 1) / s.nmat;
   if (n > most) n = most;
   return (int)(n < 1 ? 1 : n);
 }
-static int gram_splits(const MuShape& s) { return mu_splits(s, 256); }
+static int gram_splits(const MuShape& s) { return mu_splits(s, 1024, 256); }
 
 static size_t mu_part_bytes(const MuShape& s) {
   return (size_t)s.nmat * gram_splits(s) * mu_tiles(mu_nt(s)) * 256 * sizeof(double);
@@ -643,11 +696,15 @@ template <int NT, bool TALL>
 static void muon_kernels(uint16_t* P, float* W, const uint16_t* G, float* m, const MuShape& s, float momentum,
                          int nesterov, float decay, float step, float eps, const MuonCoef& co, double* part, float* Q,
                          hipStream_t st) {
-  const int gs = gram_splits(s), as = mu_splits(s, 4 * ApplyShape<NT, TALL>::kStep);
+  const int gs = gram_splits(s), as = mu_splits(s, 512, 4 * ApplyShape<NT, TALL>::kStep);
   const dim3 block(kMuThreads);
   QLORA_LAUNCH("muon_gram", st, (k_muon_gram<NT, TALL>), dim3((unsigned)(s.nmat * gs)), block, 0, st, G, m, s,
                momentum, nesterov, gs, part);
-  QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), block, 0, st, part, gs, co, eps, Q);
+  if constexpr (NT == 1)
+    QLORA_LAUNCH("muon_poly", st, k_muon_poly16, dim3((unsigned)s.nmat), dim3(64), 0, st, part, gs, co, eps, Q);
+  else
+    QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), dim3(64 * kPolyWaves<NT>), 0, st,
+                 part, gs, co, eps, Q);
   QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL>), dim3((unsigned)(s.nmat * as)), block, 0, st,
                ApplyArgs{G, m, W, P, momentum, decay, step, nesterov}, s, as, Q);
 }

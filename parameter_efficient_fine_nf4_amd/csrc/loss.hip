@@ -8,13 +8,18 @@
 //   t_v = tau (z_v - max z),  S = sum_v exp t_v,  logp = t_y - ln S,
 //   d logp / d z_v = tau ([v = y] - exp(t_v) / S).
 //
-// Subtracting the maximum from z before the product (not fma(z, c, -max c))
-// keeps rows of very low finite values, whose scaled maximum is not finite,
-// and the label at the maximum exact.  Sums and statistics are fp32 and go
-// through a fixed tree, so results do not depend on the schedule.
+// Exponentials are e_v = 2^(fma(z_v, c, -k)) with c = fl(tau log2 e) and k =
+// fl(c max z): one rounding each, and k's own rounding is the same factor in
+// every e_v and in their sum s, so that p_v = e_v / s is free of it and only
+// ln S takes it back, ln S = ln s + ln 2 (k - c max z), in fp64.  Where |max z|
+// is so large that k could overflow (a row of the type's lowest value) the
+// difference z - max z is taken first.  Sums are fp32 and go through a fixed
+// tree, so results do not depend on the schedule.
 //
-// A row is a work-group's: it is read 16 bytes a lane, at the alignment the
-// row happens to have (an odd V or row stride starts rows at any element).
+// A row is a work-group's, read 16 bytes a lane.  Where it fits the work-group's registers it is read once: all of its loads are in
+// flight together, then the maximum, the sum and the gradient follow from the
+// registers.  Longer rows are read in pieces with a running maximum, and again
+// for the gradient.
 #include <cmath>
 
 #include "common.hpp"
@@ -25,9 +30,9 @@ namespace qlora {
 // 16 bytes at element alignment.
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr double kLn2 = 0.69314718055994530942;
 constexpr float kNegInf = -__builtin_inff();
-constexpr int kRowThreads = 256;
 
 template <typename E>
 struct Elem;
@@ -63,6 +68,20 @@ struct Elem<float> {
   }
 };
 
+// A 16-byte piece of a gradient.  `stream`: the gradient as a whole is larger
+// than half the last-level cache and would only push the logits out of it
+// (T = 4096, V = 32000, bf16, 40 % masked: the next call's log-probabilities
+// take 31 us after such stores and 47 us after ordinary ones, whose lines it
+// has to write back first; the gradient itself 68 and 74 us).  A template
+// argument: of a branch between the two the compiler makes one ordinary store.
+template <bool STREAM>
+__device__ __forceinline__ void put16(void* out, const u32x4& v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(out));
+  else
+    *reinterpret_cast<u32x4_any*>(out) = v;
+}
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -71,28 +90,127 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Maximum and sum over the work-group; every thread gets the result.  `red`
-// holds one float per wave and is free again after the next barrier.
+// Maximum and sum over the work-group of T threads; every thread gets the
+// result.  `red` holds one float per wave.
+template <int T>
 __device__ __forceinline__ float block_max(float v, float* red) {
   v = wave_max(v);
+  if (T == 64) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float r = red[0];
-  for (int i = 1; i < (int)blockDim.x / 64; ++i) r = fmaxf(r, red[i]);
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) r = fmaxf(r, red[i]);
   return r;
 }
+template <int T>
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = wave_sum(v);
+  if (T == 64) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float r = red[0];
-  for (int i = 1; i < (int)blockDim.x / 64; ++i) r += red[i];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) r += red[i];
   return r;
 }
 
-// Running maximum and sum of exp2((z - m) c).  A maximum of -inf (nothing
-// but masked values so far) is read as 0 in the exponents: -inf - (-inf)
-// would make a NaN of it.
+// How a row's exponentials are formed from its maximum m.
+struct RowExp {
+  float c, k, m;
+  bool far;
+  __device__ __forceinline__ RowExp(float m_, float c_)
+      : c(c_), k((float)((double)m_ * (double)c_)), m(m_), far(!(fabsf(m_) < 1e30f)) {}
+  __device__ __forceinline__ float near_e(float z) const { return exp2_hw(fmaf(z, c, -k)); }
+  __device__ __forceinline__ float far_e(float z) const { return exp2_hw((z - m) * c); }
+  __device__ __forceinline__ float e(float z) const { return far ? far_e(z) : near_e(z); }
+  // factor of near_e over far_e: what k's rounding is
+  __device__ __forceinline__ float shift() const {
+    return far ? 1.0f : exp2_hw((float)((double)m * (double)c - (double)k));
+  }
+  // ln of the sum of exp(tau (z - m)), from the sum s of e()
+  __device__ __forceinline__ double ln_sum(float s) const {
+    return log((double)s) + (far ? 0.0 : kLn2 * ((double)k - (double)m * (double)c));
+  }
+};
+
+// The same piece, as far as the compiler knows another one: each pass over a
+// row in registers unpacks its pieces one at a time.  Otherwise the values of
+// one pass, or those that two branches share, are all kept at once (twice the
+// registers of the row, for bf16).
+template <int PASS>
+__device__ __forceinline__ u32x4 anew(u32x4 w) {
+  if (PASS == 0) asm volatile("; maximum" : "+v"(w));
+  if (PASS == 1) asm volatile("; near" : "+v"(w));
+  if (PASS == 2) asm volatile("; far" : "+v"(w));
+  if (PASS == 3) asm volatile("; near, streamed" : "+v"(w));
+  return w;
+}
+
+// A row as 16-byte pieces: nv of them from the first 16-byte boundary on
+// (element `head`), and fewer than 16 single elements before and after, one a
+// thread.  Rows of an odd stride start anywhere; read or written at their own
+// boundaries they take no longer than aligned ones (V = ld = 131071, bf16,
+// policy loss and gradient: 549 us at the rows' starts).
+struct RowSpan {
+  int head, nv, rest;  // rest: this thread's single element, or one past the row
+  template <typename E>
+  __device__ __forceinline__ RowSpan(const E* z, int V) {
+    constexpr int kPer = Elem<E>::kPer16;
+    const int h = (int)((16u - ((uint32_t)(uintptr_t)z & 15u)) & 15u) / (int)sizeof(E);
+    head = h < V ? h : V;
+    nv = (V - head) / kPer;
+    rest = (int)threadIdx.x < head ? (int)threadIdx.x : (int)threadIdx.x + nv * kPer;
+    if (threadIdx.x >= 16 || rest > V) rest = V;
+  }
+};
+// A row of V elements in the registers of T threads: N pieces each and a
+// single element.  What is past the end holds -inf.
+template <typename E, int T, int N>
+struct RowRegs {
+  static constexpr int kPer = Elem<E>::kPer16;
+  u32x4 w[N];
+  float last;
+
+  __device__ __forceinline__ void load(const E* z, int V, const RowSpan& at) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = j * T + threadIdx.x;
+      w[j] = u32x4{Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill};
+      if (i < at.nv) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (size_t)i * kPer);
+    }
+    last = kNegInf;
+    if (at.rest < V) last = Elem<E>::get(z + at.rest);
+  }
+  __device__ __forceinline__ float max() const {
+    float m = last;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float f[kPer];
+      Elem<E>::unpack(anew<0>(w[j]), f);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) m = fmaxf(m, f[q]);
+    }
+    return m;
+  }
+  template <bool FAR>
+  __device__ __forceinline__ float sum_of(const RowExp& x) const {
+    float s[2] = {FAR ? x.far_e(last) : x.near_e(last), 0.0f};
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float f[kPer];
+      Elem<E>::unpack(anew<1 + FAR>(w[j]), f);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) s[q & 1] += FAR ? x.far_e(f[q]) : x.near_e(f[q]);
+    }
+    return s[0] + s[1];
+  }
+  __device__ __forceinline__ float sum(const RowExp& x) const { return x.far ? sum_of<true>(x) : sum_of<false>(x); }
+};
+
+// Running maximum and sum of exp2((z - m) c), for rows read in pieces.  A
+// maximum of -inf (nothing but masked values so far) is read as 0 in the
+// exponents: -inf - (-inf) would make a NaN of it.
 struct Online {
   float m = kNegInf, s = 0.0f;
   template <int N>
@@ -109,118 +227,133 @@ struct Online {
   }
 };
 
-struct RowStats {
-  float m, s;  // max z; sum exp(tau (z - m))
-};
-
-// zy: the label's logit, one of the row's.  It joins the maximum (which it
-// cannot change) so that every wave has it in hand before the first barrier:
-// a caller that writes over the row in place may do so after this returns.
-template <typename E>
-__device__ __forceinline__ RowStats row_stats(const E* z, int V, float zy, float c, float* red) {
-  constexpr int N = Elem<E>::kPer16;
-  const int nv = V / N;
+// Maximum and sum of a row of any length, in pieces.
+template <typename E, int T, int N>
+__device__ __forceinline__ Online row_pieces(const E* z, int V, const RowSpan& at, float c) {
+  constexpr int kPer = Elem<E>::kPer16;
   Online o;
-  for (int i = threadIdx.x; i < nv; i += kRowThreads) {
-    float f[N];
-    Elem<E>::unpack(*reinterpret_cast<const u32x4_any*>(z + (size_t)i * N), f);
-    o.add(f, c);
-  }
-  const int rest = nv * N + threadIdx.x;
-  if (rest < V) {
-    const float f[1] = {Elem<E>::get(z + rest)};
-    o.add(f, c);
-  }
-  RowStats r;
-  r.m = block_max(fmaxf(o.m, zy), red);
-  // a thread without a finite value holds m = -inf and s = 0; a row of
-  // nothing but -inf has no distribution and gives NaN
-  r.s = block_sum(o.s * exp2_hw((o.m - r.m) * c), red + 16);
-  return r;
-}
-
-// z -> g tau ([v = y] - exp2((z - m) c - log2 s)) over one row, and zeros in
-// the columns V..cols-1.
-template <typename E>
-__device__ __forceinline__ void row_grad(const E* z, E* out, int V, int cols, int label,
-                                         float m, float log2s, float c, float g) {
-  constexpr int N = Elem<E>::kPer16;
-  const int nv = V / N;
-  for (int i = threadIdx.x; i < nv; i += kRowThreads) {
-    float f[N];
-    Elem<E>::unpack(*reinterpret_cast<const u32x4_any*>(z + (size_t)i * N), f);
+  for (int i0 = threadIdx.x; i0 < at.nv; i0 += N * T) {
+    float f[N * kPer];
+    u32x4 w[N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const float p = exp2_hw((f[q] - m) * c - log2s);
-      f[q] = (label == i * N + q ? 1.0f - p : -p) * g;
+    for (int j = 0; j < N; ++j) {
+      w[j] = u32x4{Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill};
+      if (i0 + j * T < at.nv) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (size_t)(i0 + j * T) * kPer);
     }
-    *reinterpret_cast<u32x4_any*>(out + (size_t)i * N) = Elem<E>::pack(f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float g[kPer];
+      Elem<E>::unpack(w[j], g);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) f[j * kPer + q] = g[q];
+    }
+    o.add(f, c);
   }
-  const int rest = nv * N + threadIdx.x;
-  if (rest < V) {
-    const float p = exp2_hw((Elem<E>::get(z + rest) - m) * c - log2s);
-    Elem<E>::put(out + rest, (label == rest ? 1.0f - p : -p) * g);
+  if (at.rest < V) {
+    const float f[1] = {Elem<E>::get(z + at.rest)};
+    o.add(f, c);
   }
-  for (int i = V + threadIdx.x; i < cols; i += kRowThreads) Elem<E>::put(out + i, 0.0f);
+  return o;
 }
 
-template <typename E>
-__device__ __forceinline__ void row_zero(E* __restrict__ out, int cols) {
-  constexpr int N = Elem<E>::kPer16;
-  const int nv = cols / N;
-  for (int i = threadIdx.x; i < nv; i += kRowThreads)
-    *reinterpret_cast<u32x4_any*>(out + (size_t)i * N) = u32x4{0u, 0u, 0u, 0u};
-  const int rest = nv * N + threadIdx.x;
-  if (rest < cols) Elem<E>::put(out + rest, 0.0f);
+// One 16-byte piece of the gradient: e_v kappa with kappa = -g tau / s, and g
+// tau (1 - p) at the label.
+template <typename E, bool FAR>
+__device__ __forceinline__ u32x4 grad_piece(const u32x4& w, int first, int label, const RowExp& x, float kappa,
+                                            float gt) {
+  constexpr int kPer = Elem<E>::kPer16;
+  float f[kPer];
+  Elem<E>::unpack(w, f);
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) f[q] = (FAR ? x.far_e(f[q]) : x.near_e(f[q])) * kappa;
+  if ((unsigned)(label - first) < (unsigned)kPer) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (label - first == q) f[q] += gt;
+  }
+  return Elem<E>::pack(f);
+}
+
+template <typename E, int T>
+__device__ __forceinline__ void row_end(float last, E* out, int V, int cols, const RowSpan& at, int label, const RowExp& x,
+                                        float kappa, float gt) {
+  if (at.rest < V) {
+    const float v = x.e(last) * kappa;
+    Elem<E>::put(out + at.rest, label == at.rest ? v + gt : v);
+  }
+  for (int i = V + threadIdx.x; i < cols; i += T) Elem<E>::put(out + i, 0.0f);
+}
+
+// z -> gradient over one row read from memory; zeros in columns V..cols-1.
+template <typename E, int T, bool FAR, bool STREAM>
+__device__ __forceinline__ void row_grad_of(const E* z, E* out, int V, int cols, int label, const RowExp& x,
+                                            float kappa, float gt) {
+  constexpr int kPer = Elem<E>::kPer16;
+  const RowSpan at(z, V);
+  float last = kNegInf;
+  if (at.rest < V) last = Elem<E>::get(z + at.rest);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < at.nv; i += T) {
+    const int first = at.head + i * kPer;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(z + first);
+    put16<STREAM>(out + first, grad_piece<E, FAR>(w, first, label, x, kappa, gt));
+  }
+  row_end<E, T>(last, out, V, cols, at, label, x, kappa, gt);
+}
+template <typename E, int T>
+__device__ __forceinline__ void row_grad(const E* z, E* out, int V, int cols, int label, const RowExp& x, float s,
+                                         float gt, bool stream) {
+  const float kappa = -gt / s;
+  if (x.far)
+    row_grad_of<E, T, true, false>(z, out, V, cols, label, x, kappa, gt);
+  else if (stream)
+    row_grad_of<E, T, false, true>(z, out, V, cols, label, x, kappa, gt);
+  else
+    row_grad_of<E, T, false, false>(z, out, V, cols, label, x, kappa, gt);
+}
+
+// The same from the registers.
+template <typename E, int T, int N, bool FAR, bool STREAM>
+__device__ __forceinline__ void regs_grad_of(const RowRegs<E, T, N>& r, E* out, const RowSpan& at, int label,
+                                             const RowExp& x, float kappa, float gt) {
+  constexpr int kPer = Elem<E>::kPer16;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int i = j * T + threadIdx.x, first = at.head + i * kPer;
+    if (i < at.nv)
+      put16<STREAM>(out + first,
+                    grad_piece<E, FAR>(anew<FAR ? 2 : STREAM ? 3 : 1>(r.w[j]), first, label, x, kappa, gt));
+  }
+}
+template <typename E, int T, int N>
+__device__ __forceinline__ void regs_grad(const RowRegs<E, T, N>& r, E* out, int V, int cols, const RowSpan& at, int label,
+                                          const RowExp& x, float s, float gt, bool stream) {
+  const float kappa = -gt / s;
+  if (x.far)
+    regs_grad_of<E, T, N, true, false>(r, out, at, label, x, kappa, gt);
+  else if (stream)
+    regs_grad_of<E, T, N, false, true>(r, out, at, label, x, kappa, gt);
+  else
+    regs_grad_of<E, T, N, false, false>(r, out, at, label, x, kappa, gt);
+  row_end<E, T>(r.last, out, V, cols, at, label, x, kappa, gt);
+}
+
+template <typename E, int T, bool STREAM>
+__device__ __forceinline__ void row_zero_of(E* out, const RowSpan& at) {
+  for (int i = threadIdx.x; i < at.nv; i += T)
+    put16<STREAM>(out + at.head + (size_t)i * Elem<E>::kPer16, u32x4{0u, 0u, 0u, 0u});
+}
+template <typename E, int T>
+__device__ __forceinline__ void row_zero(E* out, int cols, bool stream) {
+  const RowSpan at(out, cols);
+  if (stream)
+    row_zero_of<E, T, true>(out, at);
+  else
+    row_zero_of<E, T, false>(out, at);
+  if (at.rest < cols) Elem<E>::put(out + at.rest, 0.0f);
 }
 
 __device__ __forceinline__ bool is_counted(int label, int V) { return (uint32_t)label < (uint32_t)V; }
-
-template <typename E>
-__global__ __launch_bounds__(kRowThreads) void k_logprob(const E* __restrict__ logits, int64_t T, int V, int64_t ld,
-                                                         const int32_t* __restrict__ labels, float tau,
-                                                         float* __restrict__ logp, float* __restrict__ stats) {
-  __shared__ float red[32];
-  const float c = tau * kLog2e;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int label = labels[t];
-    float lp = 0.0f, m = 0.0f, l2 = 0.0f;
-    if (is_counted(label, V)) {
-      const E* z = logits + t * ld;
-      const float zy = Elem<E>::get(z + label);
-      const RowStats r = row_stats(z, V, zy, c, red);
-      m = r.m;
-      l2 = log2f(r.s);
-      lp = (zy - m) * tau - logf(r.s);
-    }
-    if (threadIdx.x == 0) {
-      logp[t] = lp;
-      if (stats != nullptr) {
-        stats[2 * t] = m;
-        stats[2 * t + 1] = l2;
-      }
-    }
-    __syncthreads();  // red is written again for the next row
-  }
-}
-
-template <typename E>
-__global__ __launch_bounds__(kRowThreads) void k_logprob_grad(const E* logits, int64_t T, int V, int64_t ld,
-                                                              const int32_t* __restrict__ labels, float tau,
-                                                              const float* __restrict__ stats,
-                                                              const float* __restrict__ dlogp, E* dlogits,
-                                                              int64_t ldd) {
-  const float c = tau * kLog2e;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int label = labels[t];
-    const float g = dlogp[t];
-    E* out = dlogits + t * ldd;
-    if (!is_counted(label, V) || g == 0.0f)
-      row_zero(out, (int)ldd);
-    else
-      row_grad(logits + t * ld, out, V, (int)ldd, label, stats[2 * t], stats[2 * t + 1], c, g * tau);
-  }
-}
 
 // ------------------------------------------------------- policy loss -----
 //
@@ -230,7 +363,7 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_grad(const E* logits, i
 //   loss = -min(r A, clip(r) A) + kl_coef (exp(d) - d - 1)
 //   d loss / d lp = -r A (0 where the clip holds) - kl_coef (exp(d) - 1)
 //
-// expm1 keeps the KL term's digits where d is small.
+// lp comes in fp64: the differences with old and ref are small against it.
 struct PolicyArgs {
   const float* adv;
   const float* old_logp;  // nullptr: the policy itself (r = 1)
@@ -241,9 +374,25 @@ struct PolicyArgs {
   float* kl;
 };
 
-__device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, float lp, float& loss, float& kl) {
+// exp(d) - 1 - d: below 1/2 in size its series (to d^10 / 10!, 1e-10 of it),
+// since exp(d) - 1 and d would cancel.
+__device__ __forceinline__ float exp_less_two_terms(float d, float expm1_d) {
+  if (fabsf(d) >= 0.5f) return expm1_d - d;
+  float p = 1.0f / 3628800.0f;
+  p = fmaf(p, d, 1.0f / 362880.0f);
+  p = fmaf(p, d, 1.0f / 40320.0f);
+  p = fmaf(p, d, 1.0f / 5040.0f);
+  p = fmaf(p, d, 1.0f / 720.0f);
+  p = fmaf(p, d, 1.0f / 120.0f);
+  p = fmaf(p, d, 1.0f / 24.0f);
+  p = fmaf(p, d, 1.0f / 6.0f);
+  p = fmaf(p, d, 0.5f);
+  return p * d * d;
+}
+
+__device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, double lp, float& loss, float& kl) {
   const float A = a.adv[t];
-  const float r = a.old_logp != nullptr ? expf(lp - a.old_logp[t]) : (lp == lp ? 1.0f : lp);
+  const float r = a.old_logp != nullptr ? expf((float)(lp - (double)a.old_logp[t])) : (lp == lp ? 1.0f : (float)lp);
   const float rc = fminf(fmaxf(r, a.lo), a.hi);
   const float x = r * A, y = rc * A;
   const bool clipped = y < x;  // the clipped branch is the smaller one, and flat
@@ -251,9 +400,9 @@ __device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, fl
   float g = clipped ? 0.0f : -x;
   kl = 0.0f;
   if (a.ref_logp != nullptr) {
-    const float d = a.ref_logp[t] - lp;
+    const float d = (float)((double)a.ref_logp[t] - lp);
     const float e = expm1f(d);
-    kl = e - d;
+    kl = exp_less_two_terms(d, e);
     loss = fmaf(a.kl_coef, kl, loss);
     g = fmaf(-a.kl_coef, e, g);
   }
@@ -262,37 +411,118 @@ __device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, fl
   return w == 0.0f ? 0.0f : g * w;  // a token taken out has no gradient, not a NaN either
 }
 
-template <typename E>
-__global__ __launch_bounds__(kRowThreads) void k_policy(const E* logits, int64_t T, int V, int64_t ld,
-                                                        const int32_t* __restrict__ labels, float tau, PolicyArgs a,
-                                                        float* __restrict__ logp, E* dlogits, int64_t ldd) {
-  __shared__ float red[32];
-  const float c = tau * kLog2e;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int label = labels[t];
-    E* out = dlogits != nullptr ? dlogits + t * ldd : nullptr;
-    float lp = 0.0f, loss = 0.0f, kl = 0.0f;
-    if (is_counted(label, V)) {
-      const E* z = logits + t * ld;
-      const float zy = Elem<E>::get(z + label);
-      const RowStats r = row_stats(z, V, zy, c, red);
-      lp = (zy - r.m) * tau - logf(r.s);
-      const float g = policy_token(a, t, lp, loss, kl);
-      if (out != nullptr) {
-        if (g == 0.0f)
-          row_zero(out, (int)ldd);
-        else
-          row_grad(z, out, V, (int)ldd, label, r.m, log2f(r.s), c, g * tau);
+// ------------------------------------------------------- row kernels -----
+
+struct RowArgs {
+  const void* logits;
+  int64_t T, ld, ldd;
+  int V;
+  const int32_t* labels;
+  float tau, c;  // c = fl(tau log2 e)
+  float* logp;
+  float* stats;  // (max z, sum of e) per row
+  void* dlogits;
+  bool stream;  // dlogits past the last-level cache
+};
+
+// Log-probabilities, and with POLICY the policy loss and its gradient.  N > 0:
+// the row fits N pieces a thread; N < 0: -N pieces a thread at a time.
+template <typename E, int T, int N, bool POLICY>
+__global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
+  __shared__ float red[2][T / 64];
+  __shared__ float gsh;
+  const E* logits = reinterpret_cast<const E*>(a.logits);
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int label = a.labels[t];
+    E* out = POLICY && a.dlogits != nullptr ? reinterpret_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
+    if (!is_counted(label, a.V)) {
+      if (out != nullptr) row_zero<E, T>(out, (int)a.ldd, a.stream);
+      if (threadIdx.x == 0) {
+        a.logp[t] = 0.0f;
+        if (a.stats != nullptr) {
+          a.stats[2 * t] = 0.0f;
+          a.stats[2 * t + 1] = 1.0f;
+        }
+        if (POLICY) {
+          pa.loss[t] = 0.0f;
+          if (pa.kl != nullptr) pa.kl[t] = 0.0f;
+        }
       }
-    } else if (out != nullptr) {
-      row_zero(out, (int)ldd);
+      continue;
     }
-    if (threadIdx.x == 0) {
-      logp[t] = lp;
-      a.loss[t] = loss;
-      if (a.kl != nullptr) a.kl[t] = kl;
+    const E* z = logits + t * a.ld;
+    // the label's logit is one of the row's: it joins the maximum so that
+    // every wave has it in hand before the first barrier, and the row may be
+    // written over after that
+    const float zy = Elem<E>::get(z + label);
+    RowRegs<E, T, N < 0 ? 1 : N> r;
+    const RowSpan at(z, a.V);
+    Online o;
+    float m;
+    if constexpr (N > 0) {
+      r.load(z, a.V, at);
+      m = block_max<T>(fmaxf(r.max(), zy), red[0]);
+    } else {
+      o = row_pieces<E, T, -N>(z, a.V, at, a.c);
+      m = block_max<T>(fmaxf(o.m, zy), red[0]);
     }
-    __syncthreads();
+    const RowExp x(m, a.c);
+    // (in pieces: a thread without a finite value holds m = -inf and s = 0; a
+    // row of nothing but -inf has no distribution and gives NaN)
+    float s;
+    if constexpr (N > 0)
+      s = block_sum<T>(r.sum(x), red[1]);
+    else
+      s = block_sum<T>(o.s * x.far_e(o.m), red[1]) * x.shift();
+    float g = 0.0f;
+    if (threadIdx.x < 64) {  // fp64, once: one wave
+      const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s);
+      float loss, kl;
+      if (POLICY) g = policy_token(pa, t, lp, loss, kl);
+      if (threadIdx.x == 0) {
+        a.logp[t] = (float)lp;
+        if (a.stats != nullptr) {
+          a.stats[2 * t] = m;
+          a.stats[2 * t + 1] = s;
+        }
+        if (POLICY) {
+          gsh = g;
+          pa.loss[t] = loss;
+          if (pa.kl != nullptr) pa.kl[t] = kl;
+        }
+      }
+    }
+    if (POLICY && out != nullptr) {
+      if (T > 64) {
+        __syncthreads();
+        g = gsh;
+      }
+      if (g == 0.0f)
+        row_zero<E, T>(out, (int)a.ldd, a.stream);
+      else if constexpr (N > 0)
+        regs_grad<E, T, N>(r, out, a.V, (int)a.ldd, at, label, x, s, g * a.tau, a.stream);
+      else
+        row_grad<E, T>(z, out, a.V, (int)a.ldd, label, x, s, g * a.tau, a.stream);
+    }
+    if (T > 64) __syncthreads();  // red and gsh are written again for the next row
+  }
+}
+
+// The rows go from the last to the first: the forward ended with the last
+// ones, and what of them is in the last-level cache is read from there.
+template <typename E, int T>
+__global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __restrict__ dlogp) {
+  for (int64_t t = a.T - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
+    const int label = a.labels[t];
+    const float g = dlogp[t];
+    E* out = reinterpret_cast<E*>(a.dlogits) + t * a.ldd;
+    if (!is_counted(label, a.V) || g == 0.0f) {
+      row_zero<E, T>(out, (int)a.ldd, a.stream);
+    } else {
+      const RowExp x(a.stats[2 * t], a.c);
+      row_grad<E, T>(reinterpret_cast<const E*>(a.logits) + t * a.ld, out, a.V, (int)a.ldd, label, x,
+                     a.stats[2 * t + 1], g * a.tau, a.stream);
+    }
   }
 }
 
@@ -309,6 +539,8 @@ __global__ __launch_bounds__(kRowThreads) void k_policy(const E* logits, int64_t
 //
 // A work-group takes a pair: it sums in fp64 (thousands of terms, of which a
 // small difference is left) and writes each token's d loss / d logp.
+constexpr int kPrefThreads = 256;
+
 struct PrefArgs {
   const float* logp;
   const float* ref_logp;
@@ -332,9 +564,9 @@ __device__ __forceinline__ void seq_range(const PrefArgs& a, int64_t s, int64_t&
   hi = y < lo ? lo : (y > a.T ? a.T : y);
 }
 
-__global__ __launch_bounds__(kRowThreads) void k_preference(PrefArgs a) {
-  __shared__ double sums[2][kRowThreads / 64];
-  __shared__ int counts[2][kRowThreads / 64];
+__global__ __launch_bounds__(kPrefThreads) void k_preference(PrefArgs a) {
+  __shared__ double sums[2][kPrefThreads / 64];
+  __shared__ int counts[2][kPrefThreads / 64];
   const int64_t p = blockIdx.x;
   int64_t lo[2], hi[2];
   seq_range(a, p, lo[0], hi[0]);
@@ -343,7 +575,7 @@ __global__ __launch_bounds__(kRowThreads) void k_preference(PrefArgs a) {
   for (int k = 0; k < 2; ++k) {
     double sum = 0.0;
     int n = 0;
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) {
+    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPrefThreads) {
       if (is_counted(a.labels[t], a.V)) {
         sum += a.ref_logp != nullptr ? (double)a.logp[t] - (double)a.ref_logp[t] : (double)a.logp[t];
         ++n;
@@ -364,7 +596,7 @@ __global__ __launch_bounds__(kRowThreads) void k_preference(PrefArgs a) {
   for (int k = 0; k < 2; ++k) {
     l[k] = 0.0;
     int n = 0;
-    for (int w = 0; w < kRowThreads / 64; ++w) {
+    for (int w = 0; w < kPrefThreads / 64; ++w) {
       l[k] += sums[k][w];
       n += counts[k][w];
     }
@@ -402,57 +634,99 @@ __global__ __launch_bounds__(kRowThreads) void k_preference(PrefArgs a) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float g = (float)((k == 0 ? dl : -dl) * inv[k]);
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads)
+    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPrefThreads)
       a.dlogp[t] = is_counted(a.labels[t], a.V) ? g : 0.0f;
   }
   // tokens before the first sequence and after the last have no gradient
   if (p == 0)
-    for (int64_t t = threadIdx.x; t < lo[0]; t += kRowThreads) a.dlogp[t] = 0.0f;
+    for (int64_t t = threadIdx.x; t < lo[0]; t += kPrefThreads) a.dlogp[t] = 0.0f;
   if (p == a.P - 1)
-    for (int64_t t = hi[1] + threadIdx.x; t < a.T; t += kRowThreads) a.dlogp[t] = 0.0f;
+    for (int64_t t = hi[1] + threadIdx.x; t < a.T; t += kPrefThreads) a.dlogp[t] = 0.0f;
 }
 
 // ---------------------------------------------------------- launchers ----
 
-// Work-groups of the row kernels: a row each, up to a grid whose thread
-// count stays below 2^32.
+// Work-groups of the row kernels: a row each, up to a grid whose thread count
+// stays below 2^32.
 static dim3 row_grid(int64_t T) { return dim3((unsigned)(T < (1 << 20) ? T : (1 << 20))); }
+
+template <typename E, int T, int N, bool POLICY>
+static void rows_kernel(const char* name, const RowArgs& a, const PolicyArgs& pa, hipStream_t st) {
+  QLORA_LAUNCH(name, st, (k_rows<E, T, N, POLICY>), row_grid(a.T), dim3(T), 0, st, a, pa);
+}
+
+// Threads a row and what each holds, by the row's number of 16-byte pieces.
+// One wave takes a short row without a barrier.  Fewer rows than two per CU
+// leave CUs idle, and a row's own latency counts: the most threads.
+// Measured on 4096 rows (us; log-probabilities / policy loss and gradient):
+// V = 32000 in bf16, 4000 pieces: 256 x 16 in registers 44 / 102, 512 x 8 48 /
+// 98, in pieces 512 x 4 44 / 109; V = 131072, 16384 pieces: 1024 x 16 in
+// registers 214 / 491 (one row a CU, nothing to load while it computes), in
+// pieces 1024 x 2 160 / 397 and 1024 x 4 162 / 383 (the second reading comes
+// from the last-level cache).
+template <typename E, bool POLICY>
+static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyArgs& pa, hipStream_t st) {
+  const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
+  if (pieces <= 64 * 4)
+    rows_kernel<E, 64, 4, POLICY>(name, a, pa, st);
+  else if (a.T < 512 && pieces > 1024 && pieces <= 1024 * 8)
+    pieces <= 1024 * 4 ? rows_kernel<E, 1024, 4, POLICY>(name, a, pa, st)
+                       : rows_kernel<E, 1024, 8, POLICY>(name, a, pa, st);
+  else if (pieces <= 256 * 4)
+    rows_kernel<E, 256, 4, POLICY>(name, a, pa, st);
+  else if (pieces <= 256 * 8)
+    rows_kernel<E, 256, 8, POLICY>(name, a, pa, st);
+  else if (pieces <= 4096)
+    rows_kernel<E, POLICY ? 512 : 256, POLICY ? 8 : 16, POLICY>(name, a, pa, st);
+  else
+    rows_kernel<E, 1024, POLICY ? -4 : -2, POLICY>(name, a, pa, st);
+  return hipGetLastError();
+}
+
+// The same for the gradient alone, in pieces (V = 131072: 1024 threads 359 us,
+// 512 367, 256 381; V = 32000: 70, 68, 70).
+template <typename E>
+static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t st) {
+  const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
+  if (pieces <= 64 * 4)
+    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 64>), row_grid(a.T), dim3(64), 0, st, a, dlogp);
+  else if (pieces <= 256 * 4)
+    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 256>), row_grid(a.T), dim3(256), 0, st, a, dlogp);
+  else if (pieces <= 4096 && a.T >= 512)
+    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 512>), row_grid(a.T), dim3(512), 0, st, a, dlogp);
+  else
+    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 1024>), row_grid(a.T), dim3(1024), 0, st, a, dlogp);
+  return hipGetLastError();
+}
+
+// Half of the 256 MB last-level cache.
+static bool past_cache(int64_t T, int64_t ldd, int f32) { return T * ldd * (f32 ? 4 : 2) > ((int64_t)128 << 20); }
+
+static float exp2_scale(float tau) { return (float)((double)tau * kLog2e); }
 
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                           float* logp, float* stats, hipStream_t st) {
-  if (f32)
-    QLORA_LAUNCH("logprob", st, k_logprob<float>, row_grid(T), dim3(kRowThreads), 0, st, (const float*)logits, T, V,
-                 ld, labels, tau, logp, stats);
-  else
-    QLORA_LAUNCH("logprob", st, k_logprob<uint16_t>, row_grid(T), dim3(kRowThreads), 0, st, (const uint16_t*)logits,
-                 T, V, ld, labels, tau, logp, stats);
-  return hipGetLastError();
+  const RowArgs a{logits, T, ld, 0, V, labels, tau, exp2_scale(tau), logp, stats, nullptr, false};
+  return f32 ? launch_rows<float, false>("logprob", a, PolicyArgs{}, st)
+             : launch_rows<uint16_t, false>("logprob", a, PolicyArgs{}, st);
 }
 
 hipError_t launch_logprob_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels,
                                float tau, const float* stats, const float* dlogp, void* dlogits, int64_t ldd,
                                hipStream_t st) {
-  if (f32)
-    QLORA_LAUNCH("logprob_grad", st, k_logprob_grad<float>, row_grid(T), dim3(kRowThreads), 0, st,
-                 (const float*)logits, T, V, ld, labels, tau, stats, dlogp, (float*)dlogits, ldd);
-  else
-    QLORA_LAUNCH("logprob_grad", st, k_logprob_grad<uint16_t>, row_grid(T), dim3(kRowThreads), 0, st,
-                 (const uint16_t*)logits, T, V, ld, labels, tau, stats, dlogp, (uint16_t*)dlogits, ldd);
-  return hipGetLastError();
+  const RowArgs a{logits, T,       ld,     ldd,  V, labels, tau, exp2_scale(tau), nullptr, const_cast<float*>(stats),
+                  dlogits, past_cache(T, ldd, f32)};
+  return f32 ? launch_grad<float>(a, dlogp, st) : launch_grad<uint16_t>(a, dlogp, st);
 }
 
 hipError_t launch_policy(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                          const float* adv, const float* old_logp, const float* ref_logp, const float* weight,
                          float clip_low, float clip_high, float kl_coef, float* loss, float* kl, float* logp,
                          void* dlogits, int64_t ldd, hipStream_t st) {
-  const PolicyArgs a{adv, old_logp, ref_logp, weight, 1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, kl};
-  if (f32)
-    QLORA_LAUNCH("policy", st, k_policy<float>, row_grid(T), dim3(kRowThreads), 0, st, (const float*)logits, T, V, ld,
-                 labels, tau, a, logp, (float*)dlogits, ldd);
-  else
-    QLORA_LAUNCH("policy", st, k_policy<uint16_t>, row_grid(T), dim3(kRowThreads), 0, st, (const uint16_t*)logits, T,
-                 V, ld, labels, tau, a, logp, (uint16_t*)dlogits, ldd);
-  return hipGetLastError();
+  const PolicyArgs pa{adv, old_logp, ref_logp, weight, 1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, kl};
+  const RowArgs a{logits, T, ld, ldd, V, labels, tau, exp2_scale(tau), logp, nullptr, dlogits,
+                  past_cache(T, ldd, f32)};
+  return f32 ? launch_rows<float, true>("policy", a, pa, st) : launch_rows<uint16_t, true>("policy", a, pa, st);
 }
 
 hipError_t launch_preference(const float* logp, const float* ref_logp, const int32_t* labels, int64_t T, int V,
@@ -461,7 +735,7 @@ hipError_t launch_preference(const float* logp, const float* ref_logp, const int
                              hipStream_t st) {
   const PrefArgs a{logp, ref_logp, labels, cu, weight, T, P, V, kind, average, beta, smoothing, margin, loss, reward,
                    dlogp};
-  QLORA_LAUNCH("preference", st, k_preference, dim3((unsigned)P), dim3(kRowThreads), 0, st, a);
+  QLORA_LAUNCH("preference", st, k_preference, dim3((unsigned)P), dim3(kPrefThreads), 0, st, a);
   return hipGetLastError();
 }
 

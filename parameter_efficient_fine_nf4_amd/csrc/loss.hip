@@ -656,30 +656,39 @@ static void rows_kernel(const char* name, const RowArgs& a, const PolicyArgs& pa
 }
 
 // Threads a row and what each holds, by the row's number of 16-byte pieces.
-// One wave takes a short row without a barrier.  Fewer rows than two per CU
-// leave CUs idle, and a row's own latency counts: the most threads.
-// Measured on 4096 rows (us; log-probabilities / policy loss and gradient):
-// V = 32000 in bf16, 4000 pieces: 256 x 16 in registers 44 / 102, 512 x 8 48 /
-// 98, in pieces 512 x 4 44 / 109; V = 131072, 16384 pieces: 1024 x 16 in
-// registers 214 / 491 (one row a CU, nothing to load while it computes), in
-// pieces 1024 x 2 160 / 397 and 1024 x 4 162 / 383 (the second reading comes
-// from the last-level cache).
+// One wave takes a short row without a barrier.  Up to one row per CU a row's
+// own latency counts: the most threads.  With more rows 256 threads with a
+// row in registers that fits closely (pieces that do not exist cost their
+// exponentials all the same).  Measured on 4096 rows of bf16 (us,
+// log-probabilities / policy loss and gradient):
+//   V = 20000, 2500 pieces:   256 x 10 29 / 60, 256 x 16 36 / 74, 512 x 8 41 /
+//                             73, in pieces 256 x 4 32 / 76;
+//   V = 32000, 4000 pieces:   256 x 16 44 / 102, 512 x 8 48 / 98, in pieces 512
+//                             x 4 44 / 109;
+//   V = 131072, 16384 pieces: 1024 x 16 214 / 496 (one row a CU, nothing to
+//                             load while it computes), in pieces 1024 x 4
+//                             154 / 435, 512 x 4 161 / 422 (the second
+//                             reading comes from the last-level cache).
 template <typename E, bool POLICY>
 static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyArgs& pa, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
   if (pieces <= 64 * 4)
     rows_kernel<E, 64, 4, POLICY>(name, a, pa, st);
-  else if (a.T < 512 && pieces > 1024 && pieces <= 1024 * 8)
+  else if (a.T <= 256 && pieces > 1024 && pieces <= 1024 * 8)
     pieces <= 1024 * 4 ? rows_kernel<E, 1024, 4, POLICY>(name, a, pa, st)
                        : rows_kernel<E, 1024, 8, POLICY>(name, a, pa, st);
   else if (pieces <= 256 * 4)
     rows_kernel<E, 256, 4, POLICY>(name, a, pa, st);
-  else if (pieces <= 256 * 8)
-    rows_kernel<E, 256, 8, POLICY>(name, a, pa, st);
+  else if (pieces <= 256 * 7)
+    rows_kernel<E, 256, 7, POLICY>(name, a, pa, st);
+  else if (pieces <= 256 * 10)
+    rows_kernel<E, 256, 10, POLICY>(name, a, pa, st);
+  else if (pieces <= 256 * 12)
+    rows_kernel<E, 256, 12, POLICY>(name, a, pa, st);
   else if (pieces <= 4096)
     rows_kernel<E, POLICY ? 512 : 256, POLICY ? 8 : 16, POLICY>(name, a, pa, st);
   else
-    rows_kernel<E, 1024, POLICY ? -4 : -2, POLICY>(name, a, pa, st);
+    rows_kernel<E, 1024, -4, POLICY>(name, a, pa, st);
   return hipGetLastError();
 }
 

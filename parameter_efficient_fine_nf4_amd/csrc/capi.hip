@@ -857,7 +857,7 @@ int qlora_muon_step(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t 
   if (P == nullptr || W == nullptr || G == nullptr || m == nullptr) return QLORA_ERR_NULL;
   if (!aligned16(P) || !aligned16(W) || !aligned16(G) || !aligned16(m) || !aligned16(ws)) return QLORA_ERR_ALIGN;
   const size_t need = muon_ws_bytes(nmat, rows, cols);
-  if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
   const size_t n = (size_t)(nmat * rows * cols);
   const Region out[4] = {{P, n * 2}, {W, n * 4}, {m, n * 4}, {ws, need}};
   const Region in[1] = {{G, n * 2}};

@@ -30,6 +30,10 @@
 namespace qlora {
 
 constexpr int kMuThreads = 256;
+// Elements of a matrix with S <= 16 up to which one work-group takes it whole
+// (8 x 256: 8.4 us a call against 12.1 in two launches; 8 x 1024: 12.2 against
+// 11.8, as one CU's loads no longer keep up with many).
+constexpr int64_t kMuWhole = 4096;
 
 struct MuShape {
   int64_t nmat, rows, cols;
@@ -89,10 +93,15 @@ __device__ __forceinline__ T& lane_at(E* base, uint32_t at) {
   return *reinterpret_cast<T*>(reinterpret_cast<B*>(base) + at * (uint32_t)sizeof(E));
 }
 
-template <bool VEC, int N>
+// STREAM (with VEC): past the caches.
+template <bool VEC, bool STREAM, int N>
 __device__ __forceinline__ void load_f(const float* p, uint32_t at, int n, float (&v)[N]) {
   if constexpr (VEC) {
-    const typename Vec<N>::F x = lane_at<const typename Vec<N>::F>(p, at);
+    typename Vec<N>::F x;
+    if constexpr (STREAM)
+      x = __builtin_nontemporal_load(&lane_at<const typename Vec<N>::F>(p, at));
+    else
+      x = lane_at<const typename Vec<N>::F>(p, at);
     __builtin_memcpy(v, &x, N * 4);
   } else {
 #pragma unroll
@@ -112,13 +121,16 @@ __device__ __forceinline__ void load_h(const uint16_t* p, uint32_t at, int n, Ha
                (uint32_t)lane_at<const uint16_t>(p, at + clamp_at(2 * i + 1, n)) << 16;
   }
 }
-template <bool VEC, int N>
+template <bool VEC, bool STREAM, int N>
 __device__ __forceinline__ void store_f(float* p, uint32_t at, int n, const float (&v)[N]) {
   if constexpr (VEC) {
     if (n > 0) {
       typename Vec<N>::F x;
       __builtin_memcpy(&x, v, N * 4);
-      lane_at<typename Vec<N>::F>(p, at) = x;
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(x, &lane_at<typename Vec<N>::F>(p, at));
+      else
+        lane_at<typename Vec<N>::F>(p, at) = x;
     }
   } else {
 #pragma unroll
@@ -126,7 +138,7 @@ __device__ __forceinline__ void store_f(float* p, uint32_t at, int n, const floa
       if (i < n) lane_at<float>(p, at + i) = v[i];
   }
 }
-template <bool VEC, int N>
+template <bool VEC, bool STREAM, int N>
 __device__ __forceinline__ void store_bf16(uint16_t* p, uint32_t at, int n, const float (&v)[N]) {
   uint32_t h[(N + 1) / 2];
 #pragma unroll
@@ -135,7 +147,10 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, uint32_t at, int n, cons
     if (n > 0) {
       typename Vec<N>::H x;
       __builtin_memcpy(&x, h, N * 2);
-      lane_at<typename Vec<N>::H>(p, at) = x;
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(x, &lane_at<typename Vec<N>::H>(p, at));
+      else
+        lane_at<typename Vec<N>::H>(p, at) = x;
     }
   } else {
 #pragma unroll
@@ -219,7 +234,7 @@ struct GramLoad {
 #pragma unroll
     for (int a = 0; a < A; ++a) {
       const int n = count<VEC>(s, j0, lane, a), first = base<VEC>(s, j0, a);
-      load_f<VEC, B>(M + first, lane_part<VEC>(s, j0, lane, a), n, m[a]);
+      load_f<VEC, false, B>(M + first, lane_part<VEC>(s, j0, lane, a), n, m[a]);
       load_h<VEC, B>(G + first, lane_part<VEC>(s, j0, lane, a), n, g[a]);
     }
   }
@@ -236,7 +251,7 @@ struct GramLoad {
         m[a][b] = mu_momentum(m[a][b], g[a].f32(b), mu);
         v[a][b] = (VEC ? n > 0 : b < n) ? mu_update(m[a][b], g[a].f32(b), mu, nesterov) : 0.0f;
       }
-      store_f<VEC, B>(M + base<VEC>(s, j0, a), lane_part<VEC>(s, j0, lane, a), n, m[a]);
+      store_f<VEC, false, B>(M + base<VEC>(s, j0, a), lane_part<VEC>(s, j0, lane, a), n, m[a]);
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -251,54 +266,64 @@ struct GramLoad {
   }
 };
 
+// The sums of one wave (`wave` of `waves`) over a matrix.
 template <int NT, bool TALL>
-__global__ __launch_bounds__(kMuThreads, 2) void k_muon_gram(const uint16_t* __restrict__ Gs, float* __restrict__ Ms,
-                                                             MuShape s, float mu, int nesterov, int splits,
-                                                             double* __restrict__ part) {
-  constexpr int U = mu_tiles(NT);
-  __shared__ double red[2][U * 256];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t mat = blockIdx.x / splits;
-  const uint16_t* G = Gs + mat * s.rows * s.cols;
-  float* M = Ms + mat * s.rows * s.cols;
-  f64x4 acc[U];
+__device__ __forceinline__ void gram_sums(const uint16_t* G, float* M, const MuShape& s, int64_t mat, int wave, int waves,
+                                          int lane, float mu, int nesterov, f64x4 (&acc)[mu_tiles(NT)]) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
-  // a whole step's loads go out over the sums of the one before (no step is
-  // whole in a tall factor whose S is not a multiple of NT)
-  Steps at(s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, 32, !TALL || s.S % NT == 0);
-  {
-    GramLoad<NT, TALL> x;
+  for (int u = 0; u < mu_tiles(NT); ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
+  // (no step is whole in a tall factor whose S is not a multiple of NT)
+  Steps at(s, mat, wave, waves, 32, !TALL || s.S % NT == 0);
+  GramLoad<NT, TALL> x;
 #pragma unroll 1
-    for (; at.valid(); at.i += at.stride) {
-      x.template load<true>(G, M, s, at.j0(at.i), lane);
-      x.template use<true>(M, s, at.j0(at.i), lane, mu, nesterov, acc);
-    }
+  for (; at.valid(); at.i += at.stride) {
+    x.template load<true>(G, M, s, at.j0(at.i), lane);
+    x.template use<true>(M, s, at.j0(at.i), lane, mu, nesterov, acc);
   }
 #pragma unroll 1
   for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * 32) {
-    GramLoad<NT, TALL> x;
     x.template load<false>(G, M, s, (int)j0, lane);
     x.template use<false>(M, s, (int)j0, lane, mu, nesterov, acc);
   }
-  // the four waves' sums, pairwise: 2 and 3 hand theirs to 0 and 1, 1 to 0
+}
+
+// The W waves' sums to wave 0, halving: the upper half of the waves left hand
+// theirs to the lower half.  red: W / 2 x U x 256 doubles.
+template <int NT, int W>
+__device__ __forceinline__ void gram_reduce(f64x4 (&acc)[mu_tiles(NT)], double* red, int wave, int lane) {
+  constexpr int U = mu_tiles(NT);
 #pragma unroll
-  for (int half = 2; half >= 1; half /= 2) {
+  for (int half = W / 2; half >= 1; half /= 2) {
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[wave - half][u * 256 + q * 64 + lane] = acc[u][q];
+        for (int q = 0; q < 4; ++q) red[((wave - half) * U + u) * 256 + q * 64 + lane] = acc[u][q];
     }
     __syncthreads();
     if (wave < half) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[u][q] += red[wave][u * 256 + q * 64 + lane];
+        for (int q = 0; q < 4; ++q) acc[u][q] += red[(wave * U + u) * 256 + q * 64 + lane];
     }
     __syncthreads();
   }
+}
+
+// (three waves a SIMD: at two the loads of one step do not cover the sums)
+template <int NT, bool TALL>
+__global__ __launch_bounds__(kMuThreads, 3) void k_muon_gram(const uint16_t* __restrict__ G, float* __restrict__ M,
+                                                             MuShape s, float mu, int nesterov, int splits,
+                                                             double* __restrict__ part) {
+  constexpr int U = mu_tiles(NT);
+  __shared__ double red[2 * U * 256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t mat = blockIdx.x / splits, base = mat * s.rows * s.cols;
+  f64x4 acc[U];
+  gram_sums<NT, TALL>(G + base, M + base, s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, lane, mu,
+                      nesterov, acc);
+  gram_reduce<NT, 4>(acc, red, wave, lane);
   if (wave == 0) {
     double* out = part + (size_t)blockIdx.x * U * 256;
 #pragma unroll
@@ -336,10 +361,9 @@ struct PolyLds {
 // Two waves per SIMD (one would leave the matrix unit idle over its own LDS
 // traffic) share the tiles in turn; the second of two products that run in one
 // phase starts with the wave at which the first one's tiles ended.
+constexpr int kPolyWaves = 8;
 template <int NT>
-constexpr int kPolyWaves = NT == 2 ? 4 : 8;
-template <int NT>
-constexpr int kPolyTiles = (mu_tiles(NT) + kPolyWaves<NT> - 1) / kPolyWaves<NT>;
+constexpr int kPolyTiles = (mu_tiles(NT) + kPolyWaves - 1) / kPolyWaves;
 
 // Tile e of this wave of the first (turn 0) or second product of a phase.
 struct PolyTile {
@@ -347,7 +371,7 @@ struct PolyTile {
 };
 template <int NT>
 __device__ __forceinline__ PolyTile poly_tile(int turn, int e) {
-  constexpr int W = kPolyWaves<NT>, U = mu_tiles(NT);
+  constexpr int W = kPolyWaves, U = mu_tiles(NT);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int u = (wave + (turn ? W - U % W : 0)) % W + W * e;
   const int t2 = (u >= 1) + (u >= 3) + (u >= 6);
@@ -380,34 +404,19 @@ __device__ __forceinline__ void poly_put(double* m, int i, int k, double v) {
   if ((i ^ k) >> 4) m[PolyLds<NT>::at(k, i)] = v;
 }
 
-// Sum of the splits' partials of tile u, in order.
-__device__ __forceinline__ f64x4 poly_sum(const double* __restrict__ src, int splits, int tiles, int u, int lane) {
-  f64x4 sum = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 8
-  for (int k = 0; k < splits; ++k)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) sum[q] += src[((size_t)k * tiles + u) * 256 + q * 64 + lane];
-  return sum;
+// Short index -> the index (t, i) that the Gram matrix's tiles give it.
+template <int NT, bool TALL>
+__device__ __forceinline__ int poly_index(int e) {
+  return TALL ? (e % NT) * 16 + e / NT : e;
 }
 
-// part -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
+// G (in LDS) -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
 template <int NT, bool TALL>
-__global__ __launch_bounds__(64 * kPolyWaves<NT>) void k_muon_poly(const double* __restrict__ part, int splits,
-                                                                   MuonCoef co, float eps, float* __restrict__ Qout) {
+__device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double* R, const MuonCoef& co, float eps,
+                                         float* out) {
   using At = PolyLds<NT>;
-  constexpr int N = At::N, U = mu_tiles(NT), kThreads = 64 * kPolyWaves<NT>;
-  __shared__ double G[N * N], P[N * N], Q[N * N], R[N * N];
+  constexpr int N = At::N, U = mu_tiles(NT), kThreads = 64 * kPolyWaves;
   const int lane = threadIdx.x & 63;
-  const double* src = part + (size_t)blockIdx.x * splits * U * 256;
-#pragma unroll
-  for (int e = 0; e < kPolyTiles<NT>; ++e) {
-    const PolyTile p = poly_tile<NT>(0, e);
-    if (p.u >= U) break;
-    const f64x4 sum = poly_sum(src, splits, U, p.u, lane);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) poly_put<NT>(G, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
-  }
-  __syncthreads();
   double trace = lane < N ? G[At::at(lane, lane)] : 0.0;
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) trace += __shfl_xor(trace, o, 64);
@@ -442,10 +451,8 @@ __global__ __launch_bounds__(64 * kPolyWaves<NT>) void k_muon_poly(const double*
     if (!last) poly_mul<NT>(0, R, P, [&](int, int i, int k, double v) { poly_put<NT>(G, i, k, v); });
     __syncthreads();
   }
-  // tile index (t, i) -> the short index it stands for
-  auto of = [](int e) { return TALL ? (e % NT) * 16 + e / NT : e; };
-  float* out = Qout + (size_t)blockIdx.x * N * N;
-  for (int e = threadIdx.x; e < N * N; e += kThreads) out[e] = (float)(Q[At::at(of(e / N), of(e % N))] * inv);
+  for (int e = threadIdx.x; e < N * N; e += kThreads)
+    out[e] = (float)(Q[At::at(poly_index<NT, TALL>(e / N), poly_index<NT, TALL>(e % N))] * inv);
 }
 
 // S <= 16: one tile, one wave, no LDS.  The accumulator's register q holds row
@@ -458,16 +465,14 @@ __device__ __forceinline__ f64x4 poly_mul16(const f64x4& x, const f64x4& y) {
   return acc;
 }
 
-__global__ __launch_bounds__(64) void k_muon_poly16(const double* __restrict__ part, int splits, MuonCoef co,
-                                                    float eps, float* __restrict__ Qout) {
-  const int lane = threadIdx.x;
-  f64x4 G = poly_sum(part + (size_t)blockIdx.x * splits * 256, splits, 1, 0, lane);
+__device__ __forceinline__ void poly_run16(f64x4 G, const MuonCoef& co, float eps, float* out, int row, int lane) {
   f64x4 one;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) one[q] = lane / 16 + 4 * q == (lane & 15) ? 1.0 : 0.0;
   double trace = 0.0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) trace += one[q] != 0.0 ? G[q] : 0.0;
+  for (int q = 0; q < 4; ++q) {
+    one[q] = lane / 16 + 4 * q == (lane & 15) ? 1.0 : 0.0;
+    trace += one[q] != 0.0 ? G[q] : 0.0;
+  }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) trace += __shfl_xor(trace, o, 64);
   const double inv = 1.0 / (sqrt(trace) + (double)eps);
@@ -483,7 +488,38 @@ __global__ __launch_bounds__(64) void k_muon_poly16(const double* __restrict__ p
     if (n + 1 < co.n) G = poly_mul16(poly_mul16(P, G), P);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) Qout[(size_t)blockIdx.x * 256 + q * 64 + lane] = (float)(Q[q] * inv);
+  for (int q = 0; q < 4; ++q) out[(lane / 16 + 4 * q) * row + (lane & 15)] = (float)(Q[q] * inv);
+}
+
+// Sum of the partials first, first + stride, ... of tile u, in order.
+__device__ __forceinline__ f64x4 poly_sum(const double* __restrict__ src, int first, int stride, int splits, int tiles,
+                                          int u, int lane) {
+  f64x4 sum = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+  for (int k = first; k < splits; k += stride)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += src[((size_t)k * tiles + u) * 256 + q * 64 + lane];
+  return sum;
+}
+
+// part -> Q / (|u| + eps): N x N, zeros past S.
+template <int NT, bool TALL>
+__global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __restrict__ part, int splits,
+                                                               MuonCoef co, float eps, float* __restrict__ Qout) {
+  constexpr int N = 16 * NT, U = mu_tiles(NT);
+  __shared__ double m[4][N * N];
+  const int lane = threadIdx.x & 63;
+  const double* src = part + (size_t)blockIdx.x * splits * U * 256;
+#pragma unroll
+  for (int e = 0; e < kPolyTiles<NT>; ++e) {
+    const PolyTile p = poly_tile<NT>(0, e);
+    if (p.u >= U) break;
+    const f64x4 sum = poly_sum(src, 0, 1, splits, U, p.u, lane);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) poly_put<NT>(m[0], 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
+  }
+  __syncthreads();
+  poly_run<NT, TALL>(m[0], m[1], m[2], m[3], co, eps, Qout + (size_t)blockIdx.x * N * N);
 }
 
 // -------------------------------------------------------------- pass 2 ----
@@ -510,7 +546,7 @@ struct ApplyShape {
 
 struct ApplyArgs {
   const uint16_t* G;
-  const float* M;
+  float* M;
   float* W;
   uint16_t* P;
   float mu, decay, step;
@@ -524,7 +560,7 @@ __device__ __forceinline__ float mu_weight(const ApplyArgs& a, float w, float x)
 // VEC: all positions of the step exist and, tall, S is a multiple of 4.
 // Loads of rows or short indexes past S are clamped into the matrix: as u they
 // meet the zeros of Q, as weights they are not stored.
-template <int NT, bool VEC>
+template <int NT, bool VEC, bool STREAM>
 __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane,
                                            const float (&qf)[NT][4 * NT]) {
   constexpr int K = ApplyShape<NT, true>::kGroups;
@@ -544,9 +580,9 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
   for (int a = 0; a < K; ++a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      load_f<VEC, 4>(p.M + base(a, t), at(a, t), count(a, t), m[a][t]);
+      load_f<VEC, false, 4>(p.M + base(a, t), at(a, t), count(a, t), m[a][t]);
       load_h<VEC, 4>(p.G + base(a, t), at(a, t), count(a, t), g[a][t]);
-      load_f<VEC, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
+      load_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
   if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);  // all of the step's loads go out first
 #pragma unroll
@@ -564,8 +600,8 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[t][q]);
-      store_f<VEC, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
-      store_bf16<VEC, 4>(p.P + base(a, t), at(a, t), count(a, t), w[a][t]);
+      store_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
+      store_bf16<VEC, STREAM, 4>(p.P + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
   }
 }
@@ -575,7 +611,7 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
 template <int NT>
 constexpr int kQRow = 16 * NT + (NT % 2 == 0 ? 16 : 0);
 
-template <int NT, bool VEC>
+template <int NT, bool VEC, bool STREAM>
 __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs) {
   constexpr int C = ApplyShape<NT, false>::C;
   const int j = j0 + C * (lane & 15);
@@ -594,14 +630,14 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
   };
 #pragma unroll
   for (int k = 0; k < 4 * NT; ++k) {
-    load_f<VEC, C>(p.M + base(4 * k), at(4 * k, lane / 16), nj, m[k]);
+    load_f<VEC, false, C>(p.M + base(4 * k), at(4 * k, lane / 16), nj, m[k]);
     load_h<VEC, C>(p.G + base(4 * k), at(4 * k, lane / 16), nj, g[k]);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      load_f<VEC, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), nj, w[t][q]);
+      load_f<VEC, STREAM, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), nj, w[t][q]);
   // all of the step's loads go out first, and Q stays in LDS from step to step
   if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
@@ -629,43 +665,93 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
       const int n = 16 * t + 4 * (lane / 16) + q < s.S ? nj : 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) w[t][q][c] = mu_weight(p, w[t][q][c], acc[t][c][q]);
-      store_f<VEC, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
-      store_bf16<VEC, C>(p.P + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+      store_f<VEC, STREAM, C>(p.W + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
+      store_bf16<VEC, STREAM, C>(p.P + base(16 * t + q), at(16 * t + q, 4 * (lane / 16)), n, w[t][q]);
     }
 }
 
-template <int NT, bool TALL>
-__global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs p, MuShape s, int splits,
-                                                              const float* __restrict__ Qin) {
-  constexpr int N = 16 * NT, kStep = ApplyShape<NT, TALL>::kStep;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t mat = blockIdx.x / splits, base = mat * s.rows * s.cols;
-  p.G += base;
-  p.M += base;
-  p.W += base;
-  p.P += base;
-  const float* Q = Qin + (size_t)mat * N * N;
-  Steps at(s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, kStep, !TALL || s.S % 4 == 0);
+// All steps of one wave (`wave` of `waves`) over a matrix, Q in LDS.
+template <int NT, bool TALL, bool STREAM>
+__device__ __forceinline__ void apply_steps(const ApplyArgs& p, const MuShape& s, int64_t mat, int wave, int waves,
+                                            int lane, const float* qs) {
+  constexpr int kStep = ApplyShape<NT, TALL>::kStep;
+  Steps at(s, mat, wave, waves, kStep, !TALL || s.S % 4 == 0);
   if constexpr (TALL) {
     float qf[NT][4 * NT];  // of MFMA step 4 s + c, over all of the wave's steps
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 4 * NT; ++k)
-        qf[t][k] = Q[(16 * t + (lane & 15)) * N + 16 * (k / 4) + 4 * (lane / 16) + k % 4];
+        qf[t][k] = qs[(16 * t + (lane & 15)) * kQRow<NT> + 16 * (k / 4) + 4 * (lane / 16) + k % 4];
 #pragma unroll 1
-    for (; at.valid(); at.i += at.stride) apply_tall<NT, true>(p, s, at.j0(at.i), lane, qf);
+    for (; at.valid(); at.i += at.stride) apply_tall<NT, true, STREAM>(p, s, at.j0(at.i), lane, qf);
 #pragma unroll 1
-    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) apply_tall<NT, false>(p, s, (int)j0, lane, qf);
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
+      apply_tall<NT, false, false>(p, s, (int)j0, lane, qf);
   } else {
-    __shared__ float qs[N * kQRow<NT>];
-    for (int e = threadIdx.x; e < N * N; e += kMuThreads) qs[e / N * kQRow<NT> + e % N] = Q[e];
-    __syncthreads();
 #pragma unroll 1
-    for (; at.valid(); at.i += at.stride) apply_wide<NT, true>(p, s, at.j0(at.i), lane, qs);
+    for (; at.valid(); at.i += at.stride) apply_wide<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
 #pragma unroll 1
-    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) apply_wide<NT, false>(p, s, (int)j0, lane, qs);
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
+      apply_wide<NT, false, false>(p, s, (int)j0, lane, qs);
   }
+}
+
+__device__ __forceinline__ ApplyArgs apply_at(ApplyArgs p, int64_t base) {
+  p.G += base;
+  p.M += base;
+  p.W += base;
+  p.P += base;
+  return p;
+}
+
+// With S <= 16 the iteration takes a wave a few microseconds, less than a
+// launch: every work-group runs it for itself, from the partials.
+//
+// The matrices go from the last to the first, whose m and g pass 1 read or
+// wrote longest ago.  STREAM: the stack is larger than half the last-level
+// cache; weights and their copy, touched once, then go past it, and more of m
+// and g is still there (80 x 64 x 8192: 179 us without either, 144 with both;
+// pass 1 of the next call 119 and 108; a stack that fits takes 1 us longer).
+template <int NT, bool TALL, bool STREAM>
+__global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, MuShape s, int splits,
+                                                              const float* __restrict__ Qin,
+                                                              const double* __restrict__ part, int parts, MuonCoef co,
+                                                              float eps) {
+  constexpr int N = 16 * NT;
+  __shared__ float qs[N * kQRow<NT>];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t mat = s.nmat - 1 - blockIdx.x / splits;
+  if constexpr (NT == 1) {
+    __shared__ double red[2 * 256];
+    f64x4 sum[1] = {poly_sum(part + (size_t)mat * parts * 256, wave, 4, parts, 1, 0, lane)};
+    gram_reduce<1, 4>(sum, red, wave, lane);
+    if (wave == 0) poly_run16(sum[0], co, eps, qs, kQRow<1>, lane);
+  } else {
+    const float* Q = Qin + (size_t)mat * N * N;
+    for (int e = threadIdx.x; e < N * N; e += kMuThreads) qs[e / N * kQRow<NT> + e % N] = Q[e];
+  }
+  __syncthreads();
+  apply_steps<NT, TALL, STREAM>(apply_at(args, mat * s.rows * s.cols), s, mat, (int)(blockIdx.x % splits) * 4 + wave,
+                        splits * 4, lane, qs);
+}
+
+// A small matrix of S <= 16 whole: one work-group makes both passes and the
+// iteration, in one launch.  The second pass finds m as the first one left it
+// (the barriers between order the work-group's own stores and loads).
+template <bool TALL>
+__global__ __launch_bounds__(512) void k_muon_whole(ApplyArgs args, MuShape s, MuonCoef co, float eps) {
+  __shared__ double red[4 * 256];
+  __shared__ float qs[16 * kQRow<1>];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t mat = blockIdx.x;
+  const ApplyArgs p = apply_at(args, mat * s.rows * s.cols);
+  f64x4 acc[1];
+  gram_sums<1, TALL>(p.G, p.M, s, mat, wave, 8, lane, p.mu, p.nesterov, acc);
+  gram_reduce<1, 8>(acc, red, wave, lane);
+  if (wave == 0) poly_run16(acc[0], co, eps, qs, kQRow<1>, lane);
+  __syncthreads();
+  apply_steps<1, TALL, false>(p, s, mat, wave, 8, lane, qs);
 }
 
 // ----------------------------------------------------------- launchers ----
@@ -682,31 +768,39 @@ static int mu_splits(const MuShape& s, int all, int per) {
 }
 static int gram_splits(const MuShape& s) { return mu_splits(s, 1024, 256); }
 
+static bool mu_whole(const MuShape& s) { return s.S <= 16 && (int64_t)s.S * s.L <= kMuWhole; }
+
 static size_t mu_part_bytes(const MuShape& s) {
   return (size_t)s.nmat * gram_splits(s) * mu_tiles(mu_nt(s)) * 256 * sizeof(double);
 }
 
 size_t muon_ws_bytes(int64_t nmat, int64_t rows, int64_t cols) {
   const MuShape s = mu_shape(nmat, rows, cols);
+  if (mu_whole(s)) return 0;
   const size_t n = 16 * (size_t)mu_nt(s);
-  return mu_part_bytes(s) + (size_t)nmat * n * n * sizeof(float);
+  return mu_part_bytes(s) + (n > 16 ? (size_t)nmat * n * n * sizeof(float) : 0);
 }
 
 template <int NT, bool TALL>
-static void muon_kernels(uint16_t* P, float* W, const uint16_t* G, float* m, const MuShape& s, float momentum,
-                         int nesterov, float decay, float step, float eps, const MuonCoef& co, double* part, float* Q,
+static void muon_kernels(const ApplyArgs& a, const MuShape& s, float eps, const MuonCoef& co, double* part, float* Q,
                          hipStream_t st) {
+  if constexpr (NT == 1)
+    if (mu_whole(s)) {
+      QLORA_LAUNCH("muon_whole", st, k_muon_whole<TALL>, dim3((unsigned)s.nmat), dim3(512), 0, st, a, s, co, eps);
+      return;
+    }
   const int gs = gram_splits(s), as = mu_splits(s, 512, 4 * ApplyShape<NT, TALL>::kStep);
   const dim3 block(kMuThreads);
-  QLORA_LAUNCH("muon_gram", st, (k_muon_gram<NT, TALL>), dim3((unsigned)(s.nmat * gs)), block, 0, st, G, m, s,
-               momentum, nesterov, gs, part);
-  if constexpr (NT == 1)
-    QLORA_LAUNCH("muon_poly", st, k_muon_poly16, dim3((unsigned)s.nmat), dim3(64), 0, st, part, gs, co, eps, Q);
+  QLORA_LAUNCH("muon_gram", st, (k_muon_gram<NT, TALL>), dim3((unsigned)(s.nmat * gs)), block, 0, st, a.G, a.M, s,
+               a.mu, a.nesterov, gs, part);
+  if constexpr (NT > 1)
+    QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), dim3(64 * kPolyWaves), 0, st, part,
+                 gs, co, eps, Q);
+  const dim3 grid((unsigned)(s.nmat * as));
+  if (14 * s.nmat * s.rows * s.cols > ((int64_t)128 << 20))  // m, g, w and p
+    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, true>), grid, block, 0, st, a, s, as, Q, part, gs, co, eps);
   else
-    QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), dim3(64 * kPolyWaves<NT>), 0, st,
-                 part, gs, co, eps, Q);
-  QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL>), dim3((unsigned)(s.nmat * as)), block, 0, st,
-               ApplyArgs{G, m, W, P, momentum, decay, step, nesterov}, s, as, Q);
+    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, false>), grid, block, 0, st, a, s, as, Q, part, gs, co, eps);
 }
 
 hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t nmat, int64_t rows, int64_t cols,
@@ -715,13 +809,12 @@ hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64
   const MuShape s = mu_shape(nmat, rows, cols);
   double* part = reinterpret_cast<double*>(ws);
   float* Q = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + mu_part_bytes(s));
-  const float decay = (float)(1.0 - (double)lr * wd), step = (float)((double)lr * scale);
-  using Fn = void (*)(uint16_t*, float*, const uint16_t*, float*, const MuShape&, float, int, float, float, float,
-                      const MuonCoef&, double*, float*, hipStream_t);
+  const ApplyArgs a{G, m, W, P, momentum, (float)(1.0 - (double)lr * wd), (float)((double)lr * scale), nesterov};
+  using Fn = void (*)(const ApplyArgs&, const MuShape&, float, const MuonCoef&, double*, float*, hipStream_t);
   static const Fn table[2][4] = {
       {muon_kernels<1, false>, muon_kernels<2, false>, muon_kernels<3, false>, muon_kernels<4, false>},
       {muon_kernels<1, true>, muon_kernels<2, true>, muon_kernels<3, true>, muon_kernels<4, true>}};
-  table[s.tall][mu_nt(s) - 1](P, W, G, m, s, momentum, nesterov, decay, step, eps, co, part, Q, st);
+  table[s.tall][mu_nt(s) - 1](a, s, eps, co, part, Q, st);
   return hipGetLastError();
 }
 

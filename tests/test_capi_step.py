@@ -94,7 +94,7 @@ def test_muon_validation(L):
     P, W, G, m, ws = (p * GB for p in (21, 22, 23, 24, 25))
     F = ctypes.c_float
 
-    def f(P=P, W=W, G=G, m=m, n=2, rows=16, cols=512, lr=1e-3, mu=0.95, wd=0.0, scale=1.0, eps=1e-7, steps=5,
+    def f(P=P, W=W, G=G, m=m, n=2, rows=16, cols=4096, lr=1e-3, mu=0.95, wd=0.0, scale=1.0, eps=1e-7, steps=5,
           coef=None, ws=ws, wsb=1 << 40):
         return L.qlora_muon_step(P, W, G, m, n, rows, cols, lr, mu, 1, wd, scale, eps, steps, coef, ws, wsb, None)
 
@@ -111,8 +111,9 @@ def test_muon_validation(L):
     assert f(ws=None) == E_WS and f(wsb=64) == E_WS
     assert f(m=W + 16) == E_ALIAS and f(P=G) == E_ALIAS and f(ws=G) == E_ALIAS and f(ws=m - 16) == E_ALIAS
     need = L.qlora_muon_workspace_bytes
-    assert need(2, 16, 512) > 0 and need(2, 512, 16) > 0
-    assert need(0, 16, 512) == 0 and need(2, 65, 65) == 0 and need(1, 0, 5) == 0
+    assert need(2, 16, 4096) > 0 and need(2, 4096, 16) > 0
+    assert need(2, 16, 512) == 0 and f(cols=512, ws=None, wsb=0, W=W + 4) == E_ALIGN   # small: none needed
+    assert need(0, 16, 4096) == 0 and need(2, 65, 65) == 0 and need(1, 0, 5) == 0
 
 
 # --------------------------------------------------- the Python forms ----

@@ -428,7 +428,7 @@ def _per(name: str, t, n: int, dtype, device):
     """Pointer of an optional contiguous vector of n values on ``device``."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} is a contiguous vector of {n} {dtype} on {device}")
     return t.data_ptr()
 
@@ -440,7 +440,8 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
         # a padded head's gradient keeps the padding (as zeros), with rows
         # that start where the logits' rows do
         ldd = ld if ld - V < 256 else V
-        return torch.empty((T, ldd), dtype=logits.dtype, device=logits.device)[:, :V], ldd
+        rows = torch.empty((T, ldd), dtype=logits.dtype, device=logits.device)
+        return (rows if ldd == V else rows.narrow(1, 0, V)), ldd
     if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
         raise ValueError("out has the shape, type and device of the logits")
     if V > 1 and out.stride(1) != 1:
@@ -478,13 +479,13 @@ def token_logprobs_backward(dlogp: torch.Tensor, logits: torch.Tensor, labels: t
     dev = logits.device
     g = _per("dlogp", dlogp, T, torch.float32, dev)
     y = _per("labels", labels, T, torch.int32, dev)
-    if stats.shape != (T, 2):
+    if stats.shape != (T, 2) or stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != dev:
         raise ValueError("stats are the T x 2 values that token_logprobs returned")
-    s = _per("stats", stats.view(-1), 2 * T, torch.float32, dev)
     out, ldd = _grad_rows(logits, out, T, V, ld)
     _on_gpu(logits)
     _check(_lib.qlora_token_logprobs_backward(g, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y,
-                                              float(inv_temperature), s, out.data_ptr(), ldd, _stream(dev)),
+                                              float(inv_temperature), stats.data_ptr(), out.data_ptr(), ldd,
+                                              _stream(dev)),
            "qlora_token_logprobs_backward")
     return out
 
@@ -534,7 +535,7 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, advantages: torch.Te
     y = _per("labels", labels, T, torch.int32, dev)
     vec = [_per(n, t, T, torch.float32, dev) for n, t in (("advantages", advantages), ("old_logp", old_logp),
                                                           ("ref_logp", ref_logp), ("weight", weight))]
-    loss, kl, logp = (torch.empty(T, dtype=torch.float32, device=_on_gpu(logits)) for _ in range(3))
+    loss, kl, logp = torch.empty((3, T), dtype=torch.float32, device=_on_gpu(logits)).unbind(0)
     dlogits, ldd = _grad_rows(logits, out, T, V, ld) if need_grad else (None, 0)
     _check(_lib.qlora_policy_loss(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature), *vec,
                                   float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), kl.data_ptr(),

@@ -112,7 +112,7 @@ def test_muon_validation(L):
     assert f(m=W + 16) == E_ALIAS and f(P=G) == E_ALIAS and f(ws=G) == E_ALIAS and f(ws=m - 16) == E_ALIAS
     need = L.qlora_muon_workspace_bytes
     assert need(2, 16, 4096) > 0 and need(2, 4096, 16) > 0
-    assert need(2, 16, 512) == 0 and f(cols=512, ws=None, wsb=0, W=W + 4) == E_ALIGN   # small: none needed
+    assert need(2, 16, 256) == 0 and f(cols=256, ws=None, wsb=0, W=W + 4) == E_ALIGN   # small: none needed
     assert need(0, 16, 4096) == 0 and need(2, 65, 65) == 0 and need(1, 0, 5) == 0
 
 

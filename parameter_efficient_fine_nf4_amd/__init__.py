@@ -414,6 +414,26 @@ def _on_gpu(t: torch.Tensor):
     return t.device
 
 
+def _run(call: str, dev, *args) -> None:
+    """The C call with the tensors' GPU current: a default stream is a GPU's
+    own only while that GPU is."""
+    if torch._C._cuda_getDevice() == dev.index:
+        _check(getattr(_lib, call)(*args, _stream(dev)), call)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(_lib, call)(*args, _stream(dev)), call)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a T x V tensor.  A single row's is the matrix's that it
+    was sliced from, or says nothing."""
+    T, V = t.shape
+    ld = t.stride(0)
+    if T > 1:
+        return ld
+    return ld if V <= ld <= t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() else V
+
+
 def _rows(logits: torch.Tensor):
     """(T, V, row stride) of logits whose rows are contiguous."""
     if logits.dim() != 2 or logits.dtype not in _DTYPES:
@@ -421,7 +441,7 @@ def _rows(logits: torch.Tensor):
     T, V = logits.shape
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of one token have to be contiguous")
-    return T, V, (logits.stride(0) if T > 1 else V)
+    return T, V, _row_stride(logits)
 
 
 def _per(name: str, t, n: int, dtype, device):
@@ -446,7 +466,7 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
         raise ValueError("out has the shape, type and device of the logits")
     if V > 1 and out.stride(1) != 1:
         raise ValueError("the gradient of one token has to be contiguous")
-    ldd = out.stride(0) if T > 1 else V
+    ldd = _row_stride(out)
     room = out.untyped_storage().nbytes() // out.element_size() - out.storage_offset()
     if T * ldd > room:
         raise ValueError("out's last row ends before its stride: the rows are written whole")
@@ -464,8 +484,8 @@ def token_logprobs(logits: torch.Tensor, labels: torch.Tensor, inv_temperature: 
     y = _per("labels", labels, T, torch.int32, dev)
     logp = torch.empty(T, dtype=torch.float32, device=_on_gpu(logits))
     stats = torch.empty((T, 2), dtype=torch.float32, device=dev) if save_stats else None
-    _check(_lib.qlora_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature),
-                                     logp.data_ptr(), _ptr(stats), _stream(dev)), "qlora_token_logprobs")
+    _run("qlora_token_logprobs", dev, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature),
+         logp.data_ptr(), _ptr(stats))
     return (logp, stats) if save_stats else logp
 
 
@@ -483,10 +503,8 @@ def token_logprobs_backward(dlogp: torch.Tensor, logits: torch.Tensor, labels: t
         raise ValueError("stats are the T x 2 values that token_logprobs returned")
     out, ldd = _grad_rows(logits, out, T, V, ld)
     _on_gpu(logits)
-    _check(_lib.qlora_token_logprobs_backward(g, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y,
-                                              float(inv_temperature), stats.data_ptr(), out.data_ptr(), ldd,
-                                              _stream(dev)),
-           "qlora_token_logprobs_backward")
+    _run("qlora_token_logprobs_backward", dev, g, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y,
+         float(inv_temperature), stats.data_ptr(), out.data_ptr(), ldd)
     return out
 
 
@@ -515,9 +533,8 @@ def preference_loss(logp: torch.Tensor, labels: torch.Tensor, vocab: int, cu_seq
     dlogp = None
     if need_grad:  # without a pair there is no loss and nothing is launched
         dlogp = (torch.empty if P else torch.zeros)(T, dtype=torch.float32, device=dev)
-    _check(_lib.qlora_preference_loss(lp, ref, y, T, int(vocab), cu, P, _KINDS[kind], int(average), float(beta),
-                                      float(label_smoothing), float(margin), wt, loss.data_ptr(), reward.data_ptr(),
-                                      _ptr(dlogp), _stream(dev)), "qlora_preference_loss")
+    _run("qlora_preference_loss", dev, lp, ref, y, T, int(vocab), cu, P, _KINDS[kind], int(average), float(beta),
+         float(label_smoothing), float(margin), wt, loss.data_ptr(), reward.data_ptr(), _ptr(dlogp))
     return loss, reward, dlogp
 
 
@@ -537,9 +554,9 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, advantages: torch.Te
                                                           ("ref_logp", ref_logp), ("weight", weight))]
     loss, kl, logp = torch.empty((3, T), dtype=torch.float32, device=_on_gpu(logits)).unbind(0)
     dlogits, ldd = _grad_rows(logits, out, T, V, ld) if need_grad else (None, 0)
-    _check(_lib.qlora_policy_loss(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature), *vec,
-                                  float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), kl.data_ptr(),
-                                  logp.data_ptr(), _ptr(dlogits), ldd, _stream(dev)), "qlora_policy_loss")
+    _run("qlora_policy_loss", dev, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, float(inv_temperature), *vec,
+         float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), kl.data_ptr(), logp.data_ptr(),
+         _ptr(dlogits), ldd)
     return loss, kl, logp, dlogits
 
 
@@ -574,10 +591,9 @@ def muon_step(P: torch.Tensor, W: torch.Tensor, G: torch.Tensor, m: torch.Tensor
     if G.device != dev or any(t.device != dev and not t.is_pinned() for t in (W, m)):
         raise ValueError(f"P and G have to be on one GPU ({dev}), W and m there or in pinned host memory")
     ws = _workspace(_lib.qlora_muon_workspace_bytes(nmat, rows, cols), dev)
-    _check(_lib.qlora_muon_step(P.data_ptr(), W.data_ptr(), G.data_ptr(), m.data_ptr(), nmat, rows, cols, float(lr),
-                                float(momentum), int(nesterov), float(weight_decay), float(scale), float(eps),
-                                int(ns_steps), coef, _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)),
-           "qlora_muon_step")
+    _run("qlora_muon_step", dev, P.data_ptr(), W.data_ptr(), G.data_ptr(), m.data_ptr(), nmat, rows, cols, float(lr),
+         float(momentum), int(nesterov), float(weight_decay), float(scale), float(eps), int(ns_steps), coef, _ptr(ws),
+         0 if ws is None else ws.numel())
 
 
 def merge(w: NF4Weight, A=None, B=None, alpha: float = 0.0, out=None) -> torch.Tensor:

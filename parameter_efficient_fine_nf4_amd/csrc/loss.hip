@@ -11,10 +11,11 @@
 // Exponentials are e_v = 2^(fma(z_v, c, -k)) with c = fl(tau log2 e) and k =
 // fl(c max z): one rounding each, and k's own rounding is the same factor in
 // every e_v and in their sum s, so that p_v = e_v / s is free of it and only
-// ln S takes it back, ln S = ln s + ln 2 (k - c max z), in fp64.  Where |max z|
-// is so large that k could overflow (a row of the type's lowest value) the
-// difference z - max z is taken first.  Sums are fp32 and go through a fixed
-// tree, so results do not depend on the schedule.
+// ln S takes it back, ln S = ln s + ln 2 (k - c max z), in fp64.  From |k| =
+// 2^20 on, where its rounding is no longer a small exponent (and up to where k
+// is infinite, as in a row of the type's lowest value), the difference z - max
+// z is taken first.  Sums are fp32 and go through a fixed tree, so results do
+// not depend on the schedule.
 //
 // A row is a work-group's, read 16 bytes a lane.  Where it fits the work-group's registers it is read once: all of its loads are in
 // flight together, then the maximum, the sum and the gradient follow from the
@@ -120,7 +121,7 @@ struct RowExp {
   float c, k, m;
   bool far;
   __device__ __forceinline__ RowExp(float m_, float c_)
-      : c(c_), k((float)((double)m_ * (double)c_)), m(m_), far(!(fabsf(m_) < 1e30f)) {}
+      : c(c_), k((float)((double)m_ * (double)c_)), m(m_), far(!(fabsf(k) < 1048576.0f)) {}
   __device__ __forceinline__ float near_e(float z) const { return exp2_hw(fmaf(z, c, -k)); }
   __device__ __forceinline__ float far_e(float z) const { return exp2_hw((z - m) * c); }
   __device__ __forceinline__ float e(float z) const { return far ? far_e(z) : near_e(z); }
@@ -375,9 +376,9 @@ struct PolicyArgs {
 };
 
 // exp(d) - 1 - d: below 1/2 in size its series (to d^10 / 10!, 1e-10 of it),
-// since exp(d) - 1 and d would cancel.
+// since exp(d) - 1 and d would cancel; infinite for d = inf.
 __device__ __forceinline__ float exp_less_two_terms(float d, float expm1_d) {
-  if (fabsf(d) >= 0.5f) return expm1_d - d;
+  if (!(fabsf(d) < 0.5f)) return d == __builtin_inff() ? d : expm1_d - d;
   float p = 1.0f / 3628800.0f;
   p = fmaf(p, d, 1.0f / 362880.0f);
   p = fmaf(p, d, 1.0f / 40320.0f);
@@ -622,7 +623,8 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PrefArgs a) {
     loss = x * x;
     dh = 2.0 * x / beta;
   }
-  const double dl = dh * beta * (a.weight != nullptr ? (double)a.weight[p] : 1.0);
+  const double wt = a.weight != nullptr ? (double)a.weight[p] : 1.0;
+  const double dl = wt == 0.0 ? 0.0 : dh * beta * wt;  // a pair taken out has no gradient, not a NaN either
   if (threadIdx.x == 0) {
     a.loss[p] = (float)loss;
     if (a.reward != nullptr) {

@@ -183,6 +183,60 @@ def test_masked_and_extreme_values(lib, V, dtype):
         assert torch.all(lib.token_logprobs_backward(g, z, y, stats, inv_temperature=tau) == 0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [40, 5000, 30000, 150000])
+@pytest.mark.parametrize("size,tau", [(1e6, 1.0), (3e8, 1.0), (1e25, 1.0), (1e3, 1e9), (1.0, 1e12), (1e30, 1e30),
+                                      (1e6, 1e-6), (1.0, 1e-30)])
+def test_large_logits_and_temperatures(lib, V, dtype, size, tau):
+    # exponents far past 2^20, where the maximum's own rounding is a large
+    # exponent; a maximum that the top few share
+    _case("large", V, dtype, size, tau)
+    z, _ = _logits(4, V, dtype, 3)
+    z[1] = z[1].abs() + 1
+    z[3] = 1
+    z[3, : V // 2] = 1 - 2.0 ** -7
+    z = (z.double() * size).to(dtype)
+    z[0, 5:9] = z[0].max()
+    y = torch.tensor([6, 3, V - 1, 1], dtype=torch.int32, device=DEV)
+    tau = float(np.float32(tau))
+    logp, stats = lib.token_logprobs(z, y, inv_temperature=tau, save_stats=True)
+    zh, yh = _f64(z), y.cpu().numpy()
+    with np.errstate(over="ignore"):
+        ref = S.label_logprobs(zh, yh, tau)
+        ref = np.where(np.abs(ref) > 3.4e38, -np.inf, ref)
+    got = _f64(logp)
+    ok = np.isfinite(ref)
+    assert np.array_equal(got[~ok], ref[~ok])
+    tol = _logp_bound(zh[ok], yh[ok], ref[ok], tau)
+    assert np.all(np.abs(got[ok] - ref[ok]) <= tol)
+    g = torch.linspace(0.5, 1, 4).to(DEV)
+    dz = _f64(lib.token_logprobs_backward(g, z, y, stats, inv_temperature=tau))
+    want = S.label_logprobs_grad(zh, yh, _f64(g), tau)
+    keep = ok & (np.abs(want).max(1) < 1e38)
+    bound = np.full(int(keep.sum()), U * (12 * (np.log(V) + 1) + V / 256 + 32))   # of ln S alone
+    assert np.all(np.abs(dz[keep] - want[keep]) <= _grad_bound(want[keep], _f64(g)[keep], tau, bound, dtype))
+    if tau == 1.0:
+        pol = lib.policy_loss(z, y, torch.ones(4, device=DEV))
+        assert torch.equal(pol[2], logp)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_a_single_token_of_a_padded_head(lib, dtype):
+    # one row: the gradient's padding is written as for many
+    z, y = _logits(1, 1000, dtype, 4, ld=1024)
+    logp, stats = lib.token_logprobs(z, y, save_stats=True)
+    dY = torch.full((1, 1024), 3.0, dtype=dtype, device=DEV)
+    d = lib.token_logprobs_backward(torch.ones(1, device=DEV), z, y, stats, out=dY[:, :1000])
+    want = lib.token_logprobs_backward(torch.ones(1, device=DEV), z.contiguous(), y, stats)
+    assert torch.equal(dY[:, :1000], want) and torch.all(dY[:, 1000:] == 0) and torch.equal(d, want)
+    dY.fill_(3.0)
+    lib.policy_loss(z, y, torch.ones(1, device=DEV), out=dY[:, :1000])
+    assert torch.all(dY[:, 1000:] == 0)
+    tight = torch.full((1002,), 3.0, dtype=dtype, device=DEV)
+    lib.token_logprobs_backward(torch.ones(1, device=DEV), z, y, stats, out=tight[:1000].view(1, 1000))
+    assert torch.equal(tight[:1000], want[0]) and torch.all(tight[1000:] == 3)
+
+
 def test_more_than_2_31_elements(lib):
     _case("2^31 elements")
     T, V = 16500, 131072
@@ -270,6 +324,24 @@ def test_preference_of_extreme_margins(lib):
     cu = torch.tensor([4, 5, 6], dtype=torch.int32, device=DEV)
     loss, reward, d = lib.preference_loss(logp, y, 1, cu, 1.0)
     assert loss.item() == float("inf") and d.tolist() == [0, 0, 0, 0, -1.0, 1.0]
+
+
+def test_a_pair_of_weight_zero_has_no_gradient(lib):
+    logp = torch.tensor([-float("inf"), -1.0, -1.0, -2.0], device=DEV)
+    y = torch.zeros(4, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device=DEV)
+    for kind in ("sigmoid", "hinge", "squared"):
+        loss, _, d = lib.preference_loss(logp, y, 1, cu, 0.5, kind=kind, weight=torch.tensor([0.0, 1.0], device=DEV))
+        assert loss[0] == float("inf") and d[0] == 0 and d[2] == 0 and torch.isfinite(d).all()
+
+
+def test_a_label_of_probability_zero_has_infinite_kl(lib):
+    z = torch.zeros(1, 9, device=DEV)
+    z[0, 3] = -float("inf")
+    y = torch.tensor([3], dtype=torch.int32, device=DEV)
+    loss, kl, logp, _ = lib.policy_loss(z, y, torch.ones(1, device=DEV), old_logp=torch.full((1,), -2.0, device=DEV),
+                                        ref_logp=torch.full((1,), -2.0, device=DEV), kl_coef=0.1)
+    assert kl.item() == float("inf") and loss.item() == float("inf") and logp.item() == -float("inf")
 
 
 def test_offsets_out_of_range_are_clamped(lib):

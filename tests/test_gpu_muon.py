@@ -211,3 +211,22 @@ def test_muon_captured_replays_and_streams(lib):
         torch.cuda.synchronize()
         for s, e in zip((a, b), eager):
             assert all(torch.equal(x, y) for x, y in zip(s, e)), rep
+
+
+def test_muon_on_two_streams_at_once(lib):
+    _case("muon streams")
+    shapes = ((2, 64, 2048), (3, 3000, 16), (40, 8, 256))
+    states = [_state(*s, 20 + i) for i, s in enumerate(shapes)]
+    eager = [[t.clone() for t in s] for s in states]
+    for G, m, W, P in eager:
+        for _ in range(3):
+            lib.muon_step(P, W, G, m, lr=0.01)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in shapes]
+    for _ in range(3):
+        for st, (G, m, W, P) in zip(streams, states):
+            with torch.cuda.stream(st):
+                lib.muon_step(P, W, G, m, lr=0.01)
+    torch.cuda.synchronize()
+    for s, e in zip(states, eager):
+        assert all(torch.equal(a, b) for a, b in zip(s, e))

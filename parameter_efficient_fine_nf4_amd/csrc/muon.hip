@@ -195,16 +195,19 @@ struct Steps {
 //   not tall: 8 positions of row 16 t + l % 16 (a row's 32 are a 128-byte
 //             line of m), tile index i of t is row 16 t + i;
 //   tall:     NT consecutive short indexes of 8 long positions 4 apart, tile
-//             index i of t is NT i + t (k_muon_poly undoes the order).
+//             index i of t is NT i + t, or, in the last vector of a row, S -
+//             NT + t (k_muon_poly undoes the order).
 template <int NT, bool TALL>
 struct GramLoad {
   static constexpr int A = TALL ? 8 : NT, B = TALL ? NT : 8;  // A vectors of B consecutive values
   float m[A][B];
   Halves<B> g[A];
 
-  // Vector a of a lane starts at base(a) + lane_at(a) (clamped into the
-  // matrix) and has count(a) values.  VEC: all positions of the step exist
-  // and, tall, S is a multiple of NT, so a vector exists whole or not at all.
+  // Vector a of a lane starts at base(a) + lane_part(a) (clamped into the
+  // matrix) and has count(a) values.  VEC: all positions of the step exist.
+  // Tall, with S not a multiple of NT, the last vector of a row starts NT
+  // before the row's end: its first values (`again` of them) are the vector
+  // before's too, count for nothing in the sums and are stored twice alike.
   template <bool VEC>
   static __device__ __forceinline__ int base(const MuShape& s, int j0, int a) {
     if (TALL) return VEC ? (j0 + 4 * a) * s.S : 0;
@@ -213,7 +216,7 @@ struct GramLoad {
   template <bool VEC>
   static __device__ __forceinline__ uint32_t lane_part(const MuShape& s, int j0, int lane, int a) {
     if (TALL) {
-      const int i = NT * (lane & 15), last = VEC ? s.S - NT : s.S - 1, j = j0 + 4 * a + lane / 16;
+      const int i = NT * (lane & 15), last = s.S - NT, j = j0 + 4 * a + lane / 16;
       return (VEC ? lane / 16 : (j < s.L ? j : s.L - 1)) * s.S + (i < last ? i : last);
     }
     const int i = 16 * a + (lane & 15), j = j0 + 8 * (lane / 16);
@@ -222,12 +225,13 @@ struct GramLoad {
   }
   template <bool VEC>
   static __device__ __forceinline__ int count(const MuShape& s, int j0, int lane, int a) {
-    if (TALL) {
-      const int n = s.S - NT * (lane & 15);
-      return (VEC || j0 + lane / 16 + 4 * a < s.L) && n > 0 ? n : 0;
-    }
+    if (TALL) return NT * (lane & 15) < s.S && (VEC || j0 + lane / 16 + 4 * a < s.L) ? NT : 0;
     if (16 * a + (lane & 15) >= s.S) return 0;
     return VEC ? 8 : room(s.L, j0 + 8 * (lane / 16));
+  }
+  static __device__ __forceinline__ int again(const MuShape& s, int lane) {
+    const int i = NT * (lane & 15);
+    return TALL && i < s.S && i + NT > s.S ? i + NT - s.S : 0;
   }
   template <bool VEC>
   __device__ __forceinline__ void load(const uint16_t* G, const float* M, const MuShape& s, int j0, int lane) {
@@ -243,13 +247,14 @@ struct GramLoad {
   __device__ __forceinline__ void use(float* M, const MuShape& s, int j0, int lane, float mu, int nesterov,
                                       f64x4 (&acc)[mu_tiles(NT)]) {
     float v[A][B];
+    const int dup = again(s, lane);
 #pragma unroll
     for (int a = 0; a < A; ++a) {
       const int n = count<VEC>(s, j0, lane, a);
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         m[a][b] = mu_momentum(m[a][b], g[a].f32(b), mu);
-        v[a][b] = (VEC ? n > 0 : b < n) ? mu_update(m[a][b], g[a].f32(b), mu, nesterov) : 0.0f;
+        v[a][b] = (b < n && b >= dup) ? mu_update(m[a][b], g[a].f32(b), mu, nesterov) : 0.0f;
       }
       store_f<VEC, false, B>(M + base<VEC>(s, j0, a), lane_part<VEC>(s, j0, lane, a), n, m[a]);
     }
@@ -272,8 +277,7 @@ __device__ __forceinline__ void gram_sums(const uint16_t* G, float* M, const MuS
                                           int lane, float mu, int nesterov, f64x4 (&acc)[mu_tiles(NT)]) {
 #pragma unroll
   for (int u = 0; u < mu_tiles(NT); ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
-  // (no step is whole in a tall factor whose S is not a multiple of NT)
-  Steps at(s, mat, wave, waves, 32, !TALL || s.S % NT == 0);
+  Steps at(s, mat, wave, waves, 32, true);
   GramLoad<NT, TALL> x;
 #pragma unroll 1
   for (; at.valid(); at.i += at.stride) {
@@ -404,16 +408,17 @@ __device__ __forceinline__ void poly_put(double* m, int i, int k, double v) {
   if ((i ^ k) >> 4) m[PolyLds<NT>::at(k, i)] = v;
 }
 
-// Short index -> the index (t, i) that the Gram matrix's tiles give it.
+// Short index -> the index 16 t + i that the Gram matrix's tiles give it.
 template <int NT, bool TALL>
-__device__ __forceinline__ int poly_index(int e) {
-  return TALL ? (e % NT) * 16 + e / NT : e;
+__device__ __forceinline__ int poly_index(int e, int S) {
+  if (!TALL) return e;
+  return e < S / NT * NT ? e % NT * 16 + e / NT : (e - (S - NT)) * 16 + S / NT;
 }
 
 // G (in LDS) -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
 template <int NT, bool TALL>
 __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double* R, const MuonCoef& co, float eps,
-                                         float* out) {
+                                         float* out, int S) {
   using At = PolyLds<NT>;
   constexpr int N = At::N, U = mu_tiles(NT), kThreads = 64 * kPolyWaves;
   const int lane = threadIdx.x & 63;
@@ -451,8 +456,10 @@ __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double
     if (!last) poly_mul<NT>(0, R, P, [&](int, int i, int k, double v) { poly_put<NT>(G, i, k, v); });
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < N * N; e += kThreads)
-    out[e] = (float)(Q[At::at(poly_index<NT, TALL>(e / N), poly_index<NT, TALL>(e % N))] * inv);
+  for (int e = threadIdx.x; e < N * N; e += kThreads) {
+    const int i = e / N, k = e % N;
+    out[e] = i < S && k < S ? (float)(Q[At::at(poly_index<NT, TALL>(i, S), poly_index<NT, TALL>(k, S))] * inv) : 0.0f;
+  }
 }
 
 // S <= 16: one tile, one wave, no LDS.  The accumulator's register q holds row
@@ -465,7 +472,7 @@ __device__ __forceinline__ f64x4 poly_mul16(const f64x4& x, const f64x4& y) {
   return acc;
 }
 
-__device__ __forceinline__ void poly_run16(f64x4 G, const MuonCoef& co, float eps, float* out, int row, int lane) {
+__device__ __forceinline__ void poly_run16(f64x4 G, const MuonCoef& co, float eps, float* out, int S, int lane) {
   f64x4 one;
   double trace = 0.0;
 #pragma unroll
@@ -488,38 +495,60 @@ __device__ __forceinline__ void poly_run16(f64x4 G, const MuonCoef& co, float ep
     if (n + 1 < co.n) G = poly_mul16(poly_mul16(P, G), P);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) out[(lane / 16 + 4 * q) * row + (lane & 15)] = (float)(Q[q] * inv);
+  for (int q = 0; q < 4; ++q)
+    out[64 * q + lane] = lane / 16 + 4 * q < S && (lane & 15) < S ? (float)(Q[q] * inv) : 0.0f;
 }
 
-// Sum of the partials first, first + stride, ... of tile u, in order.
-__device__ __forceinline__ f64x4 poly_sum(const double* __restrict__ src, int first, int stride, int splits, int tiles,
-                                          int u, int lane) {
-  f64x4 sum = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 8
-  for (int k = first; k < splits; k += stride)
+// A wave's share of the sum of the splits' partials.
+__device__ __forceinline__ f64x4 poly_sum16(const double* __restrict__ src, int wave, int splits, int lane) {
+  f64x4 sum = {0.0, 0.0, 0.0, 0.0}, v[8];  // at most 32 partials: all of them in flight
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum[q] += src[((size_t)k * tiles + u) * 256 + q * 64 + lane];
+  for (int j = 0; j < 8; ++j) {
+    v[j] = f64x4{0.0, 0.0, 0.0, 0.0};
+    if (wave + 4 * j < splits)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j][q] = src[(size_t)(wave + 4 * j) * 256 + q * 64 + lane];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum += v[j];
   return sum;
 }
 
 // part -> Q / (|u| + eps): N x N, zeros past S.
 template <int NT, bool TALL>
-__global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __restrict__ part, int splits,
+__global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __restrict__ part, int splits, int S,
                                                                MuonCoef co, float eps, float* __restrict__ Qout) {
   constexpr int N = 16 * NT, U = mu_tiles(NT);
   __shared__ double m[4][N * N];
-  const int lane = threadIdx.x & 63;
+  // the partials' sum, in order, four partials' loads in flight for every
+  // element of a thread
+  constexpr int kThreads = 64 * kPolyWaves, E = (U * 256 + kThreads - 1) / kThreads;
   const double* src = part + (size_t)blockIdx.x * splits * U * 256;
+  double sum[E] = {};
+#pragma unroll 1
+  for (int k = 0; k < splits; k += 4) {
+    double v[4][E];
 #pragma unroll
-  for (int e = 0; e < kPolyTiles<NT>; ++e) {
-    const PolyTile p = poly_tile<NT>(0, e);
-    if (p.u >= U) break;
-    const f64x4 sum = poly_sum(src, 0, 1, splits, U, p.u, lane);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) poly_put<NT>(m[0], 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), sum[q]);
+      for (int e = 0; e < E; ++e) {
+        const int at = e * kThreads + threadIdx.x;
+        v[j][e] = 0.0;
+        if (k + j < splits && at < U * 256) v[j][e] = src[(size_t)(k + j) * U * 256 + at];
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += v[j][e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int at = e * kThreads + threadIdx.x;
+    const int u = at / 256, q = at / 64 % 4, lane = at % 64, t2 = (u >= 1) + (u >= 3) + (u >= 6);
+    if (u < U) poly_put<NT>(m[0], 16 * (u - t2 * (t2 + 1) / 2) + lane / 16 + 4 * q, 16 * t2 + (lane & 15), sum[e]);
   }
   __syncthreads();
-  poly_run<NT, TALL>(m[0], m[1], m[2], m[3], co, eps, Qout + (size_t)blockIdx.x * N * N);
+  poly_run<NT, TALL>(m[0], m[1], m[2], m[3], co, eps, Qout + (size_t)blockIdx.x * N * N, S);
 }
 
 // -------------------------------------------------------------- pass 2 ----
@@ -534,15 +563,41 @@ __global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __r
 //             and D gives it the same C positions of rows 16 t + 4 (l / 16) + q;
 //   tall:     lane l has short indexes 16 s + 4 (l / 16) + c of position l % 16,
 //             so that k of MFMA (s, c) is 16 s + 4 (l / 16) + c, and D gives it
-//             short indexes 16 t + 4 (l / 16) + q of that position.
+//             short indexes 16 t + 4 (l / 16) + q of that position.  With S
+//             not a multiple of 4 a position's last four overlap the four
+//             before: D repeats them, and as k they count once (put_q).
+//
+// Q is in LDS (64 x 64 of it would take the registers of the loads in flight),
+// in rows of a stride that puts an operand's four rows, next to each other or
+// four apart, into four sets of banks.
 template <int NT, bool TALL>
 struct ApplyShape {
   // positions per lane (not tall) or 16-position groups per step (tall): as
   // much in flight as two waves' share of the registers holds
-  static constexpr int C = TALL ? 4 : (NT >= 3 ? 2 : 4);
-  static constexpr int kGroups = TALL ? (NT == 1 ? 4 : NT == 2 ? 2 : 1) : 1;
-  static constexpr int kStep = TALL ? 16 * kGroups : 16 * C;
+  static constexpr int C = NT >= 3 ? 2 : 4;
+  static constexpr int kStep = 16 * C;
+  static constexpr int kQRow = 16 * NT + (TALL ? 4 : NT % 2 == 0 ? 16 : 0);
 };
+
+// Q (N x N, zeros past S) into an operand's place.
+template <int NT, bool TALL>
+__device__ __forceinline__ void put_q(const float* Q, float* qs, int S, int threads) {
+  constexpr int N = 16 * NT;
+  const int whole = S & ~3, last = S - 4;  // the last four begin at `last`, in the place of `whole`
+  const bool shifted = TALL && S > 4 && whole < S;
+  for (int e = threadIdx.x; e < N * N; e += threads) {
+    int k = e / N, i = e % N;  // Q is symmetric; the operand is read by rows of k
+    bool count = true;
+    if (shifted) {
+      if (k >= whole) {
+        k = k < whole + 4 ? k - whole + last : N;
+        count = k >= whole && k < N;
+      }
+      if (i >= whole) i = i < whole + 4 ? i - whole + last : 0;
+    }
+    qs[e / N * ApplyShape<NT, TALL>::kQRow + e % N] = count ? Q[i * N + k] : 0.0f;
+  }
+}
 
 struct ApplyArgs {
   const uint16_t* G;
@@ -557,24 +612,27 @@ __device__ __forceinline__ float mu_weight(const ApplyArgs& a, float w, float x)
   return __fsub_rn(__fmul_rn(w, a.decay), __fmul_rn(a.step, x));
 }
 
-// VEC: all positions of the step exist and, tall, S is a multiple of 4.
-// Loads of rows or short indexes past S are clamped into the matrix: as u they
-// meet the zeros of Q, as weights they are not stored.
+// VEC: all positions of the step exist and, tall, S >= 4.  Loads of rows or
+// short indexes past S are clamped into the matrix: as u they meet zeros of Q,
+// as weights they are not stored.
 template <int NT, bool VEC, bool STREAM>
-__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane,
-                                           const float (&qf)[NT][4 * NT]) {
-  constexpr int K = ApplyShape<NT, true>::kGroups;
+__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs) {
+  constexpr int K = ApplyShape<NT, true>::C;
   float m[K][NT][4], w[K][NT][4];
   Halves<4> g[K][NT];
-  auto base = [&](int a, int t) { return VEC ? (j0 + 16 * a) * s.S + 16 * t : 0; };
+  // (the last tile's base is clamped on its own, so that a lane's offset from
+  // it is never negative)
+  const int last = VEC || s.S >= 4 ? s.S - 4 : 0;
+  auto tile0 = [&](int t) { return t < NT - 1 || 16 * t < last ? 16 * t : last; };
+  auto base = [&](int a, int t) { return VEC ? (j0 + 16 * a) * s.S + tile0(t) : 0; };
   auto at = [&](int a, int t) -> uint32_t {
-    const int i = 16 * t + 4 * (lane / 16), last = VEC ? s.S - 4 : s.S - 1, j = j0 + 16 * a + (lane & 15);
-    if (VEC) return (lane & 15) * s.S + (t < NT - 1 || i < last ? i : last) - 16 * t;
+    const int i = 16 * t + 4 * (lane / 16), j = j0 + 16 * a + (lane & 15);
+    if (VEC) return (lane & 15) * s.S + (t < NT - 1 || i < last ? i : last) - tile0(t);
     return (j < s.L ? j : s.L - 1) * s.S + (i < last ? i : last);
   };
   auto count = [&](int a, int t) {
-    const int n = s.S - 16 * t - 4 * (lane / 16);
-    return VEC || j0 + 16 * a + (lane & 15) < s.L ? n : 0;
+    if (16 * t + 4 * (lane / 16) >= s.S || (!VEC && j0 + 16 * a + (lane & 15) >= s.L)) return 0;
+    return VEC || s.S >= 4 ? 4 : s.S;
   };
 #pragma unroll
   for (int a = 0; a < K; ++a)
@@ -585,31 +643,35 @@ __device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s,
       load_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
   if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);  // all of the step's loads go out first
+  asm volatile("" ::: "memory");                         // and Q stays in LDS from step to step
+  f32x4 acc[K][NT];
 #pragma unroll
-  for (int a = 0; a < K; ++a) {
-    f32x4 acc[NT];
+  for (int a = 0; a < K; ++a)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < NT; ++t) acc[a][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < 4 * NT; ++k) {
+  for (int k = 0; k < 4 * NT; ++k) {
+    float q[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      q[t] = qs[(16 * (k / 4) + 4 * (lane / 16) + k % 4) * ApplyShape<NT, true>::kQRow + 16 * t + (lane & 15)];
+#pragma unroll
+    for (int a = 0; a < K; ++a) {
       const float u = mu_update(m[a][k / 4][k % 4], g[a][k / 4].f32(k % 4), p.mu, p.nesterov);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = mfma_f32(qf[t][k], u, acc[t]);
+      for (int t = 0; t < NT; ++t) acc[a][t] = mfma_f32(q[t], u, acc[a][t]);
     }
+  }
+#pragma unroll
+  for (int a = 0; a < K; ++a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[t][q]);
+      for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[a][t][q]);
       store_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
       store_bf16<VEC, STREAM, 4>(p.P + base(a, t), at(a, t), count(a, t), w[a][t]);
     }
-  }
 }
-
-// Q in LDS (64 x 64 of it would take the registers of the loads in flight):
-// row strides that put the four rows of an operand into four sets of banks.
-template <int NT>
-constexpr int kQRow = 16 * NT + (NT % 2 == 0 ? 16 : 0);
 
 template <int NT, bool VEC, bool STREAM>
 __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs) {
@@ -650,7 +712,7 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
   for (int k = 0; k < 4 * NT; ++k) {
     float q[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) q[t] = qs[(4 * k + lane / 16) * kQRow<NT> + 16 * t + (lane & 15)];
+    for (int t = 0; t < NT; ++t) q[t] = qs[(4 * k + lane / 16) * ApplyShape<NT, false>::kQRow + 16 * t + (lane & 15)];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const float u = mu_update(m[k][c], g[k].f32(c), p.mu, p.nesterov);
@@ -670,29 +732,24 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
     }
 }
 
-// All steps of one wave (`wave` of `waves`) over a matrix, Q in LDS.
+// All steps of one wave (`wave` of `waves`) over a matrix.
 template <int NT, bool TALL, bool STREAM>
 __device__ __forceinline__ void apply_steps(const ApplyArgs& p, const MuShape& s, int64_t mat, int wave, int waves,
                                             int lane, const float* qs) {
   constexpr int kStep = ApplyShape<NT, TALL>::kStep;
-  Steps at(s, mat, wave, waves, kStep, !TALL || s.S % 4 == 0);
-  if constexpr (TALL) {
-    float qf[NT][4 * NT];  // of MFMA step 4 s + c, over all of the wave's steps
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 4 * NT; ++k)
-        qf[t][k] = qs[(16 * t + (lane & 15)) * kQRow<NT> + 16 * (k / 4) + 4 * (lane / 16) + k % 4];
+  Steps at(s, mat, wave, waves, kStep, !TALL || s.S >= 4);
 #pragma unroll 1
-    for (; at.valid(); at.i += at.stride) apply_tall<NT, true, STREAM>(p, s, at.j0(at.i), lane, qf);
+  for (; at.valid(); at.i += at.stride) {
+    if constexpr (TALL)
+      apply_tall<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
+    else
+      apply_wide<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
+  }
 #pragma unroll 1
-    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
-      apply_tall<NT, false, false>(p, s, (int)j0, lane, qf);
-  } else {
-#pragma unroll 1
-    for (; at.valid(); at.i += at.stride) apply_wide<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
-#pragma unroll 1
-    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
+  for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) {
+    if constexpr (TALL)
+      apply_tall<NT, false, false>(p, s, (int)j0, lane, qs);
+    else
       apply_wide<NT, false, false>(p, s, (int)j0, lane, qs);
   }
 }
@@ -719,21 +776,23 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
                                                               const double* __restrict__ part, int parts, MuonCoef co,
                                                               float eps) {
   constexpr int N = 16 * NT;
-  __shared__ float qs[N * kQRow<NT>];
+  __shared__ float qs[N * ApplyShape<NT, TALL>::kQRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = s.nmat - 1 - blockIdx.x / splits;
   if constexpr (NT == 1) {
     __shared__ double red[2 * 256];
-    f64x4 sum[1] = {poly_sum(part + (size_t)mat * parts * 256, wave, 4, parts, 1, 0, lane)};
+    __shared__ float Q[256];
+    f64x4 sum[1] = {poly_sum16(part + (size_t)mat * parts * 256, wave, parts, lane)};
     gram_reduce<1, 4>(sum, red, wave, lane);
-    if (wave == 0) poly_run16(sum[0], co, eps, qs, kQRow<1>, lane);
+    if (wave == 0) poly_run16(sum[0], co, eps, Q, s.S, lane);
+    __syncthreads();
+    put_q<1, TALL>(Q, qs, s.S, kMuThreads);
   } else {
-    const float* Q = Qin + (size_t)mat * N * N;
-    for (int e = threadIdx.x; e < N * N; e += kMuThreads) qs[e / N * kQRow<NT> + e % N] = Q[e];
+    put_q<NT, TALL>(Qin + (size_t)mat * N * N, qs, s.S, kMuThreads);
   }
   __syncthreads();
   apply_steps<NT, TALL, STREAM>(apply_at(args, mat * s.rows * s.cols), s, mat, (int)(blockIdx.x % splits) * 4 + wave,
-                        splits * 4, lane, qs);
+                                splits * 4, lane, qs);
 }
 
 // A small matrix of S <= 16 whole: one work-group makes both passes and the
@@ -742,14 +801,16 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
 template <bool TALL>
 __global__ __launch_bounds__(512) void k_muon_whole(ApplyArgs args, MuShape s, MuonCoef co, float eps) {
   __shared__ double red[4 * 256];
-  __shared__ float qs[16 * kQRow<1>];
+  __shared__ float Q[256], qs[16 * ApplyShape<1, TALL>::kQRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = blockIdx.x;
   const ApplyArgs p = apply_at(args, mat * s.rows * s.cols);
   f64x4 acc[1];
   gram_sums<1, TALL>(p.G, p.M, s, mat, wave, 8, lane, p.mu, p.nesterov, acc);
   gram_reduce<1, 8>(acc, red, wave, lane);
-  if (wave == 0) poly_run16(acc[0], co, eps, qs, kQRow<1>, lane);
+  if (wave == 0) poly_run16(acc[0], co, eps, Q, s.S, lane);
+  __syncthreads();
+  put_q<1, TALL>(Q, qs, s.S, 512);
   __syncthreads();
   apply_steps<1, TALL, false>(p, s, mat, wave, 8, lane, qs);
 }
@@ -766,7 +827,12 @@ static int mu_splits(const MuShape& s, int all, int per) {
   if (n > most) n = most;
   return (int)(n < 1 ? 1 : n);
 }
-static int gram_splits(const MuShape& s) { return mu_splits(s, 1024, 256); }
+// The Gram pass's partials (2 to 20 KB, by S) are read again by the one
+// work-group that sums them: at most 32 a matrix.
+static int gram_splits(const MuShape& s) {
+  const int n = mu_splits(s, 1024, 256);
+  return n < 32 ? n : 32;
+}
 
 static bool mu_whole(const MuShape& s) { return s.S <= 16 && (int64_t)s.S * s.L <= kMuWhole; }
 
@@ -795,7 +861,7 @@ static void muon_kernels(const ApplyArgs& a, const MuShape& s, float eps, const 
                a.mu, a.nesterov, gs, part);
   if constexpr (NT > 1)
     QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), dim3(64 * kPolyWaves), 0, st, part,
-                 gs, co, eps, Q);
+                 gs, s.S, co, eps, Q);
   const dim3 grid((unsigned)(s.nmat * as));
   if (14 * s.nmat * s.rows * s.cols > ((int64_t)128 << 20))  // m, g, w and p
     QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, true>), grid, block, 0, st, a, s, as, Q, part, gs, co, eps);

@@ -77,7 +77,10 @@ def _check(G, m0, W0, P, W, m, *, lr, mu=0.95, nesterov=True, wd=0.0, coef=(S.US
 SHAPES = [(1, 1, 1), (2, 1, 64), (1, 64, 1), (3, 2, 3), (1, 8, 256), (2, 256, 8), (3, 7, 1001), (3, 1001, 7),
           (2, 15, 129), (2, 129, 15), (2, 16, 4096), (2, 4096, 16), (2, 17, 640), (2, 640, 17), (1, 32, 4160),
           (2, 33, 130), (2, 130, 33), (1, 48, 1000), (1, 1000, 48), (1, 63, 65), (1, 65, 63), (2, 64, 64),
-          (2, 64, 8192), (1, 11008, 64), (5, 11008, 16), (40, 16, 300), (1, 60, 22016), (300, 4, 64)]
+          (2, 64, 8192), (1, 11008, 64), (5, 11008, 16), (40, 16, 300), (1, 60, 22016), (300, 4, 64),
+          # tall, with a rank that no vector divides
+          (3, 5000, 1), (3, 5000, 2), (3, 5000, 3), (3, 5001, 5), (2, 5000, 6), (2, 2003, 13), (2, 700, 19),
+          (2, 2001, 31), (2, 700, 35), (2, 1300, 47), (2, 700, 50), (2, 1111, 53), (1, 900, 61), (70, 333, 62)]
 
 
 @pytest.mark.parametrize("n,rows,cols", SHAPES)

@@ -561,11 +561,13 @@ __global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __r
 //
 //   not tall: lane l has C positions C (l % 16) + c of row k = 4 s + l / 16,
 //             and D gives it the same C positions of rows 16 t + 4 (l / 16) + q;
-//   tall:     lane l has short indexes 16 s + 4 (l / 16) + c of position l % 16,
-//             so that k of MFMA (s, c) is 16 s + 4 (l / 16) + c, and D gives it
-//             short indexes 16 t + 4 (l / 16) + q of that position.  With S
-//             not a multiple of 4 a position's last four overlap the four
-//             before: D repeats them, and as k they count once (put_q).
+//   tall:     a step's positions are one run of memory, which the lanes load
+//             and store in consecutive fours whatever S is; u and X change
+//             between that order and the operands' (k of MFMA (s, c) is 16 s +
+//             4 (l / 16) + c of position l % 16; D: short indexes 16 t + 4 (l /
+//             16) + q of that position) in LDS of the wave's own.  Loaded in
+//             the operands' order, rows of 64 took 222 us where this takes
+//             133 (80 x 8192 x 64).
 //
 // Q is in LDS (64 x 64 of it would take the registers of the loads in flight),
 // in rows of a stride that puts an operand's four rows, next to each other or
@@ -577,26 +579,14 @@ struct ApplyShape {
   static constexpr int C = NT >= 3 ? 2 : 4;
   static constexpr int kStep = 16 * C;
   static constexpr int kQRow = 16 * NT + (TALL ? 4 : NT % 2 == 0 ? 16 : 0);
+  static constexpr int kScratch = TALL ? kStep * (16 * NT + 4) : 0;  // floats of a wave
 };
 
-// Q (N x N, zeros past S) into an operand's place.
+// Q (N x N) into an operand's place.
 template <int NT, bool TALL>
-__device__ __forceinline__ void put_q(const float* Q, float* qs, int S, int threads) {
+__device__ __forceinline__ void put_q(const float* Q, float* qs, int threads) {
   constexpr int N = 16 * NT;
-  const int whole = S & ~3, last = S - 4;  // the last four begin at `last`, in the place of `whole`
-  const bool shifted = TALL && S > 4 && whole < S;
-  for (int e = threadIdx.x; e < N * N; e += threads) {
-    int k = e / N, i = e % N;  // Q is symmetric; the operand is read by rows of k
-    bool count = true;
-    if (shifted) {
-      if (k >= whole) {
-        k = k < whole + 4 ? k - whole + last : N;
-        count = k >= whole && k < N;
-      }
-      if (i >= whole) i = i < whole + 4 ? i - whole + last : 0;
-    }
-    qs[e / N * ApplyShape<NT, TALL>::kQRow + e % N] = count ? Q[i * N + k] : 0.0f;
-  }
+  for (int e = threadIdx.x; e < N * N; e += threads) qs[e / N * ApplyShape<NT, TALL>::kQRow + e % N] = Q[e];
 }
 
 struct ApplyArgs {
@@ -612,65 +602,131 @@ __device__ __forceinline__ float mu_weight(const ApplyArgs& a, float w, float x)
   return __fsub_rn(__fmul_rn(w, a.decay), __fmul_rn(a.step, x));
 }
 
-// VEC: all positions of the step exist and, tall, S >= 4.  Loads of rows or
-// short indexes past S are clamped into the matrix: as u they meet zeros of Q,
-// as weights they are not stored.
-template <int NT, bool VEC, bool STREAM>
-__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs) {
-  constexpr int K = ApplyShape<NT, true>::C;
-  float m[K][NT][4], w[K][NT][4];
-  Halves<4> g[K][NT];
-  // (the last tile's base is clamped on its own, so that a lane's offset from
-  // it is never negative)
-  const int last = VEC || s.S >= 4 ? s.S - 4 : 0;
-  auto tile0 = [&](int t) { return t < NT - 1 || 16 * t < last ? 16 * t : last; };
-  auto base = [&](int a, int t) { return VEC ? (j0 + 16 * a) * s.S + tile0(t) : 0; };
-  auto at = [&](int a, int t) -> uint32_t {
-    const int i = 16 * t + 4 * (lane / 16), j = j0 + 16 * a + (lane & 15);
-    if (VEC) return (lane & 15) * s.S + (t < NT - 1 || i < last ? i : last) - tile0(t);
-    return (j < s.L ? j : s.L - 1) * s.S + (i < last ? i : last);
-  };
-  auto count = [&](int a, int t) {
-    if (16 * t + 4 * (lane / 16) >= s.S || (!VEC && j0 + 16 * a + (lane & 15) >= s.L)) return 0;
-    return VEC || s.S >= 4 ? 4 : s.S;
-  };
+// The LDS of a wave in the tall form: a row of S + pad floats a position.  Pad
+// makes the stride an odd number of 16-byte slots where S is a multiple of 4
+// (a quarter wave then reads its 16 positions' slots without a conflict);
+// other strides are read and written by single values.
+template <int NT>
+struct TallLds {
+  static constexpr int E = ApplyShape<NT, true>::C * NT;  // fours a lane
+  float* lds;
+  int S, row, fours;
+  bool quads;
+  int off[E];  // of the lane's fours in LDS
+
+  __device__ __forceinline__ TallLds(float* lds_, int S_, int lane)
+      : lds(lds_), S(S_), row(S_ + (S_ % 8 == 0 ? 4 : 0)), fours(ApplyShape<NT, true>::kStep / 4 * S_),
+        quads(S_ % 4 == 0) {
 #pragma unroll
-  for (int a = 0; a < K; ++a)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      load_f<VEC, false, 4>(p.M + base(a, t), at(a, t), count(a, t), m[a][t]);
-      load_h<VEC, 4>(p.G + base(a, t), at(a, t), count(a, t), g[a][t]);
-      load_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
+    for (int e = 0; e < E; ++e) {
+      const int at = 4 * four(e, lane);
+      off[e] = row == S ? at : at + 4 * (at / S);
     }
+  }
+  __device__ __forceinline__ int four(int e, int lane) const {
+    const int f = lane + 64 * e;
+    return f < fours ? f : fours - 1;
+  }
+  __device__ __forceinline__ void get4(int e, float (&v)[4]) const {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(lds + off[e]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = x[c];
+  }
+  __device__ __forceinline__ void put4(int e, const float (&v)[4]) const {
+    *reinterpret_cast<f32x4*>(lds + off[e]) = f32x4{v[0], v[1], v[2], v[3]};
+  }
+  // four of a position from short index i on; past S any finite ones (they
+  // meet zeros of Q)
+  __device__ __forceinline__ f32x4 get(int pos, int i) const {
+    const float* p = lds + pos * row;
+    if (quads) return *reinterpret_cast<const f32x4*>(p + (i < S ? i : S - 4));
+    f32x4 v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = p[i + c < S ? i + c : S - 1];
+    return v;
+  }
+  __device__ __forceinline__ void put(int pos, int i, const f32x4& v) const {
+    float* p = lds + pos * row;
+    if (quads) {
+      if (i < S) *reinterpret_cast<f32x4*>(p + i) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (i + c < S) p[i + c] = v[c];
+    }
+  }
+};
+
+// The wave's own LDS accesses take effect in order; this keeps the compiler to
+// it across lanes.
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// VEC: all positions of the step exist.
+template <int NT, bool VEC, bool STREAM>
+__device__ __forceinline__ void apply_tall(const ApplyArgs& p, const MuShape& s, int j0, int lane, const float* qs,
+                                           const TallLds<NT>& x) {
+  constexpr int K = ApplyShape<NT, true>::C, E = TallLds<NT>::E;
+  const int first = j0 * s.S, there = (s.L - j0) * s.S;  // elements from the step's first on
+  float m[E][4], w[E][4];
+  Halves<4> g[E];
+  auto at = [&](int e) { return (uint32_t)(VEC ? 4 * x.four(e, lane) : min(4 * x.four(e, lane), there - 1)); };
+  auto count = [&](int e) { return VEC ? 4 : room(there, 4 * x.four(e, lane)); };
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    load_f<VEC, false, 4>(p.M + first, at(e), count(e), m[e]);
+    load_h<VEC, 4>(p.G + first, at(e), count(e), g[e]);
+    load_f<VEC, STREAM, 4>(p.W + first, at(e), count(e), w[e]);
+  }
   if constexpr (VEC) __builtin_amdgcn_sched_barrier(0);  // all of the step's loads go out first
-  asm volatile("" ::: "memory");                         // and Q stays in LDS from step to step
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float u[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) u[c] = mu_update(m[e][c], g[e].f32(c), p.mu, p.nesterov);
+    x.put4(e, u);
+  }
+  wave_lds_order();
   f32x4 acc[K][NT];
 #pragma unroll
   for (int a = 0; a < K; ++a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[a][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 4 * NT; ++k) {
-    float q[NT];
+  for (int k4 = 0; k4 < NT; ++k4) {
+    f32x4 u[K];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      q[t] = qs[(16 * (k / 4) + 4 * (lane / 16) + k % 4) * ApplyShape<NT, true>::kQRow + 16 * t + (lane & 15)];
+    for (int a = 0; a < K; ++a) u[a] = x.get(16 * a + (lane & 15), 16 * k4 + 4 * (lane / 16));
 #pragma unroll
-    for (int a = 0; a < K; ++a) {
-      const float u = mu_update(m[a][k / 4][k % 4], g[a][k / 4].f32(k % 4), p.mu, p.nesterov);
+    for (int c = 0; c < 4; ++c) {
+      float q[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[a][t] = mfma_f32(q[t], u, acc[a][t]);
+      for (int t = 0; t < NT; ++t)
+        q[t] = qs[(16 * k4 + 4 * (lane / 16) + c) * ApplyShape<NT, true>::kQRow + 16 * t + (lane & 15)];
+#pragma unroll
+      for (int a = 0; a < K; ++a)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[a][t] = mfma_f32(q[t], u[a][c], acc[a][t]);
     }
   }
+  wave_lds_order();
 #pragma unroll
   for (int a = 0; a < K; ++a)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t) x.put(16 * a + (lane & 15), 16 * t + 4 * (lane / 16), acc[a][t]);
+  wave_lds_order();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[a][t][q] = mu_weight(p, w[a][t][q], acc[a][t][q]);
-      store_f<VEC, STREAM, 4>(p.W + base(a, t), at(a, t), count(a, t), w[a][t]);
-      store_bf16<VEC, STREAM, 4>(p.P + base(a, t), at(a, t), count(a, t), w[a][t]);
-    }
+  for (int e = 0; e < E; ++e) {
+    float o[4];
+    x.get4(e, o);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[e][c] = mu_weight(p, w[e][c], o[c]);
+    store_f<VEC, STREAM, 4>(p.W + first, at(e), count(e), w[e]);
+    store_bf16<VEC, STREAM, 4>(p.P + first, at(e), count(e), w[e]);
+  }
+  wave_lds_order();
 }
 
 template <int NT, bool VEC, bool STREAM>
@@ -732,24 +788,25 @@ __device__ __forceinline__ void apply_wide(const ApplyArgs& p, const MuShape& s,
     }
 }
 
-// All steps of one wave (`wave` of `waves`) over a matrix.
+// All steps of one wave (`wave` of `waves`) over a matrix.  scratch: kScratch
+// floats of the wave's own.
 template <int NT, bool TALL, bool STREAM>
 __device__ __forceinline__ void apply_steps(const ApplyArgs& p, const MuShape& s, int64_t mat, int wave, int waves,
-                                            int lane, const float* qs) {
+                                            int lane, const float* qs, float* scratch) {
   constexpr int kStep = ApplyShape<NT, TALL>::kStep;
-  Steps at(s, mat, wave, waves, kStep, !TALL || s.S >= 4);
+  Steps at(s, mat, wave, waves, kStep, true);
+  if constexpr (TALL) {
+    const TallLds<NT> x(scratch, s.S, lane);
 #pragma unroll 1
-  for (; at.valid(); at.i += at.stride) {
-    if constexpr (TALL)
-      apply_tall<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
-    else
-      apply_wide<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
-  }
+    for (; at.valid(); at.i += at.stride) apply_tall<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs, x);
 #pragma unroll 1
-  for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep) {
-    if constexpr (TALL)
-      apply_tall<NT, false, false>(p, s, (int)j0, lane, qs);
-    else
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
+      apply_tall<NT, false, false>(p, s, (int)j0, lane, qs, x);
+  } else {
+#pragma unroll 1
+    for (; at.valid(); at.i += at.stride) apply_wide<NT, true, STREAM>(p, s, at.j0(at.i), lane, qs);
+#pragma unroll 1
+    for (int64_t j0 = at.rest; j0 < s.L; j0 += (int64_t)at.stride * kStep)
       apply_wide<NT, false, false>(p, s, (int)j0, lane, qs);
   }
 }
@@ -776,7 +833,9 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
                                                               const double* __restrict__ part, int parts, MuonCoef co,
                                                               float eps) {
   constexpr int N = 16 * NT;
-  __shared__ float qs[N * ApplyShape<NT, TALL>::kQRow];
+  using Sh = ApplyShape<NT, TALL>;
+  __shared__ float qs[N * Sh::kQRow];
+  __shared__ __attribute__((aligned(16))) float scratch[TALL ? 4 * Sh::kScratch : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = s.nmat - 1 - blockIdx.x / splits;
   if constexpr (NT == 1) {
@@ -786,13 +845,13 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
     gram_reduce<1, 4>(sum, red, wave, lane);
     if (wave == 0) poly_run16(sum[0], co, eps, Q, s.S, lane);
     __syncthreads();
-    put_q<1, TALL>(Q, qs, s.S, kMuThreads);
+    put_q<1, TALL>(Q, qs, kMuThreads);
   } else {
-    put_q<NT, TALL>(Qin + (size_t)mat * N * N, qs, s.S, kMuThreads);
+    put_q<NT, TALL>(Qin + (size_t)mat * N * N, qs, kMuThreads);
   }
   __syncthreads();
   apply_steps<NT, TALL, STREAM>(apply_at(args, mat * s.rows * s.cols), s, mat, (int)(blockIdx.x % splits) * 4 + wave,
-                                splits * 4, lane, qs);
+                                splits * 4, lane, qs, scratch + wave * Sh::kScratch);
 }
 
 // A small matrix of S <= 16 whole: one work-group makes both passes and the
@@ -801,7 +860,9 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
 template <bool TALL>
 __global__ __launch_bounds__(512) void k_muon_whole(ApplyArgs args, MuShape s, MuonCoef co, float eps) {
   __shared__ double red[4 * 256];
-  __shared__ float Q[256], qs[16 * ApplyShape<1, TALL>::kQRow];
+  using Sh = ApplyShape<1, TALL>;
+  __shared__ float Q[256], qs[16 * Sh::kQRow];
+  __shared__ __attribute__((aligned(16))) float scratch[TALL ? 8 * Sh::kScratch : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t mat = blockIdx.x;
   const ApplyArgs p = apply_at(args, mat * s.rows * s.cols);
@@ -810,9 +871,9 @@ __global__ __launch_bounds__(512) void k_muon_whole(ApplyArgs args, MuShape s, M
   gram_reduce<1, 8>(acc, red, wave, lane);
   if (wave == 0) poly_run16(acc[0], co, eps, Q, s.S, lane);
   __syncthreads();
-  put_q<1, TALL>(Q, qs, s.S, 512);
+  put_q<1, TALL>(Q, qs, 512);
   __syncthreads();
-  apply_steps<1, TALL, false>(p, s, mat, wave, 8, lane, qs);
+  apply_steps<1, TALL, false>(p, s, mat, wave, 8, lane, qs, scratch + wave * Sh::kScratch);
 }
 
 // ----------------------------------------------------------- launchers ----

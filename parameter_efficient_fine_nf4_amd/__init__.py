@@ -626,7 +626,7 @@ class kernel_timing:
              "prep_adapters", "lora_proj", "lora_proj_finish", "token_reduce",
              "token_reduce_finish", "fwd_decode", "fwd_decode_finish", "fwd_rich", "dx", "drop_input", "adam",
              "fwd_sum_splits", "dx_sum_splits", "logprob", "logprob_grad", "preference", "policy", "muon_gram",
-             "muon_poly", "muon_apply", "muon_whole")
+             "muon_sum", "muon_poly", "muon_apply", "muon_whole")
 
     def __enter__(self):
         _check(_lib.qlora_timing_reset(), "qlora_timing_reset")

@@ -21,6 +21,7 @@
 // G_0 and the iteration are held in fp64: a small singular value s of X enters
 // G as s^2, which fp32 loses below 3e-4 of the largest, while the iteration
 // amplifies it by a^n (485 for the usual five steps).
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -184,6 +185,23 @@ struct Steps {
   __device__ __forceinline__ int j0(int at) const { return (first + at < n ? first + at : first + at - n) * step; }
 };
 
+// A work-group's matrix and split.  Work-groups go to the 8 dies in turn; each
+// die takes neighbouring ones of the stack, so that a line of memory that two
+// of them share is read once and written whole by one L2 (27 x 64 x 10704,
+// pass 1: 50 us in plain order, 46 so).  last_first: a die's from the last to
+// the first.
+struct MuPlace {
+  int64_t mat;
+  int split, group;
+  __device__ __forceinline__ MuPlace(const MuShape& s, int splits, bool last_first) {
+    const int all = (int)s.nmat * splits, die = blockIdx.x % 8, i = blockIdx.x / 8;
+    const int each = all / 8, more = all % 8, n = each + (die < more);
+    group = die * each + min(die, more) + (last_first ? n - 1 - i : i);
+    mat = group / splits;
+    split = group % splits;
+  }
+};
+
 // -------------------------------------------------------------- pass 1 ----
 //
 // m <- mu m + g, and one fp64 partial of u u^T per (matrix, split), as the
@@ -323,13 +341,14 @@ __global__ __launch_bounds__(kMuThreads, 3) void k_muon_gram(const uint16_t* __r
   constexpr int U = mu_tiles(NT);
   __shared__ double red[2 * U * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t mat = blockIdx.x / splits, base = mat * s.rows * s.cols;
+  const MuPlace at(s, splits, false);
+  const int64_t base = at.mat * s.rows * s.cols;
   f64x4 acc[U];
-  gram_sums<NT, TALL>(G + base, M + base, s, mat, (int)(blockIdx.x % splits) * 4 + wave, splits * 4, lane, mu,
-                      nesterov, acc);
+  gram_sums<NT, TALL>(G + base, M + base, s, at.mat, at.split * 4 + wave, splits * 4, lane, mu, nesterov,
+                      acc);
   gram_reduce<NT, 4>(acc, red, wave, lane);
   if (wave == 0) {
-    double* out = part + (size_t)blockIdx.x * U * 256;
+    double* out = part + (size_t)at.group * U * 256;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -514,22 +533,52 @@ __device__ __forceinline__ f64x4 poly_sum16(const double* __restrict__ src, int 
   return sum;
 }
 
+// The sum of many partials (a quarter of a tile of a matrix a work-group), so
+// that the one work-group of the iteration need not read them all.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_muon_sum(const double* __restrict__ part, int splits, int quarters,
+                                                             double* __restrict__ sums) {
+  __shared__ double red[kSumWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+  const double* src = part + ((int64_t)(blockIdx.x / quarters) * splits * quarters + blockIdx.x % quarters) * 64 + lane;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k = wave; k < splits; k += 8 * kSumWaves) {
+    double v[8];  // in flight
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = k + j * kSumWaves;
+      v[j] = at < splits ? src[(int64_t)at * quarters * 64] : 0.0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j];
+  }
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int j = 1; j < kSumWaves; ++j) sum += red[j][lane];
+    sums[(int64_t)blockIdx.x * 64 + lane] = sum;
+  }
+}
+
 // part -> Q / (|u| + eps): N x N, zeros past S.
 template <int NT, bool TALL>
 __global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __restrict__ part, int splits, int S,
                                                                MuonCoef co, float eps, float* __restrict__ Qout) {
   constexpr int N = 16 * NT, U = mu_tiles(NT);
   __shared__ double m[4][N * N];
-  // the partials' sum, in order, four partials' loads in flight for every
+  // the partials' sum, in order, several partials' loads in flight for every
   // element of a thread
   constexpr int kThreads = 64 * kPolyWaves, E = (U * 256 + kThreads - 1) / kThreads;
+  constexpr int J = NT == 4 ? 8 : 16;
   const double* src = part + (size_t)blockIdx.x * splits * U * 256;
   double sum[E] = {};
 #pragma unroll 1
-  for (int k = 0; k < splits; k += 4) {
-    double v[4][E];
+  for (int k = 0; k < splits; k += J) {
+    double v[J][E];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int at = e * kThreads + threadIdx.x;
@@ -537,7 +586,7 @@ __global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __r
         if (k + j < splits && at < U * 256) v[j][e] = src[(size_t)(k + j) * U * 256 + at];
       }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] += v[j][e];
   }
@@ -837,21 +886,21 @@ __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, Mu
   __shared__ float qs[N * Sh::kQRow];
   __shared__ __attribute__((aligned(16))) float scratch[TALL ? 4 * Sh::kScratch : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t mat = s.nmat - 1 - blockIdx.x / splits;
+  const MuPlace at(s, splits, true);
   if constexpr (NT == 1) {
     __shared__ double red[2 * 256];
     __shared__ float Q[256];
-    f64x4 sum[1] = {poly_sum16(part + (size_t)mat * parts * 256, wave, parts, lane)};
+    f64x4 sum[1] = {poly_sum16(part + (size_t)at.mat * parts * 256, wave, parts, lane)};
     gram_reduce<1, 4>(sum, red, wave, lane);
     if (wave == 0) poly_run16(sum[0], co, eps, Q, s.S, lane);
     __syncthreads();
     put_q<1, TALL>(Q, qs, kMuThreads);
   } else {
-    put_q<NT, TALL>(Qin + (size_t)mat * N * N, qs, kMuThreads);
+    put_q<NT, TALL>(Qin + (size_t)at.mat * N * N, qs, kMuThreads);
   }
   __syncthreads();
-  apply_steps<NT, TALL, STREAM>(apply_at(args, mat * s.rows * s.cols), s, mat, (int)(blockIdx.x % splits) * 4 + wave,
-                                splits * 4, lane, qs, scratch + wave * Sh::kScratch);
+  apply_steps<NT, TALL, STREAM>(apply_at(args, at.mat * s.rows * s.cols), s, at.mat, at.split * 4 + wave, splits * 4,
+                                lane, qs, scratch + wave * Sh::kScratch);
 }
 
 // A small matrix of S <= 16 whole: one work-group makes both passes and the
@@ -880,25 +929,32 @@ __global__ __launch_bounds__(512) void k_muon_whole(ApplyArgs args, MuShape s, M
 
 static int mu_nt(const MuShape& s) { return (s.S + 15) / 16; }
 
-// Work-groups per matrix: `all` over the stack (a few per CU), each with at
-// least `per` long positions.
+// Work-groups per matrix: as many as the chip holds at a time (`all`), for one
+// more would wait for a whole turn of the others (80 x 64 x 8192, pass 2: 115
+// us with 6 a matrix, 143 with 7); each with at least `per` long positions.
 static int mu_splits(const MuShape& s, int all, int per) {
-  const int64_t most = ((int64_t)s.L + per - 1) / per;
-  int64_t n = (all + s.nmat - 1) / s.nmat;
-  if (n > most) n = most;
-  return (int)(n < 1 ? 1 : n);
+  const int64_t most = ((int64_t)s.L + per - 1) / per, n = std::min<int64_t>(all / s.nmat, most);
+  return (int)std::max<int64_t>(n, 1);
 }
-// The Gram pass's partials (2 to 20 KB, by S) are read again by the one
-// work-group that sums them: at most 32 a matrix.
+// Splits of pass 1.  The work-group that needs the sum of the partials makes
+// it, of up to mu_parts (each costs it 0.3 us at S = 64: 8 x 64 x 8192, pass 1
+// and iteration: 62 us with 32, 64 with 16, 55 with 32 that a launch has
+// summed; 27 x 32 x 10704: 36 with 28, 38 with 16, 40 summed by a launch).
+// More are worth that launch where a split's part of the long axis would take
+// longer (1 x 64 x 131072, pass 1 and the sum: 282 us with 16, 30 with 512; 1
+// x 32 x 65536: 51 with 32, 37 with 256; even at the lengths of the rule).
+static int mu_parts(const MuShape& s) { return s.S > 48 ? 16 : 32; }
 static int gram_splits(const MuShape& s) {
-  const int n = mu_splits(s, 1024, 256);
-  return n < 32 ? n : 32;
+  const int n = mu_splits(s, 3 * 256, 256);
+  return s.L > (s.S > 48 ? 4096 : s.S > 32 ? 16384 : 32768) ? n : std::min(n, mu_parts(s));
 }
 
 static bool mu_whole(const MuShape& s) { return s.S <= 16 && (int64_t)s.S * s.L <= kMuWhole; }
 
+// Partials and, of more than mu_parts, their sums.
 static size_t mu_part_bytes(const MuShape& s) {
-  return (size_t)s.nmat * gram_splits(s) * mu_tiles(mu_nt(s)) * 256 * sizeof(double);
+  const int n = gram_splits(s);
+  return (size_t)s.nmat * (n + (n > mu_parts(s))) * mu_tiles(mu_nt(s)) * 256 * sizeof(double);
 }
 
 size_t muon_ws_bytes(int64_t nmat, int64_t rows, int64_t cols) {
@@ -916,18 +972,29 @@ static void muon_kernels(const ApplyArgs& a, const MuShape& s, float eps, const 
       QLORA_LAUNCH("muon_whole", st, k_muon_whole<TALL>, dim3((unsigned)s.nmat), dim3(512), 0, st, a, s, co, eps);
       return;
     }
-  const int gs = gram_splits(s), as = mu_splits(s, 512, 4 * ApplyShape<NT, TALL>::kStep);
+  const int gs = gram_splits(s), as = mu_splits(s, 2 * 256, 4 * ApplyShape<NT, TALL>::kStep);
   const dim3 block(kMuThreads);
   QLORA_LAUNCH("muon_gram", st, (k_muon_gram<NT, TALL>), dim3((unsigned)(s.nmat * gs)), block, 0, st, a.G, a.M, s,
                a.mu, a.nesterov, gs, part);
+  int parts = gs;
+  if (gs > mu_parts(s)) {
+    double* sums = part + (size_t)s.nmat * gs * mu_tiles(NT) * 256;
+    QLORA_LAUNCH("muon_sum", st, k_muon_sum, dim3((unsigned)(s.nmat * mu_tiles(NT) * 4)), dim3(64 * kSumWaves), 0, st,
+                 part, gs, mu_tiles(NT) * 4, sums);
+    part = sums;
+    parts = 1;
+  }
   if constexpr (NT > 1)
     QLORA_LAUNCH("muon_poly", st, (k_muon_poly<NT, TALL>), dim3((unsigned)s.nmat), dim3(64 * kPolyWaves), 0, st, part,
-                 gs, s.S, co, eps, Q);
+                 parts, s.S, co, eps, Q);
   const dim3 grid((unsigned)(s.nmat * as));
-  if (14 * s.nmat * s.rows * s.cols > ((int64_t)128 << 20))  // m, g, w and p
-    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, true>), grid, block, 0, st, a, s, as, Q, part, gs, co, eps);
+  // m, g, w and p; rows that do not start on a line go through the cache, which
+  // puts the lines that steps share together (27 x 52 x 10706: 57 us, past it
+  // 101; 80 x 64 x 8192: 153, past it 116)
+  if (14 * s.nmat * s.rows * s.cols > ((int64_t)128 << 20) && (TALL || s.L % 32 == 0))
+    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, true>), grid, block, 0, st, a, s, as, Q, part, parts, co, eps);
   else
-    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, false>), grid, block, 0, st, a, s, as, Q, part, gs, co, eps);
+    QLORA_LAUNCH("muon_apply", st, (k_muon_apply<NT, TALL, false>), grid, block, 0, st, a, s, as, Q, part, parts, co, eps);
 }
 
 hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t nmat, int64_t rows, int64_t cols,

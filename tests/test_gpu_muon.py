@@ -80,7 +80,9 @@ SHAPES = [(1, 1, 1), (2, 1, 64), (1, 64, 1), (3, 2, 3), (1, 8, 256), (2, 256, 8)
           (2, 64, 8192), (1, 11008, 64), (5, 11008, 16), (40, 16, 300), (1, 60, 22016), (300, 4, 64),
           # tall, with a rank that no vector divides
           (3, 5000, 1), (3, 5000, 2), (3, 5000, 3), (3, 5001, 5), (2, 5000, 6), (2, 2003, 13), (2, 700, 19),
-          (2, 2001, 31), (2, 700, 35), (2, 1300, 47), (2, 700, 50), (2, 1111, 53), (1, 900, 61), (70, 333, 62)]
+          (2, 2001, 31), (2, 700, 35), (2, 1300, 47), (2, 700, 50), (2, 1111, 53), (1, 900, 61), (70, 333, 62),
+          # long: many partials; m, g, w and p larger than half the last-level cache, rows on lines or not
+          (1, 40, 20000), (1, 16, 70000), (1, 70001, 3), (2, 32, 40000), (3, 52, 65536), (3, 65536, 52), (2, 50, 98305)]
 
 
 @pytest.mark.parametrize("n,rows,cols", SHAPES)

@@ -17,8 +17,15 @@
 // z is taken first.  Sums are fp32 and go through a fixed tree, so results do
 // not depend on the schedule.
 //
-// A row is a work-group's, read 16 bytes a lane.  Where it fits the work-group's registers it is read once: all of its loads are in
-// flight together, then the maximum, the sum and the gradient follow from the
+// c's rounding is the same for every row too, and it stays: with the exponents
+// x_v as formed and c (1 + d) unrounded, ln S is off by -ln 2 d E_p[x], some
+// 4e-8 that has one sign in all of a sequence's tokens (4096 of them: 1.5e-4
+// in its sum, where fp32 log-probabilities leave 2e-5).  E_p[x] is needed to a
+// digit only, so it is taken from one element of a 16-byte piece, or of a few.
+//
+// A row is a work-group's, read 16 bytes a lane.  Where it fits the
+// work-group's registers it is read once: all of its loads are in flight
+// together, then the maximum, the sum and the gradient follow from the
 // registers.  Longer rows are read in pieces with a running maximum, and again
 // for the gradient.
 #include <cmath>
@@ -85,6 +92,9 @@ __device__ __forceinline__ void put16(void* out, const u32x4& v) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// 2^x's share e x of a mean of x: 0 for x = -inf, as for any x whose e is 0.
+__device__ __forceinline__ float weigh(float e, float x) { return e * fmaxf(x, -200.0f); }
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
@@ -104,16 +114,36 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   for (int i = 1; i < T / 64; ++i) r = fmaxf(r, red[i]);
   return r;
 }
+
+// The sum of a row's exponentials e = 2^x, and of e x over the sampled ones.
+struct RowSum {
+  float e, ex;
+};
+// Over the work-group: e for every thread; of ex each wave leaves its sum in
+// `part`, for wave 0 to join (join_ex, after the barrier here).
 template <int T>
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  v = wave_sum(v);
-  if (T == 64) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+__device__ __forceinline__ float block_sum(const RowSum& v, float* red, float* part) {
+  const float e = wave_sum(v.e), ex = wave_sum(v.ex);
+  if (T == 64) {
+    part[0] = ex;
+    return e;
+  }
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = e;
+    part[threadIdx.x >> 6] = ex;
+  }
   __syncthreads();
   float r = red[0];
 #pragma unroll
   for (int i = 1; i < T / 64; ++i) r += red[i];
   return r;
+}
+template <int T>
+__device__ __forceinline__ float join_ex(const float* part) {
+  float v = part[T == 64 ? 0 : threadIdx.x & (T / 64 - 1)];
+#pragma unroll
+  for (int o = T / 128; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
 }
 
 // How a row's exponentials are formed from its maximum m.
@@ -122,16 +152,20 @@ struct RowExp {
   bool far;
   __device__ __forceinline__ RowExp(float m_, float c_)
       : c(c_), k((float)((double)m_ * (double)c_)), m(m_), far(!(fabsf(k) < 1048576.0f)) {}
-  __device__ __forceinline__ float near_e(float z) const { return exp2_hw(fmaf(z, c, -k)); }
-  __device__ __forceinline__ float far_e(float z) const { return exp2_hw((z - m) * c); }
+  __device__ __forceinline__ float near_x(float z) const { return fmaf(z, c, -k); }
+  __device__ __forceinline__ float far_x(float z) const { return (z - m) * c; }
+  __device__ __forceinline__ float near_e(float z) const { return exp2_hw(near_x(z)); }
+  __device__ __forceinline__ float far_e(float z) const { return exp2_hw(far_x(z)); }
   __device__ __forceinline__ float e(float z) const { return far ? far_e(z) : near_e(z); }
   // factor of near_e over far_e: what k's rounding is
   __device__ __forceinline__ float shift() const {
     return far ? 1.0f : exp2_hw((float)((double)m * (double)c - (double)k));
   }
-  // ln of the sum of exp(tau (z - m)), from the sum s of e()
-  __device__ __forceinline__ double ln_sum(float s) const {
-    return log((double)s) + (far ? 0.0 : kLn2 * ((double)k - (double)m * (double)c));
+  // ln of the sum of exp(tau (z - m)), from the sum s of e(); drift: ln 2 d
+  // times the sum of e x
+  __device__ __forceinline__ double ln_sum(float s, float drift) const {
+    return log((double)s) + (far ? 0.0 : kLn2 * ((double)k - (double)m * (double)c)) +
+           (double)(drift * __builtin_amdgcn_rcpf(s));
   }
 };
 
@@ -195,65 +229,85 @@ struct RowRegs {
     return m;
   }
   template <bool FAR>
-  __device__ __forceinline__ float sum_of(const RowExp& x) const {
-    float s[2] = {FAR ? x.far_e(last) : x.near_e(last), 0.0f};
+  __device__ __forceinline__ RowSum sum_of(const RowExp& x) const {
+    float s[2] = {FAR ? x.far_e(last) : x.near_e(last), 0.0f}, ex = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float f[kPer];
       Elem<E>::unpack(anew<1 + FAR>(w[j]), f);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) s[q & 1] += FAR ? x.far_e(f[q]) : x.near_e(f[q]);
+      for (int q = 0; q < kPer; ++q) {
+        const float xq = FAR ? x.far_x(f[q]) : x.near_x(f[q]), e = exp2_hw(xq);
+        s[q & 1] += e;
+        if (q == 0) ex += weigh(e, xq);
+      }
     }
-    return s[0] + s[1];
+    return RowSum{s[0] + s[1], ex};
   }
-  __device__ __forceinline__ float sum(const RowExp& x) const { return x.far ? sum_of<true>(x) : sum_of<false>(x); }
+  __device__ __forceinline__ RowSum sum(const RowExp& x) const { return x.far ? sum_of<true>(x) : sum_of<false>(x); }
 };
 
 // Running maximum and sum of exp2((z - m) c), for rows read in pieces.  A
 // maximum of -inf (nothing but masked values so far) is read as 0 in the
 // exponents: -inf - (-inf) would make a NaN of it.
+// One of PER elements is sampled: the first that add() takes of so many.
+template <int PER>
 struct Online {
-  float m = kNegInf, s = 0.0f;
-  template <int N>
-  __device__ __forceinline__ void add(const float (&f)[N], float c) {
-    float mx = m;
+  float m = kNegInf;
+  RowSum s{0.0f, 0.0f};
+  // the sums with x + shift for x
+  __device__ __forceinline__ RowSum shifted(float shift) const {
+    const float f = exp2_hw(shift);
+    return RowSum{s.e * f, s.ex * f + weigh(s.e * f, shift) * (1.0f / PER)};
+  }
+  template <typename E, int N>
+  __device__ __forceinline__ void add(const u32x4 (&w)[N], float c) {
+    constexpr int kPer = Elem<E>::kPer16;
+    float f[kPer], mx = m;
 #pragma unroll
-    for (int i = 0; i < N; ++i) mx = fmaxf(mx, f[i]);
+    for (int j = 0; j < N; ++j) {
+      Elem<E>::unpack(anew<0>(w[j]), f);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) mx = fmaxf(mx, f[q]);
+    }
     const float ref = mx == kNegInf ? 0.0f : mx;
-    float sum = s * exp2_hw((m - ref) * c);
+    RowSum sum = shifted((m - ref) * c);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += exp2_hw((f[i] - ref) * c);
+    for (int j = 0; j < N; ++j) {
+      Elem<E>::unpack(anew<2>(w[j]), f);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const float x = (f[q] - ref) * c, e = exp2_hw(x);
+        sum.e += e;
+        if (j == 0 && q == 0) sum.ex += weigh(e, x);
+      }
+    }
     m = mx;
     s = sum;
+  }
+  __device__ __forceinline__ void add_one(float f, float c) {
+    const float mx = fmaxf(m, f), ref = mx == kNegInf ? 0.0f : mx;
+    s = shifted((m - ref) * c);
+    s.e += exp2_hw((f - ref) * c);
+    m = mx;
   }
 };
 
 // Maximum and sum of a row of any length, in pieces.
 template <typename E, int T, int N>
-__device__ __forceinline__ Online row_pieces(const E* z, int V, const RowSpan& at, float c) {
+__device__ __forceinline__ Online<N * Elem<E>::kPer16> row_pieces(const E* z, int V, const RowSpan& at, float c) {
   constexpr int kPer = Elem<E>::kPer16;
-  Online o;
+  Online<N * kPer> o;
   for (int i0 = threadIdx.x; i0 < at.nv; i0 += N * T) {
-    float f[N * kPer];
     u32x4 w[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       w[j] = u32x4{Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill};
       if (i0 + j * T < at.nv) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (size_t)(i0 + j * T) * kPer);
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      float g[kPer];
-      Elem<E>::unpack(w[j], g);
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) f[j * kPer + q] = g[q];
-    }
-    o.add(f, c);
+    o.template add<E, N>(w, c);
   }
-  if (at.rest < V) {
-    const float f[1] = {Elem<E>::get(z + at.rest)};
-    o.add(f, c);
-  }
+  if (at.rest < V) o.add_one(Elem<E>::get(z + at.rest), c);
   return o;
 }
 
@@ -419,7 +473,7 @@ struct RowArgs {
   int64_t T, ld, ldd;
   int V;
   const int32_t* labels;
-  float tau, c;  // c = fl(tau log2 e)
+  float tau, c, drift;  // c = fl(tau log2 e) = tau log2 e / (1 + d), drift = ln 2 d
   float* logp;
   float* stats;  // (max z, sum of e) per row
   void* dlogits;
@@ -429,8 +483,9 @@ struct RowArgs {
 // Log-probabilities, and with POLICY the policy loss and its gradient.  N > 0:
 // the row fits N pieces a thread; N < 0: -N pieces a thread at a time.
 template <typename E, int T, int N, bool POLICY>
-__global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
-  __shared__ float red[2][T / 64];
+__global__ __launch_bounds__(T, N < 0 ? 8 : 1) void k_rows(RowArgs a, PolicyArgs pa) {
+  __shared__ float maxima[T / 64];
+  __shared__ float sums[T / 64], sampled[T / 64];
   __shared__ float gsh;
   const E* logits = reinterpret_cast<const E*>(a.logits);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -458,26 +513,27 @@ __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
     const float zy = Elem<E>::get(z + label);
     RowRegs<E, T, N < 0 ? 1 : N> r;
     const RowSpan at(z, a.V);
-    Online o;
+    constexpr int kSample = (N < 0 ? -N : 1) * Elem<E>::kPer16;
+    Online<kSample> o;
     float m;
     if constexpr (N > 0) {
       r.load(z, a.V, at);
-      m = block_max<T>(fmaxf(r.max(), zy), red[0]);
+      m = block_max<T>(fmaxf(r.max(), zy), maxima);
     } else {
       o = row_pieces<E, T, -N>(z, a.V, at, a.c);
-      m = block_max<T>(fmaxf(o.m, zy), red[0]);
+      m = block_max<T>(fmaxf(o.m, zy), maxima);
     }
     const RowExp x(m, a.c);
     // (in pieces: a thread without a finite value holds m = -inf and s = 0; a
     // row of nothing but -inf has no distribution and gives NaN)
     float s;
     if constexpr (N > 0)
-      s = block_sum<T>(r.sum(x), red[1]);
+      s = block_sum<T>(r.sum(x), sums, sampled);
     else
-      s = block_sum<T>(o.s * x.far_e(o.m), red[1]) * x.shift();
+      s = block_sum<T>(o.shifted(x.far_x(o.m)), sums, sampled) * x.shift();
     float g = 0.0f;
     if (threadIdx.x < 64) {  // fp64, once: one wave
-      const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s);
+      const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s, a.drift * kSample * join_ex<T>(sampled));
       float loss, kl;
       if (POLICY) g = policy_token(pa, t, lp, loss, kl);
       if (threadIdx.x == 0) {
@@ -714,10 +770,14 @@ static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t 
 static bool past_cache(int64_t T, int64_t ldd, int f32) { return T * ldd * (f32 ? 4 : 2) > ((int64_t)128 << 20); }
 
 static float exp2_scale(float tau) { return (float)((double)tau * kLog2e); }
+static float exp2_drift(float tau) {
+  const double c = exp2_scale(tau);
+  return c > 0.0 && std::isfinite(c) ? (float)(kLn2 * ((double)tau * kLog2e / c - 1.0)) : 0.0f;
+}
 
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                           float* logp, float* stats, hipStream_t st) {
-  const RowArgs a{logits, T, ld, 0, V, labels, tau, exp2_scale(tau), logp, stats, nullptr, false};
+  const RowArgs a{logits, T, ld, 0, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, stats, nullptr, false};
   return f32 ? launch_rows<float, false>("logprob", a, PolicyArgs{}, st)
              : launch_rows<uint16_t, false>("logprob", a, PolicyArgs{}, st);
 }
@@ -725,7 +785,7 @@ hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t
 hipError_t launch_logprob_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels,
                                float tau, const float* stats, const float* dlogp, void* dlogits, int64_t ldd,
                                hipStream_t st) {
-  const RowArgs a{logits, T,       ld,     ldd,  V, labels, tau, exp2_scale(tau), nullptr, const_cast<float*>(stats),
+  const RowArgs a{logits, T,       ld,     ldd,  V, labels, tau, exp2_scale(tau), exp2_drift(tau), nullptr, const_cast<float*>(stats),
                   dlogits, past_cache(T, ldd, f32)};
   return f32 ? launch_grad<float>(a, dlogp, st) : launch_grad<uint16_t>(a, dlogp, st);
 }
@@ -735,7 +795,7 @@ hipError_t launch_policy(const void* logits, int f32, int64_t T, int V, int64_t 
                          float clip_low, float clip_high, float kl_coef, float* loss, float* kl, float* logp,
                          void* dlogits, int64_t ldd, hipStream_t st) {
   const PolicyArgs pa{adv, old_logp, ref_logp, weight, 1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, kl};
-  const RowArgs a{logits, T, ld, ldd, V, labels, tau, exp2_scale(tau), logp, nullptr, dlogits,
+  const RowArgs a{logits, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, nullptr, dlogits,
                   past_cache(T, ldd, f32)};
   return f32 ? launch_rows<float, true>("policy", a, pa, st) : launch_rows<uint16_t, true>("policy", a, pa, st);
 }

@@ -469,3 +469,20 @@ def test_captured_step_replays(lib):
         torch.cuda.synchronize()
         for o in outs:
             assert all(torch.equal(a, b) for a, b in zip(o, want)), rep
+
+
+@pytest.mark.parametrize("tau", [0.6934478282928467, 0.6936106085777283])
+@pytest.mark.parametrize("T,V,dtype", [(4096, 8191, F32), (4096, 70001, BF)], ids=["f32", "bf16"])
+def test_logprobs_do_not_drift(lib, T, V, dtype, tau):
+    # temperatures whose scale tau log2 e rounds by most, 2^-24 of it, either way: exponents taken with it alone put
+    # ln S off by 2^-24 E_p|t|, 1.3e-7 here, the same way in every token.  Of the mean over T tokens are left the
+    # results' roundings (half steps of 2^-21 for -16 < logp < -8, 2^-21 / sqrt 3 a token, six standard deviations) and of the
+    # hardware's exp2 as much as half a step one way.
+    _case("drift", T, V, dtype, tau)
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = torch.randn(T, V, device=DEV, generator=g).to(dtype)
+    y = torch.randint(0, V, (T,), device=DEV, generator=g, dtype=torch.int32)
+    logp = lib.token_logprobs(z, y, tau)
+    want = torch.cat([(r.double() * tau).log_softmax(1)[torch.arange(len(r), device=DEV), i.long()]
+                      for r, i in zip(z.split(256), y.split(256))])
+    assert abs((logp.double() - want).mean().item()) <= U + 6 * 2.0 ** -21 / (3 * T) ** 0.5

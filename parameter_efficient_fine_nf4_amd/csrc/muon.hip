@@ -333,7 +333,11 @@ __device__ __forceinline__ void gram_reduce(f64x4 (&acc)[mu_tiles(NT)], double* 
   }
 }
 
-// (three waves a SIMD: at two the loads of one step do not cover the sums)
+// Bound by memory, 10 bytes a parameter, where S is large (80 x 64 x 8192: 90
+// us, 420 MB at 4.7 TB/s; the fp64 MFMAs of a triangle of tiles take 60 us of
+// the matrix units beside it), by the latency of its few steps where it is
+// not (32 x 11008 x 16: 11 us, 56 MB).  Three waves a SIMD: at two the loads of
+// one step do not cover the sums (368 us for the whole call, 336 with three).
 template <int NT, bool TALL>
 __global__ __launch_bounds__(kMuThreads, 3) void k_muon_gram(const uint16_t* __restrict__ G, float* __restrict__ M,
                                                              MuShape s, float mu, int nesterov, int splits,
@@ -381,10 +385,15 @@ struct PolyLds {
   }
 };
 
-// Two waves per SIMD (one would leave the matrix unit idle over its own LDS
-// traffic) share the tiles in turn; the second of two products that run in one
-// phase starts with the wave at which the first one's tiles ended.
-constexpr int kPolyWaves = 8;
+// Four waves per SIMD (one would leave the matrix unit idle over its own LDS
+// traffic; S = 64: two 36.7 us, four 34.5) share the tiles in turn; the second
+// of two products that run in one phase starts with the wave at which the
+// first one's tiles ended.
+//
+// 17 products in five steps at S = 64 are 2720 MFMAs of 64 cycles, 18 us of
+// the four matrix units of the one CU that a matrix has; the rest are 15 LDS
+// phases and the sum of the partials (S = 48: 24 us, S = 32: 14).
+constexpr int kPolyWaves = 16;
 template <int NT>
 constexpr int kPolyTiles = (mu_tiles(NT) + kPolyWaves - 1) / kPolyWaves;
 
@@ -874,8 +883,11 @@ __device__ __forceinline__ ApplyArgs apply_at(ApplyArgs p, int64_t base) {
 // The matrices go from the last to the first, whose m and g pass 1 read or
 // wrote longest ago.  STREAM: the stack is larger than half the last-level
 // cache; weights and their copy, touched once, then go past it, and more of m
-// and g is still there (80 x 64 x 8192: 179 us without either, 144 with both;
-// pass 1 of the next call 119 and 108; a stack that fits takes 1 us longer).
+// and g is still there (80 x 64 x 8192: 153 us without STREAM, 116 with it;
+// pass 1 of the next call 114 and 91; a stack that fits takes 1 us longer).
+//
+// Bound by memory: 16 bytes a parameter, 671 MB at 5.8 TB/s there; 32 x 11008 x
+// 16, in the cache, 18 us, 90 MB at 5 TB/s with the iteration.
 template <int NT, bool TALL, bool STREAM>
 __global__ __launch_bounds__(kMuThreads, 2) void k_muon_apply(ApplyArgs args, MuShape s, int splits,
                                                               const float* __restrict__ Qin,

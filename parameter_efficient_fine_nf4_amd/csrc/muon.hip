@@ -334,7 +334,7 @@ __device__ __forceinline__ void gram_reduce(f64x4 (&acc)[mu_tiles(NT)], double* 
 }
 
 // Bound by memory, 10 bytes a parameter, where S is large (80 x 64 x 8192: 90
-// us, 420 MB at 4.7 TB/s; the fp64 MFMAs of a triangle of tiles take 60 us of
+// us, 420 MB at 4.7 TB/s; the fp64 MFMAs of a triangle of tiles take 51 us of
 // the matrix units beside it), by the latency of its few steps where it is
 // not (32 x 11008 x 16: 11 us, 56 MB).  Three waves a SIMD: at two the loads of
 // one step do not cover the sums (368 us for the whole call, 336 with three).

@@ -28,6 +28,7 @@
 // together, then the maximum, the sum and the gradient follow from the
 // registers.  Longer rows are read in pieces with a running maximum, and again
 // for the gradient.
+#include <algorithm>
 #include <cmath>
 
 #include "common.hpp"
@@ -311,86 +312,94 @@ __device__ __forceinline__ Online<N * Elem<E>::kPer16> row_pieces(const E* z, in
   return o;
 }
 
-// One 16-byte piece of the gradient: e_v kappa with kappa = -g tau / s, and g
-// tau (1 - p) at the label.
+// One 16-byte piece of the gradient: e_v kappa with kappa = -g tau / s.  (The
+// label's g tau (1 - p) is stored over it at the row's end: a test for it in
+// every piece would keep the loads of the next ones back.)
 template <typename E, bool FAR>
-__device__ __forceinline__ u32x4 grad_piece(const u32x4& w, int first, int label, const RowExp& x, float kappa,
-                                            float gt) {
+__device__ __forceinline__ u32x4 grad_piece(const u32x4& w, const RowExp& x, float kappa) {
   constexpr int kPer = Elem<E>::kPer16;
   float f[kPer];
   Elem<E>::unpack(w, f);
 #pragma unroll
   for (int q = 0; q < kPer; ++q) f[q] = (FAR ? x.far_e(f[q]) : x.near_e(f[q])) * kappa;
-  if ((unsigned)(label - first) < (unsigned)kPer) {
-#pragma unroll
-    for (int q = 0; q < kPer; ++q)
-      if (label - first == q) f[q] += gt;
-  }
   return Elem<E>::pack(f);
 }
 
+// What the pieces leave of a row: the single elements, the label's (zy its
+// logit; by the thread that stored its piece) and zeros in columns V..cols-1.
 template <typename E, int T>
-__device__ __forceinline__ void row_end(float last, E* out, int V, int cols, const RowSpan& at, int label, const RowExp& x,
-                                        float kappa, float gt) {
+__device__ __forceinline__ void row_end(float last, float zy, E* out, int V, int cols, const RowSpan& at, int label,
+                                        const RowExp& x, float kappa, float gt) {
+  const int piece = (label - at.head) / Elem<E>::kPer16;
   if (at.rest < V) {
     const float v = x.e(last) * kappa;
     Elem<E>::put(out + at.rest, label == at.rest ? v + gt : v);
   }
+  if (label >= at.head && piece < at.nv && piece % T == (int)threadIdx.x)
+    Elem<E>::put(out + label, x.e(zy) * kappa + gt);
   for (int i = V + threadIdx.x; i < cols; i += T) Elem<E>::put(out + i, 0.0f);
 }
 
-// z -> gradient over one row read from memory; zeros in columns V..cols-1.
+// z -> gradient over one row read from memory.  Where out is z, a thread
+// overwrites only what it has read.
 template <typename E, int T, bool FAR, bool STREAM>
-__device__ __forceinline__ void row_grad_of(const E* z, E* out, int V, int cols, int label, const RowExp& x,
-                                            float kappa, float gt) {
-  constexpr int kPer = Elem<E>::kPer16;
-  const RowSpan at(z, V);
-  float last = kNegInf;
-  if (at.rest < V) last = Elem<E>::get(z + at.rest);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < at.nv; i += T) {
-    const int first = at.head + i * kPer;
-    const u32x4 w = *reinterpret_cast<const u32x4*>(z + first);
-    put16<STREAM>(out + first, grad_piece<E, FAR>(w, first, label, x, kappa, gt));
+__device__ __forceinline__ void row_grad_of(const E* z, E* out, const RowSpan& at, const RowExp& x, float kappa) {
+  constexpr int kPer = Elem<E>::kPer16, kBatch = 4;  // pieces in flight
+  int i = threadIdx.x;
+  for (; i + (kBatch - 1) * T < at.nv; i += kBatch * T) {
+    u32x4 w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (i + j * T) * kPer);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      put16<STREAM>(out + at.head + (i + j * T) * kPer, grad_piece<E, FAR>(w[j], x, kappa));
   }
-  row_end<E, T>(last, out, V, cols, at, label, x, kappa, gt);
+#pragma unroll 1
+  for (; i < at.nv; i += T) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(z + at.head + i * kPer);
+    put16<STREAM>(out + at.head + i * kPer, grad_piece<E, FAR>(w, x, kappa));
+  }
 }
 template <typename E, int T>
-__device__ __forceinline__ void row_grad(const E* z, E* out, int V, int cols, int label, const RowExp& x, float s,
-                                         float gt, bool stream) {
+__device__ __forceinline__ void row_grad(const E* z, float zy, E* out, int V, int cols, int label, const RowExp& x,
+                                         float s, float gt, bool stream) {
+  const RowSpan at(z, V);
   const float kappa = -gt / s;
+  float last = kNegInf;
+  if (at.rest < V) last = Elem<E>::get(z + at.rest);
   if (x.far)
-    row_grad_of<E, T, true, false>(z, out, V, cols, label, x, kappa, gt);
+    row_grad_of<E, T, true, false>(z, out, at, x, kappa);
   else if (stream)
-    row_grad_of<E, T, false, true>(z, out, V, cols, label, x, kappa, gt);
+    row_grad_of<E, T, false, true>(z, out, at, x, kappa);
   else
-    row_grad_of<E, T, false, false>(z, out, V, cols, label, x, kappa, gt);
+    row_grad_of<E, T, false, false>(z, out, at, x, kappa);
+  row_end<E, T>(last, zy, out, V, cols, at, label, x, kappa, gt);
 }
 
 // The same from the registers.
 template <typename E, int T, int N, bool FAR, bool STREAM>
-__device__ __forceinline__ void regs_grad_of(const RowRegs<E, T, N>& r, E* out, const RowSpan& at, int label,
-                                             const RowExp& x, float kappa, float gt) {
-  constexpr int kPer = Elem<E>::kPer16;
+__device__ __forceinline__ void regs_grad_of(const RowRegs<E, T, N>& r, E* out, const RowSpan& at, const RowExp& x,
+                                             float kappa) {
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int i = j * T + threadIdx.x, first = at.head + i * kPer;
+    const int i = j * T + threadIdx.x;
     if (i < at.nv)
-      put16<STREAM>(out + first,
-                    grad_piece<E, FAR>(anew<FAR ? 2 : STREAM ? 3 : 1>(r.w[j]), first, label, x, kappa, gt));
+      put16<STREAM>(out + at.head + i * Elem<E>::kPer16,
+                    grad_piece<E, FAR>(anew<FAR ? 2 : STREAM ? 3 : 1>(r.w[j]), x, kappa));
   }
 }
 template <typename E, int T, int N>
-__device__ __forceinline__ void regs_grad(const RowRegs<E, T, N>& r, E* out, int V, int cols, const RowSpan& at, int label,
-                                          const RowExp& x, float s, float gt, bool stream) {
+__device__ __forceinline__ void regs_grad(const RowRegs<E, T, N>& r, float zy, E* out, int V, int cols,
+                                          const RowSpan& at, int label, const RowExp& x, float s, float gt,
+                                          bool stream) {
   const float kappa = -gt / s;
   if (x.far)
-    regs_grad_of<E, T, N, true, false>(r, out, at, label, x, kappa, gt);
+    regs_grad_of<E, T, N, true, false>(r, out, at, x, kappa);
   else if (stream)
-    regs_grad_of<E, T, N, false, true>(r, out, at, label, x, kappa, gt);
+    regs_grad_of<E, T, N, false, true>(r, out, at, x, kappa);
   else
-    regs_grad_of<E, T, N, false, false>(r, out, at, label, x, kappa, gt);
-  row_end<E, T>(r.last, out, V, cols, at, label, x, kappa, gt);
+    regs_grad_of<E, T, N, false, false>(r, out, at, x, kappa);
+  row_end<E, T>(r.last, zy, out, V, cols, at, label, x, kappa, gt);
 }
 
 template <typename E, int T, bool STREAM>
@@ -470,7 +479,7 @@ __device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, do
 
 struct RowArgs {
   const void* logits;
-  int64_t T, ld, ldd;
+  int64_t first, T, ld, ldd;  // rows first to T - 1
   int V;
   const int32_t* labels;
   float tau, c, drift;  // c = fl(tau log2 e) = tau log2 e / (1 + d), drift = ln 2 d
@@ -481,93 +490,91 @@ struct RowArgs {
 };
 
 // Log-probabilities, and with POLICY the policy loss and its gradient.  N > 0:
-// the row fits N pieces a thread; N < 0: -N pieces a thread at a time, in 64
-// registers, so that a CU holds two rows.
+// the row fits N pieces a thread; N < 0: -N pieces a thread at a time.
+//
 //
 // Bound by memory: the counted rows are read once and the gradient written
 // once.  T = 4093, V = 50021, fp32, a tenth uncounted: 119 us, 737 MB at 6.2
 // TB/s; T = 4096, V = 32000, bf16, a fifth uncounted, with the gradient: 91
 // us, 472 MB at 5.2 TB/s; V = 131071: 429 us, 2.04 GB at 4.8 TB/s.
 template <typename E, int T, int N, bool POLICY>
-__global__ __launch_bounds__(T, N < 0 ? 8 : 1) void k_rows(RowArgs a, PolicyArgs pa) {
+__global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
   __shared__ float maxima[T / 64];
   __shared__ float sums[T / 64], sampled[T / 64];
   __shared__ float gsh;
   const E* logits = reinterpret_cast<const E*>(a.logits);
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int label = a.labels[t];
-    E* out = POLICY && a.dlogits != nullptr ? reinterpret_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
-    if (!is_counted(label, a.V)) {
-      if (out != nullptr) row_zero<E, T>(out, (int)a.ldd, a.stream);
-      if (threadIdx.x == 0) {
-        a.logp[t] = 0.0f;
-        if (a.stats != nullptr) {
-          a.stats[2 * t] = 0.0f;
-          a.stats[2 * t + 1] = 1.0f;
-        }
-        if (POLICY) {
-          pa.loss[t] = 0.0f;
-          if (pa.kl != nullptr) pa.kl[t] = 0.0f;
-        }
+  const int64_t t = a.first + blockIdx.x;
+  const int label = a.labels[t];
+  E* out = POLICY && a.dlogits != nullptr ? reinterpret_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
+  if (!is_counted(label, a.V)) {
+    if (out != nullptr) row_zero<E, T>(out, (int)a.ldd, a.stream);
+    if (threadIdx.x == 0) {
+      a.logp[t] = 0.0f;
+      if (a.stats != nullptr) {
+        a.stats[2 * t] = 0.0f;
+        a.stats[2 * t + 1] = 1.0f;
       }
-      continue;
+      if (POLICY) {
+        pa.loss[t] = 0.0f;
+        if (pa.kl != nullptr) pa.kl[t] = 0.0f;
+      }
     }
-    const E* z = logits + t * a.ld;
-    // the label's logit is one of the row's: it joins the maximum so that
-    // every wave has it in hand before the first barrier, and the row may be
-    // written over after that
-    const float zy = Elem<E>::get(z + label);
-    RowRegs<E, T, N < 0 ? 1 : N> r;
-    const RowSpan at(z, a.V);
-    constexpr int kSample = (N < 0 ? -N : 1) * Elem<E>::kPer16;
-    Online<kSample> o;
-    float m;
-    if constexpr (N > 0) {
-      r.load(z, a.V, at);
-      m = block_max<T>(fmaxf(r.max(), zy), maxima);
-    } else {
-      o = row_pieces<E, T, -N>(z, a.V, at, a.c);
-      m = block_max<T>(fmaxf(o.m, zy), maxima);
+    return;
+  }
+  const E* z = logits + t * a.ld;
+  // the label's logit is one of the row's: it joins the maximum so that
+  // every wave has it in hand before the first barrier, and the row may be
+  // written over after that
+  const float zy = Elem<E>::get(z + label);
+  RowRegs<E, T, N < 0 ? 1 : N> r;
+  const RowSpan at(z, a.V);
+  constexpr int kSample = (N < 0 ? -N : 1) * Elem<E>::kPer16;
+  Online<kSample> o;
+  float m;
+  if constexpr (N > 0) {
+    r.load(z, a.V, at);
+    m = block_max<T>(fmaxf(r.max(), zy), maxima);
+  } else {
+    o = row_pieces<E, T, -N>(z, a.V, at, a.c);
+    m = block_max<T>(fmaxf(o.m, zy), maxima);
+  }
+  const RowExp x(m, a.c);
+  // (in pieces: a thread without a finite value holds m = -inf and s = 0; a
+  // row of nothing but -inf has no distribution and gives NaN)
+  float s;
+  if constexpr (N > 0)
+    s = block_sum<T>(r.sum(x), sums, sampled);
+  else
+    s = block_sum<T>(o.shifted(x.far_x(o.m)), sums, sampled) * x.shift();
+  float g = 0.0f;
+  if (threadIdx.x < 64) {  // fp64, once: one wave
+    const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s, a.drift * kSample * join_ex<T>(sampled));
+    float loss, kl;
+    if (POLICY) g = policy_token(pa, t, lp, loss, kl);
+    if (threadIdx.x == 0) {
+      a.logp[t] = (float)lp;
+      if (a.stats != nullptr) {
+        a.stats[2 * t] = m;
+        a.stats[2 * t + 1] = s;
+      }
+      if (POLICY) {
+        gsh = g;
+        pa.loss[t] = loss;
+        if (pa.kl != nullptr) pa.kl[t] = kl;
+      }
     }
-    const RowExp x(m, a.c);
-    // (in pieces: a thread without a finite value holds m = -inf and s = 0; a
-    // row of nothing but -inf has no distribution and gives NaN)
-    float s;
-    if constexpr (N > 0)
-      s = block_sum<T>(r.sum(x), sums, sampled);
+  }
+  if (POLICY && out != nullptr) {
+    if (T > 64) {
+      __syncthreads();
+      g = gsh;
+    }
+    if (g == 0.0f)
+      row_zero<E, T>(out, (int)a.ldd, a.stream);
+    else if constexpr (N > 0)
+      regs_grad<E, T, N>(r, zy, out, a.V, (int)a.ldd, at, label, x, s, g * a.tau, a.stream);
     else
-      s = block_sum<T>(o.shifted(x.far_x(o.m)), sums, sampled) * x.shift();
-    float g = 0.0f;
-    if (threadIdx.x < 64) {  // fp64, once: one wave
-      const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s, a.drift * kSample * join_ex<T>(sampled));
-      float loss, kl;
-      if (POLICY) g = policy_token(pa, t, lp, loss, kl);
-      if (threadIdx.x == 0) {
-        a.logp[t] = (float)lp;
-        if (a.stats != nullptr) {
-          a.stats[2 * t] = m;
-          a.stats[2 * t + 1] = s;
-        }
-        if (POLICY) {
-          gsh = g;
-          pa.loss[t] = loss;
-          if (pa.kl != nullptr) pa.kl[t] = kl;
-        }
-      }
-    }
-    if (POLICY && out != nullptr) {
-      if (T > 64) {
-        __syncthreads();
-        g = gsh;
-      }
-      if (g == 0.0f)
-        row_zero<E, T>(out, (int)a.ldd, a.stream);
-      else if constexpr (N > 0)
-        regs_grad<E, T, N>(r, out, a.V, (int)a.ldd, at, label, x, s, g * a.tau, a.stream);
-      else
-        row_grad<E, T>(z, out, a.V, (int)a.ldd, label, x, s, g * a.tau, a.stream);
-    }
-    if (T > 64) __syncthreads();  // red and gsh are written again for the next row
+      row_grad<E, T>(z, zy, out, a.V, (int)a.ldd, label, x, s, g * a.tau, a.stream);
   }
 }
 
@@ -577,17 +584,17 @@ __global__ __launch_bounds__(T, N < 0 ? 8 : 1) void k_rows(RowArgs a, PolicyArgs
 // 5.9 TB/s; V = 32000, two fifths uncounted: 67 us, 420 MB at 6.3 TB/s.
 template <typename E, int T>
 __global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __restrict__ dlogp) {
-  for (int64_t t = a.T - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
-    const int label = a.labels[t];
-    const float g = dlogp[t];
-    E* out = reinterpret_cast<E*>(a.dlogits) + t * a.ldd;
-    if (!is_counted(label, a.V) || g == 0.0f) {
-      row_zero<E, T>(out, (int)a.ldd, a.stream);
-    } else {
-      const RowExp x(a.stats[2 * t], a.c);
-      row_grad<E, T>(reinterpret_cast<const E*>(a.logits) + t * a.ld, out, a.V, (int)a.ldd, label, x,
-                     a.stats[2 * t + 1], g * a.tau, a.stream);
-    }
+  const int64_t t = a.first + gridDim.x - 1 - blockIdx.x;
+  const int label = a.labels[t];
+  const float g = dlogp[t];
+  E* out = reinterpret_cast<E*>(a.dlogits) + t * a.ldd;
+  if (!is_counted(label, a.V) || g == 0.0f) {
+    row_zero<E, T>(out, (int)a.ldd, a.stream);
+  } else {
+    const RowExp x(a.stats[2 * t], a.c);
+    const E* z = reinterpret_cast<const E*>(a.logits) + t * a.ld;
+    row_grad<E, T>(z, Elem<E>::get(z + label), out, a.V, (int)a.ldd, label, x, a.stats[2 * t + 1], g * a.tau,
+                   a.stream);
   }
 }
 
@@ -714,13 +721,17 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PrefArgs a) {
 
 // ---------------------------------------------------------- launchers ----
 
-// Work-groups of the row kernels: a row each, up to a grid whose thread count
-// stays below 2^32.
-static dim3 row_grid(int64_t T) { return dim3((unsigned)(T < (1 << 20) ? T : (1 << 20))); }
+// The row kernels' work-groups have a row each (in a loop over rows the fp64
+// logarithm's constants would stay in registers through the whole of it, 20 of
+// a thread's); a launch has up to 2^20 of them, below 2^32 threads.
+constexpr int64_t kRowsALaunch = (int64_t)1 << 20;
+static dim3 row_grid(const RowArgs& a) { return dim3((unsigned)std::min(a.T - a.first, kRowsALaunch)); }
 
 template <typename E, int T, int N, bool POLICY>
 static void rows_kernel(const char* name, const RowArgs& a, const PolicyArgs& pa, hipStream_t st) {
-  QLORA_LAUNCH(name, st, (k_rows<E, T, N, POLICY>), row_grid(a.T), dim3(T), 0, st, a, pa);
+  RowArgs b = a;
+  for (; b.first < b.T; b.first += kRowsALaunch)
+    QLORA_LAUNCH(name, st, (k_rows<E, T, N, POLICY>), row_grid(b), dim3(T), 0, st, b, pa);
 }
 
 // Threads a row and what each holds, by the row's number of 16-byte pieces.
@@ -761,19 +772,26 @@ static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyAr
   return hipGetLastError();
 }
 
+template <typename E, int T>
+static void grad_kernel(const RowArgs& a, const float* dlogp, hipStream_t st) {
+  RowArgs b = a;  // the last rows first here too
+  for (b.first = (a.T - 1) / kRowsALaunch * kRowsALaunch; b.first >= 0; b.first -= kRowsALaunch)
+    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, T>), row_grid(b), dim3(T), 0, st, b, dlogp);
+}
+
 // The same for the gradient alone, in pieces (V = 131072: 1024 threads 359 us,
 // 512 367, 256 381; V = 32000: 70, 68, 70).
 template <typename E>
 static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
   if (pieces <= 64 * 4)
-    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 64>), row_grid(a.T), dim3(64), 0, st, a, dlogp);
+    grad_kernel<E, 64>(a, dlogp, st);
   else if (pieces <= 256 * 4)
-    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 256>), row_grid(a.T), dim3(256), 0, st, a, dlogp);
+    grad_kernel<E, 256>(a, dlogp, st);
   else if (pieces <= 4096 && a.T >= 512)
-    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 512>), row_grid(a.T), dim3(512), 0, st, a, dlogp);
+    grad_kernel<E, 512>(a, dlogp, st);
   else
-    QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, 1024>), row_grid(a.T), dim3(1024), 0, st, a, dlogp);
+    grad_kernel<E, 1024>(a, dlogp, st);
   return hipGetLastError();
 }
 
@@ -788,7 +806,7 @@ static float exp2_drift(float tau) {
 
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                           float* logp, float* stats, hipStream_t st) {
-  const RowArgs a{logits, T, ld, 0, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, stats, nullptr, false};
+  const RowArgs a{logits, 0, T, ld, 0, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, stats, nullptr, false};
   return f32 ? launch_rows<float, false>("logprob", a, PolicyArgs{}, st)
              : launch_rows<uint16_t, false>("logprob", a, PolicyArgs{}, st);
 }
@@ -796,8 +814,8 @@ hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t
 hipError_t launch_logprob_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels,
                                float tau, const float* stats, const float* dlogp, void* dlogits, int64_t ldd,
                                hipStream_t st) {
-  const RowArgs a{logits, T,       ld,     ldd,  V, labels, tau, exp2_scale(tau), exp2_drift(tau), nullptr, const_cast<float*>(stats),
-                  dlogits, past_cache(T, ldd, f32)};
+  const RowArgs a{logits,  0, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), nullptr,
+                  const_cast<float*>(stats), dlogits, past_cache(T, ldd, f32)};
   return f32 ? launch_grad<float>(a, dlogp, st) : launch_grad<uint16_t>(a, dlogp, st);
 }
 
@@ -806,7 +824,7 @@ hipError_t launch_policy(const void* logits, int f32, int64_t T, int V, int64_t 
                          float clip_low, float clip_high, float kl_coef, float* loss, float* kl, float* logp,
                          void* dlogits, int64_t ldd, hipStream_t st) {
   const PolicyArgs pa{adv, old_logp, ref_logp, weight, 1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, kl};
-  const RowArgs a{logits, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, nullptr, dlogits,
+  const RowArgs a{logits, 0, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, nullptr, dlogits,
                   past_cache(T, ldd, f32)};
   return f32 ? launch_rows<float, true>("policy", a, pa, st) : launch_rows<uint16_t, true>("policy", a, pa, st);
 }

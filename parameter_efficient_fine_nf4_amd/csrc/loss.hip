@@ -342,9 +342,9 @@ __device__ __forceinline__ void row_end(float last, float zy, E* out, int V, int
 
 // z -> gradient over one row read from memory.  Where out is z, a thread
 // overwrites only what it has read.
-template <typename E, int T, bool FAR, bool STREAM>
+template <typename E, int T, int kBatch, bool FAR, bool STREAM>
 __device__ __forceinline__ void row_grad_of(const E* z, E* out, const RowSpan& at, const RowExp& x, float kappa) {
-  constexpr int kPer = Elem<E>::kPer16, kBatch = 4;  // pieces in flight
+  constexpr int kPer = Elem<E>::kPer16;
   int i = threadIdx.x;
   for (; i + (kBatch - 1) * T < at.nv; i += kBatch * T) {
     u32x4 w[kBatch];
@@ -354,13 +354,15 @@ __device__ __forceinline__ void row_grad_of(const E* z, E* out, const RowSpan& a
     for (int j = 0; j < kBatch; ++j)
       put16<STREAM>(out + at.head + (i + j * T) * kPer, grad_piece<E, FAR>(w[j], x, kappa));
   }
-#pragma unroll 1
-  for (; i < at.nv; i += T) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(z + at.head + i * kPer);
-    put16<STREAM>(out + at.head + i * kPer, grad_piece<E, FAR>(w, x, kappa));
-  }
+  u32x4 w[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (i + j * T < at.nv) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (i + j * T) * kPer);
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (i + j * T < at.nv) put16<STREAM>(out + at.head + (i + j * T) * kPer, grad_piece<E, FAR>(w[j], x, kappa));
 }
-template <typename E, int T>
+template <typename E, int T, int B>
 __device__ __forceinline__ void row_grad(const E* z, float zy, E* out, int V, int cols, int label, const RowExp& x,
                                          float s, float gt, bool stream) {
   const RowSpan at(z, V);
@@ -368,11 +370,11 @@ __device__ __forceinline__ void row_grad(const E* z, float zy, E* out, int V, in
   float last = kNegInf;
   if (at.rest < V) last = Elem<E>::get(z + at.rest);
   if (x.far)
-    row_grad_of<E, T, true, false>(z, out, at, x, kappa);
+    row_grad_of<E, T, B, true, false>(z, out, at, x, kappa);
   else if (stream)
-    row_grad_of<E, T, false, true>(z, out, at, x, kappa);
+    row_grad_of<E, T, B, false, true>(z, out, at, x, kappa);
   else
-    row_grad_of<E, T, false, false>(z, out, at, x, kappa);
+    row_grad_of<E, T, B, false, false>(z, out, at, x, kappa);
   row_end<E, T>(last, zy, out, V, cols, at, label, x, kappa, gt);
 }
 
@@ -492,11 +494,11 @@ struct RowArgs {
 // Log-probabilities, and with POLICY the policy loss and its gradient.  N > 0:
 // the row fits N pieces a thread; N < 0: -N pieces a thread at a time.
 //
-//
 // Bound by memory: the counted rows are read once and the gradient written
 // once.  T = 4093, V = 50021, fp32, a tenth uncounted: 119 us, 737 MB at 6.2
-// TB/s; T = 4096, V = 32000, bf16, a fifth uncounted, with the gradient: 91
-// us, 472 MB at 5.2 TB/s; V = 131071: 429 us, 2.04 GB at 4.8 TB/s.
+// TB/s; T = 4096, V = 32000, bf16, a fifth uncounted, with the gradient: 88
+// us, 472 MB at 5.4 TB/s; V = 131071, a tenth uncounted: 409 us, 2.04 GB at
+// 5.0 TB/s.
 template <typename E, int T, int N, bool POLICY>
 __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
   __shared__ float maxima[T / 64];
@@ -574,14 +576,14 @@ __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
     else if constexpr (N > 0)
       regs_grad<E, T, N>(r, zy, out, a.V, (int)a.ldd, at, label, x, s, g * a.tau, a.stream);
     else
-      row_grad<E, T>(z, zy, out, a.V, (int)a.ldd, label, x, s, g * a.tau, a.stream);
+      row_grad<E, T, 4>(z, zy, out, a.V, (int)a.ldd, label, x, s, g * a.tau, a.stream);
   }
 }
 
 // The rows go from the last to the first: the forward ended with the last
 // ones, and what of them is in the last-level cache is read from there.  Bound
-// by memory: T = 4096, V = 131072, bf16, a tenth uncounted: 347 us, 2.04 GB at
-// 5.9 TB/s; V = 32000, two fifths uncounted: 67 us, 420 MB at 6.3 TB/s.
+// by memory: T = 4096, V = 131072, bf16, a tenth uncounted: 338 us, 2.04 GB at
+// 6.0 TB/s; V = 32000, two fifths uncounted: 64 us, 420 MB at 6.5 TB/s.
 template <typename E, int T>
 __global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __restrict__ dlogp) {
   const int64_t t = a.first + gridDim.x - 1 - blockIdx.x;
@@ -593,7 +595,7 @@ __global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __re
   } else {
     const RowExp x(a.stats[2 * t], a.c);
     const E* z = reinterpret_cast<const E*>(a.logits) + t * a.ld;
-    row_grad<E, T>(z, Elem<E>::get(z + label), out, a.V, (int)a.ldd, label, x, a.stats[2 * t + 1], g * a.tau,
+    row_grad<E, T, T == 1024 ? 8 : 4>(z, Elem<E>::get(z + label), out, a.V, (int)a.ldd, label, x, a.stats[2 * t + 1], g * a.tau,
                    a.stream);
   }
 }
@@ -736,19 +738,22 @@ static void rows_kernel(const char* name, const RowArgs& a, const PolicyArgs& pa
 
 // Threads a row and what each holds, by the row's number of 16-byte pieces.
 // One wave takes a short row without a barrier.  Up to one row per CU a row's
-// own latency counts: the most threads.  With more rows 256 threads with a
-// row in registers that fits closely (pieces that do not exist cost their
-// exponentials all the same).  Measured on 4096 rows of bf16 (us,
+// own latency counts: the most threads.  With more rows the row in registers,
+// as closely as it fits (pieces that do not exist cost their exponentials all
+// the same), as long as a CU holds several rows; beyond that the
+// log-probabilities read in pieces, two rows a CU, while the gradient gains
+// more from not reading the row again.  Measured on 4096 rows (us,
 // log-probabilities / policy loss and gradient):
-//   V = 20000, 2500 pieces:   256 x 10 29 / 60, 256 x 16 36 / 74, 512 x 8 41 /
-//                             73, in pieces 256 x 4 32 / 76;
-//   V = 32000, 4000 pieces:   256 x 16 44 / 102, 512 x 8 48 / 98, in pieces 512
-//                             x 4 44 / 109;
-//   V = 131072, 16384 pieces: 1024 x 16 214 / 496 (one row a CU, nothing to
-//                             load while it computes), in pieces 1024 x 4
-//                             161 / 430 (two rows a CU), 512 x 4 172 / 485,
-//                             1024 x 2 164 / 434 (the second reading comes
-//                             from the last-level cache).
+//   bf16, V = 32000, 4000 pieces:   512 x 8 46 / 94, 256 x 16 48 / 97;
+//   bf16, V = 40000, 5000 pieces:   512 x 10 56 / 119, 512 x 16 70 / 120, in
+//                                   pieces 1024 x 4 78 / 150;
+//   bf16, V = 65536, 8192 pieces:   512 x 16 90 / 196, in pieces 87 / 227;
+//   bf16, V = 70000, 8750 pieces:   1024 x 12 - / 264, in pieces 107 / 250;
+//   fp32, V = 50000, 12500 pieces:  1024 x 16 - / 312, in pieces 134 / 353;
+//   bf16, V = 131072, 16384 pieces: 1024 x 16 220 / 437, 512 x 32 230 / 440,
+//                                   in pieces 1024 x 4 176 / 456, 1024 x 8 178
+//                                   / -, 512 x 4 183 / 520 (the second reading
+//                                   comes from the last-level cache).
 template <typename E, bool POLICY>
 static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyArgs& pa, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
@@ -765,8 +770,18 @@ static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyAr
     rows_kernel<E, 256, 10, POLICY>(name, a, pa, st);
   else if (pieces <= 256 * 12)
     rows_kernel<E, 256, 12, POLICY>(name, a, pa, st);
-  else if (pieces <= 4096)
-    rows_kernel<E, POLICY ? 512 : 256, POLICY ? 8 : 16, POLICY>(name, a, pa, st);
+  else if (pieces <= 512 * 8)
+    rows_kernel<E, 512, 8, POLICY>(name, a, pa, st);
+  else if (pieces <= 512 * 10)
+    rows_kernel<E, 512, 10, POLICY>(name, a, pa, st);
+  else if (pieces <= 512 * 12)
+    rows_kernel<E, 512, 12, POLICY>(name, a, pa, st);
+  else if (pieces <= 512 * 16)
+    rows_kernel<E, 512, 16, POLICY>(name, a, pa, st);
+  else if (POLICY && pieces > 1024 * 9 && pieces <= 1024 * 12)
+    rows_kernel<E, 1024, 12, true>(name, a, pa, st);
+  else if (POLICY && pieces > 1024 * 9 && pieces <= 1024 * 16)
+    rows_kernel<E, 1024, 16, true>(name, a, pa, st);
   else
     rows_kernel<E, 1024, -4, POLICY>(name, a, pa, st);
   return hipGetLastError();
@@ -779,8 +794,10 @@ static void grad_kernel(const RowArgs& a, const float* dlogp, hipStream_t st) {
     QLORA_LAUNCH("logprob_grad", st, (k_logprob_grad<E, T>), row_grid(b), dim3(T), 0, st, b, dlogp);
 }
 
-// The same for the gradient alone, in pieces (V = 131072: 1024 threads 359 us,
-// 512 367, 256 381; V = 32000: 70, 68, 70).
+// The same for the gradient alone, in pieces, four of a thread's loads in
+// flight, eight with 1024 threads (V = 131072: 1024 threads 338 us, with four
+// loads 346, 512 threads 353, 256 375; V = 32000: 512 threads 64, 1024 66, 256
+// 69).
 template <typename E>
 static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;

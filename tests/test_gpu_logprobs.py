@@ -486,3 +486,64 @@ def test_logprobs_do_not_drift(lib, T, V, dtype, tau):
     want = torch.cat([(r.double() * tau).log_softmax(1)[torch.arange(len(r), device=DEV), i.long()]
                       for r, i in zip(z.split(256), y.split(256))])
     assert abs((logp.double() - want).mean().item()) <= U + 6 * 2.0 ** -21 / (3 * T) ** 0.5
+
+
+# a row in one wave, in 256, 512 and 1024 threads' registers of each width, and in pieces
+FORMS = [(BF, v) for v in (2001, 4001, 8150, 14001, 20009, 24500, 32011, 40007, 48011, 65530, 70001, 98000, 131071,
+                           140000)] + [(F32, v) for v in (1003, 12003, 20011, 32000, 48011, 65535, 70001)]
+
+
+@pytest.mark.parametrize("dtype,V", FORMS, ids=lambda x: str(x).split(".")[-1])
+def test_every_form_of_a_row(lib, dtype, V):
+    # more rows than a CU has to itself, with a policy of its own (ratio 1: the
+    # gradient of -A r is -A) beside the log-probabilities; in place as well
+    _case("forms", dtype, V)
+    T, tau = 261, 0.8
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = (2 * torch.randn(T, V, device=DEV, generator=g)).to(dtype)
+    z[7, 5:] = -float("inf")
+    y = torch.randint(0, V, (T,), device=DEV, generator=g, dtype=torch.int32)
+    y[::9], y[1], y[2], y[7] = -1, 0, V - 1, 3
+    adv = torch.randn(T, device=DEV, generator=g)
+    logp, stats = lib.token_logprobs(z, y, tau, save_stats=True)
+    dz = lib.token_logprobs_backward(adv, z, y, stats, tau)
+    loss, _, plogp, pdz = lib.policy_loss(z, y, -adv, inv_temperature=tau)
+    zz = z.clone()
+    assert torch.equal(lib.token_logprobs_backward(adv, zz, y, stats, tau, out=zz), dz)
+    zz.copy_(z)
+    assert torch.equal(lib.policy_loss(zz, y, -adv, inv_temperature=tau, out=zz)[3], pdz)
+    tau = float(np.float32(tau))
+    for r in range(0, T, 29):
+        t = tau * (z[r:r + 29].double() - z[r:r + 29].double().amax(1, keepdim=True))
+        yy = y[r:r + 29].long()
+        c = yy >= 0
+        ty = t.gather(1, yy.clamp(min=0)[:, None])[:, 0]
+        want = torch.where(c, ty - t.logsumexp(1), 0)
+        bound = U * (12 * (np.log(V) + 1) + V / 256 + 32 + 3 * ty.abs() + want.abs())
+        p = t.softmax(1)
+        onehot = torch.zeros_like(p).scatter_(1, yy.clamp(min=0)[:, None], 1.0)
+        a = adv[r:r + 29].double()
+        dwant = (a * tau * c)[:, None] * (onehot - p)
+        half = torch.finfo(dtype).eps / 2
+        dbound = (a.abs() * tau)[:, None] * (3 * U + p * bound[:, None]) + (4 * U + half) * dwant.abs() + 1e-37
+        for lp, d in ((logp, dz), (plogp, pdz)):
+            assert ((lp[r:r + 29].double() - want).abs() <= bound).all()
+            assert ((d[r:r + 29].double() - dwant).abs() <= dbound).all()
+    assert torch.equal(loss, torch.where(y >= 0, adv, 0))
+
+
+def test_more_rows_than_a_launch_takes(lib):
+    _case("2^20 + 37 rows")
+    T, cut = (1 << 20) + 37, 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.randn(T, 9, device=DEV, generator=g).bfloat16()
+    y = torch.randint(-1, 9, (T,), device=DEV, generator=g, dtype=torch.int32)
+    adv = torch.randn(T, device=DEV, generator=g)
+
+    def calls(z, y, adv):
+        logp, stats = lib.token_logprobs(z, y, save_stats=True)
+        return (logp, stats, lib.token_logprobs_backward(adv, z, y, stats)) + lib.policy_loss(z, y, adv)
+
+    for got, a, b in zip(calls(z, y, adv), calls(z[:cut], y[:cut], adv[:cut]),
+                         calls(z[cut:].clone(), y[cut:].clone(), adv[cut:].clone())):
+        assert torch.equal(got[:cut], a) and torch.equal(got[cut:], b)

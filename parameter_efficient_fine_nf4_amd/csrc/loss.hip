@@ -30,6 +30,7 @@
 // for the gradient.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -815,10 +816,11 @@ static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t 
 // Half of the 256 MB last-level cache.
 static bool past_cache(int64_t T, int64_t ldd, int f32) { return T * ldd * (f32 ? 4 : 2) > ((int64_t)128 << 20); }
 
-static float exp2_scale(float tau) { return (float)((double)tau * kLog2e); }
+// (finite for every finite tau: the row's maximum has 0 times it)
+static float exp2_scale(float tau) { return std::min((float)((double)tau * kLog2e), std::numeric_limits<float>::max()); }
 static float exp2_drift(float tau) {
-  const double c = exp2_scale(tau);
-  return c > 0.0 && std::isfinite(c) ? (float)(kLn2 * ((double)tau * kLog2e / c - 1.0)) : 0.0f;
+  const double c = exp2_scale(tau), off = (double)tau * kLog2e / c - 1.0;
+  return off < 1e-6 ? (float)(kLn2 * off) : 0.0f;
 }
 
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,

@@ -186,7 +186,7 @@ def test_masked_and_extreme_values(lib, V, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("V", [40, 5000, 30000, 150000])
 @pytest.mark.parametrize("size,tau", [(1e6, 1.0), (3e8, 1.0), (1e25, 1.0), (1e3, 1e9), (1.0, 1e12), (1e30, 1e30),
-                                      (1e6, 1e-6), (1.0, 1e-30)])
+                                      (1e6, 1e-6), (1.0, 1e-30), (1.0, 3.3e38), (1.0, 1e-40)])
 def test_large_logits_and_temperatures(lib, V, dtype, size, tau):
     # exponents far past 2^20, where the maximum's own rounding is a large
     # exponent; a maximum that the top few share

@@ -100,3 +100,46 @@ def test_policy_step_of_an_adapted_head_in_place(lib):
     dX, dA, dB = lib.backward(dY, H.X, H.w, H.A, H.B, H.alpha)
     dXr, dAr, dBr = O.backward(bits_host(dY), H.inp["X"], H.Wt, H.inp["A"], H.inp["B"], H.alpha)
     assert rel(bits_host(dX), dXr) <= 1e-2 and rel(bits_host(dA), dAr) <= 2e-2 and rel(bits_host(dB), dBr) <= 2e-2
+
+
+def test_preference_steps_captured(lib):
+    # whole steps replayed from a graph, between eager ones on a second copy of the adapter: the same bits each time
+    d, k, r, M, V = 512, 256, 16, 64, 500
+    print("case: captured preference steps", d, k, r, M, V, flush=True)
+    H = Layer(lib, d, k, r, M, cfg=83)
+    y = torch.randint(0, V, (M,), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(DEV)
+    cu = torch.tensor([0, 20, 31, 50, 64], dtype=torch.int32, device=DEV)
+
+    def state():
+        f = [H.A.clone(), H.B.clone()]
+        return f + [p.float() for p in f] + [torch.zeros_like(p, dtype=torch.float32) for p in f]
+
+    def step(s):
+        A, B, WA, WB, mA, mB = s
+        ref = lib.token_logprobs(lib.forward(H.X, H.w)[:, :V], y)
+        logits, T = lib.forward(H.X, H.w, A, B, H.alpha, save_t=True)
+        logp, stats = lib.token_logprobs(logits[:, :V], y, save_stats=True)
+        _, _, dlogp = lib.preference_loss(logp, y, V, cu, 0.5, ref_logp=ref)
+        lib.token_logprobs_backward(dlogp, logits[:, :V], y, stats, out=logits[:, :V])
+        _, dA, dB = lib.backward(logits, H.X, H.w, A, B, H.alpha, T_saved=T)
+        lib.muon_step(A, WA, dA, mA, lr=0.01)
+        lib.muon_step(B, WB, dB, mB, lr=0.01)
+
+    eager, replayed, warm = state(), state(), state()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(warm)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(replayed)
+    for n in range(4):
+        step(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, eager)), n
+    assert not torch.equal(eager[0], H.A) and torch.isfinite(eager[2]).all()

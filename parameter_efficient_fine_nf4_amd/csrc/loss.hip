@@ -596,8 +596,8 @@ __global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __re
   } else {
     const RowExp x(a.stats[2 * t], a.c);
     const E* z = reinterpret_cast<const E*>(a.logits) + t * a.ld;
-    row_grad<E, T, T == 1024 ? 8 : 4>(z, Elem<E>::get(z + label), out, a.V, (int)a.ldd, label, x, a.stats[2 * t + 1], g * a.tau,
-                   a.stream);
+    row_grad<E, T, T == 1024 ? 8 : 4>(z, Elem<E>::get(z + label), out, a.V, (int)a.ldd, label, x, a.stats[2 * t + 1],
+                                      g * a.tau, a.stream);
   }
 }
 
@@ -612,11 +612,11 @@ __global__ __launch_bounds__(T) void k_logprob_grad(RowArgs a, const float* __re
 //   hinge    max(0, 1 - h)
 //   squared  (D - margin/beta - 1/(2 beta))^2  = ((h - 1/2) / beta)^2
 //
-// A work-group takes a pair: it sums in fp64 (thousands of terms, of which a
-// small difference is left) and writes each token's d loss / d logp.  Bound by
-// the latency of its few dependent loads and barriers (8 pairs of 4096 tokens
-// in all: 5 us, 80 KB).
-constexpr int kPrefThreads = 256;
+// A work-group takes a pair, a half of it a sequence: it sums in fp64
+// (thousands of terms, of which a small difference is left) and writes each
+// token's d loss / d logp.  Bound by the latency of its few dependent loads
+// and barriers (8 pairs of 4096 tokens in all: 6 us, 80 KB).
+constexpr int kPrefThreads = 512, kPrefHalf = kPrefThreads / 2;
 
 struct PrefArgs {
   const float* logp;
@@ -642,43 +642,55 @@ __device__ __forceinline__ void seq_range(const PrefArgs& a, int64_t s, int64_t&
 }
 
 __global__ __launch_bounds__(kPrefThreads) void k_preference(PrefArgs a) {
-  __shared__ double sums[2][kPrefThreads / 64];
-  __shared__ int counts[2][kPrefThreads / 64];
+  constexpr int W = kPrefHalf / 64;
+  __shared__ double sums[2 * W];
+  __shared__ int counts[2 * W];
   const int64_t p = blockIdx.x;
-  int64_t lo[2], hi[2];
-  seq_range(a, p, lo[0], hi[0]);
-  seq_range(a, a.P + p, lo[1], hi[1]);
+  const int k = threadIdx.x / kPrefHalf, i = threadIdx.x % kPrefHalf;  // chosen: 0, rejected: 1
+  int64_t lo, hi;
+  seq_range(a, k * a.P + p, lo, hi);
+  double sum = 0.0;
+  int n = 0;
+  for (int64_t t0 = lo + i; t0 < hi; t0 += 4 * kPrefHalf) {
+    int label[4];
+    float lp[4], ref[4];  // in flight
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    double sum = 0.0;
-    int n = 0;
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPrefThreads) {
-      if (is_counted(a.labels[t], a.V)) {
-        sum += a.ref_logp != nullptr ? (double)a.logp[t] - (double)a.ref_logp[t] : (double)a.logp[t];
-        ++n;
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = t0 + j * kPrefHalf;
+      label[j] = -1;
+      if (t < hi) {
+        label[j] = a.labels[t];
+        lp[j] = a.logp[t];
+        ref[j] = a.ref_logp != nullptr ? a.ref_logp[t] : 0.0f;
       }
     }
-    for (int o = 32; o >= 1; o >>= 1) {
-      sum += __shfl_xor(sum, o, 64);
-      n += __shfl_xor(n, o, 64);
-    }
-    if ((threadIdx.x & 63) == 0) {
-      sums[k][threadIdx.x >> 6] = sum;
-      counts[k][threadIdx.x >> 6] = n;
-    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (is_counted(label[j], a.V)) {
+        sum += (double)lp[j] - (double)ref[j];
+        ++n;
+      }
+  }
+  for (int o = 32; o >= 1; o >>= 1) {
+    sum += __shfl_xor(sum, o, 64);
+    n += __shfl_xor(n, o, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sums[threadIdx.x >> 6] = sum;
+    counts[threadIdx.x >> 6] = n;
   }
   __syncthreads();
   double l[2], inv[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    l[k] = 0.0;
-    int n = 0;
-    for (int w = 0; w < kPrefThreads / 64; ++w) {
-      l[k] += sums[k][w];
-      n += counts[k][w];
+  for (int q = 0; q < 2; ++q) {
+    l[q] = 0.0;
+    int c = 0;
+    for (int w = 0; w < W; ++w) {
+      l[q] += sums[q * W + w];
+      c += counts[q * W + w];
     }
-    inv[k] = a.average ? 1.0 / (double)(n > 1 ? n : 1) : 1.0;
-    l[k] *= inv[k];
+    inv[q] = a.average ? 1.0 / (double)(c > 1 ? c : 1) : 1.0;
+    l[q] *= inv[q];
   }
   const double beta = a.beta, e = a.smoothing;
   const double h = beta * (l[0] - l[1]) - a.margin;
@@ -709,17 +721,13 @@ __global__ __launch_bounds__(kPrefThreads) void k_preference(PrefArgs a) {
     }
   }
   if (a.dlogp == nullptr) return;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float g = (float)((k == 0 ? dl : -dl) * inv[k]);
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPrefThreads)
-      a.dlogp[t] = is_counted(a.labels[t], a.V) ? g : 0.0f;
-  }
+  const float g = (float)(k == 0 ? dl * inv[0] : -dl * inv[1]);
+  for (int64_t t = lo + i; t < hi; t += kPrefHalf) a.dlogp[t] = is_counted(a.labels[t], a.V) ? g : 0.0f;
   // tokens before the first sequence and after the last have no gradient
-  if (p == 0)
-    for (int64_t t = threadIdx.x; t < lo[0]; t += kPrefThreads) a.dlogp[t] = 0.0f;
-  if (p == a.P - 1)
-    for (int64_t t = hi[1] + threadIdx.x; t < a.T; t += kPrefThreads) a.dlogp[t] = 0.0f;
+  if (p == 0 && k == 0)
+    for (int64_t t = i; t < lo; t += kPrefHalf) a.dlogp[t] = 0.0f;
+  if (p == a.P - 1 && k == 1)
+    for (int64_t t = hi + i; t < a.T; t += kPrefHalf) a.dlogp[t] = 0.0f;
 }
 
 // ---------------------------------------------------------- launchers ----

@@ -625,7 +625,7 @@ __global__ __launch_bounds__(64 * kPolyWaves) void k_muon_poly(const double* __r
 //             4 (l / 16) + c of position l % 16; D: short indexes 16 t + 4 (l /
 //             16) + q of that position) in LDS of the wave's own.  Loaded in
 //             the operands' order, rows of 64 took 222 us where this takes
-//             133 (80 x 8192 x 64).
+//             108 (80 x 8192 x 64).
 //
 // Q is in LDS (64 x 64 of it would take the registers of the loads in flight),
 // in rows of a stride that puts an operand's four rows, next to each other or

@@ -410,9 +410,11 @@ __device__ __forceinline__ PolyTile poly_tile(int turn, int e) {
   return PolyTile{u, u - t2 * (t2 + 1) / 2, t2};
 }
 
-// The wave's tiles of x y, handed element by element to f(q, i, k, value).
-template <int NT, typename F>
-__device__ __forceinline__ void poly_mul(int turn, const double* x, const double* y, F f) {
+// The wave's tiles of x y, handed element by element to f(q, i, k, value,
+// add(i, k)); add is called before the products, so that the LDS reads in it
+// do not wait for f's writes one by one (S = 32: 18.1 us, 16.9 so).
+template <int NT, typename A, typename F>
+__device__ __forceinline__ void poly_mul(int turn, const double* x, const double* y, A add, F f) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int e = 0; e < kPolyTiles<NT>; ++e) {
@@ -421,12 +423,15 @@ __device__ __forceinline__ void poly_mul(int turn, const double* x, const double
     // row lane / 16; row + 4 k differs in bits 2 and 3 of the column
     const int xo = PolyLds<NT>::at(lane / 16, 16 * p.t + (lane & 15));
     const int yo = PolyLds<NT>::at(lane / 16, 16 * p.t2 + (lane & 15));
+    double more[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) more[q] = add(16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15));
     f64x4 acc = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
     for (int k = 0; k < 4 * NT; ++k)
       acc = mfma_f64(x[(xo ^ (4 * (k & 3))) + k * 64 * NT], y[(yo ^ (4 * (k & 3))) + k * 64 * NT], acc);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) f(4 * e + q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), acc[q]);
+    for (int q = 0; q < 4; ++q) f(4 * e + q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), acc[q], more[q]);
   }
 }
 
@@ -449,6 +454,7 @@ __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double
                                          float* out, int S) {
   using At = PolyLds<NT>;
   constexpr int N = At::N, U = mu_tiles(NT), kThreads = 64 * kPolyWaves;
+  const auto none = [](int, int) { return 0.0; };
   const int lane = threadIdx.x & 63;
   double trace = lane < N ? G[At::at(lane, lane)] : 0.0;
 #pragma unroll
@@ -461,15 +467,17 @@ __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double
   for (int n = 0; n < co.n; ++n) {
     const double ca = co.c[n][0], cb = co.c[n][1], cc = co.c[n][2];
     const bool last = n + 1 == co.n;
-    poly_mul<NT>(0, G, G, [&](int, int i, int k, double v) {
-      const double p = fma(cc, v, fma(cb, G[At::at(i, k)], i == k ? ca : 0.0));
-      poly_put<NT>(P, i, k, p);
-      if (n == 0) poly_put<NT>(Q, i, k, p);
-    });
+    poly_mul<NT>(
+        0, G, G, [&](int i, int k) { return fma(cb, G[At::at(i, k)], i == k ? ca : 0.0); },
+        [&](int, int i, int k, double v, double add) {
+          const double p = fma(cc, v, add);
+          poly_put<NT>(P, i, k, p);
+          if (n == 0) poly_put<NT>(Q, i, k, p);
+        });
     __syncthreads();
     double hold[4 * kPolyTiles<NT>];  // P Q, until every wave has read Q
-    if (n > 0) poly_mul<NT>(0, P, Q, [&](int e, int, int, double v) { hold[e] = v; });
-    if (!last) poly_mul<NT>(1, P, G, [&](int, int i, int k, double v) { poly_put<NT>(R, i, k, v); });
+    if (n > 0) poly_mul<NT>(0, P, Q, none, [&](int e, int, int, double v, double) { hold[e] = v; });
+    if (!last) poly_mul<NT>(1, P, G, none, [&](int, int i, int k, double v, double) { poly_put<NT>(R, i, k, v); });
     __syncthreads();
     if (n > 0) {
 #pragma unroll
@@ -481,7 +489,7 @@ __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double
           poly_put<NT>(Q, 16 * p.t + lane / 16 + 4 * q, 16 * p.t2 + (lane & 15), hold[4 * e + q]);
       }
     }
-    if (!last) poly_mul<NT>(0, R, P, [&](int, int i, int k, double v) { poly_put<NT>(G, i, k, v); });
+    if (!last) poly_mul<NT>(0, R, P, none, [&](int, int i, int k, double v, double) { poly_put<NT>(G, i, k, v); });
     __syncthreads();
   }
   for (int e = threadIdx.x; e < N * N; e += kThreads) {

@@ -547,3 +547,25 @@ def test_more_rows_than_a_launch_takes(lib):
     for got, a, b in zip(calls(z, y, adv), calls(z[:cut], y[:cut], adv[:cut]),
                          calls(z[cut:].clone(), y[cut:].clone(), adv[cut:].clone())):
         assert torch.equal(got[:cut], a) and torch.equal(got[cut:], b)
+
+
+def test_logits_past_4_gib(lib):
+    # element offsets past 2^31, byte offsets past 2^32: the last rows give what they give alone
+    T, V = 17000, 131072
+    _case("large offsets", T, V)
+    z = torch.empty(T, V, dtype=BF, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    z[-3:] = torch.randn(3, V, device=DEV, generator=g).to(BF)
+    y = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    y[-3:] = torch.tensor([5, V - 1, 77777], dtype=torch.int32, device=DEV)
+    adv = torch.ones(T, device=DEV)
+    few = z[-3:].clone()
+    logp, stats = lib.token_logprobs(z, y, save_stats=True)
+    flogp, fstats = lib.token_logprobs(few, y[-3:].clone(), save_stats=True)
+    assert torch.equal(logp[-3:], flogp) and torch.equal(stats[-3:], fstats) and torch.all(logp[:-3] == 0)
+    assert torch.isfinite(flogp).all()
+    dz = lib.token_logprobs_backward(adv, z, y, stats)
+    assert torch.equal(dz[-3:], lib.token_logprobs_backward(adv[-3:], few, y[-3:].clone(), fstats))
+    assert not dz[:-3].any()
+    pdz = lib.policy_loss(z, y, adv, out=dz)[3]
+    assert torch.equal(pdz[-3:], lib.policy_loss(few, y[-3:].clone(), adv[-3:])[3]) and not pdz[:-3].any()

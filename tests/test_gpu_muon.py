@@ -235,3 +235,38 @@ def test_muon_on_two_streams_at_once(lib):
     torch.cuda.synchronize()
     for s, e in zip(states, eager):
         assert all(torch.equal(a, b) for a, b in zip(s, e))
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 8388600), (8388480, 63)])
+def test_muon_largest_matrix(lib, rows, cols):
+    # just below 2^29 elements, offsets of 2 GiB: the ends of the long axis against the formula in float64.  With no
+    # decay and no weights before, w = -lr scale X, off by Q's and the products' roundings, S + 8 half steps of
+    # sum |Q| |u| / |u|, and two of its own.
+    _case("muon largest", rows, cols)
+    short, tall, lr, mu = min(rows, cols), rows > cols, 0.01, float(np.float32(0.95))
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    G = torch.randn(rows, cols, device=DEV, generator=gen, dtype=torch.bfloat16)
+    m, W = (torch.zeros(rows, cols, device=DEV) for _ in range(2))
+    P = torch.empty(rows, cols, device=DEV, dtype=torch.bfloat16)
+    lib.muon_step(P, W, G, m, lr=lr, scale=1.0)
+    update = lambda g: (g.float() + mu * g.float()).double()  # noqa: E731
+    axis = 0 if tall else 1
+    gram = torch.zeros(short, short, device=DEV, dtype=torch.float64)
+    for part in G.split(1 << 19, dim=axis):
+        u = update(part)
+        gram += u.t() @ u if tall else u @ u.t().contiguous()
+    norm = gram.trace().sqrt()
+    g, eye = gram / norm ** 2, torch.eye(short, device=DEV, dtype=torch.float64)
+    q = eye
+    for _ in range(5):
+        a, b, c = (float(np.float32(v)) for v in S.USUAL)
+        p = a * eye + b * g + c * g @ g
+        q, g = p @ q, p @ g @ p
+    n = 1000
+    for at in (0, max(rows, cols) - n):
+        u, w, pp = (update(G.narrow(axis, at, n)), W.narrow(axis, at, n).double(), P.narrow(axis, at, n))
+        want = -lr * (u @ q if tall else q @ u) / norm
+        size = lr * (u.abs() @ q.abs() if tall else q.abs() @ u.abs()) / norm
+        assert ((w - want).abs() <= U * ((short + 8) * size + 2 * want.abs())).all()
+        assert torch.equal(pp, w.float().bfloat16())
+    assert torch.equal(m, G.float())

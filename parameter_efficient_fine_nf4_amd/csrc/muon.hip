@@ -111,7 +111,14 @@ __device__ __forceinline__ void load_f(const float* p, uint32_t at, int n, float
 }
 template <bool VEC, int N>
 __device__ __forceinline__ void load_h(const uint16_t* p, uint32_t at, int n, Halves<N>& v) {
-  if constexpr (VEC) {
+  if constexpr (VEC && N == 3) {
+    // 4 and 2 bytes: the compiler reads a vector of three as four, which past a
+    // matrix's last three is past the end of G; and a copy of 6 bytes into two
+    // registers goes through scratch memory
+    const typename Vec<2>::H x = lane_at<const typename Vec<2>::H>(p, at);
+    __builtin_memcpy(v.w, &x, 4);
+    v.w[1] = lane_at<const uint16_t>(p, at + 2);
+  } else if constexpr (VEC) {
     const typename Vec<N>::H x = lane_at<const typename Vec<N>::H>(p, at);
     v.w[(N - 1) / 2] = 0;
     __builtin_memcpy(v.w, &x, N * 2);

@@ -87,11 +87,13 @@ __device__ __forceinline__ int clamp_at(int i, int n) { return i < n ? i : (n > 
 // An access is a wave-uniform base (scalar registers) plus a lane's 32-bit
 // offset in elements: row and step go into the base, so that the many rows of
 // a step in flight take no vector registers for addresses.  A matrix has
-// fewer than 2^29 elements.
-template <typename T, typename E>
-__device__ __forceinline__ T& lane_at(E* base, uint32_t at) {
+// fewer than 2^29 elements.  Vectors are accessed by casts of the pointer to
+// their types in place: a type's alignment is lost where the type is a
+// template argument.
+template <typename E>
+__device__ __forceinline__ E* lane_at(E* base, uint32_t at) {
   typedef typename std::conditional<std::is_const<E>::value, const char, char>::type B;
-  return *reinterpret_cast<T*>(reinterpret_cast<B*>(base) + at * (uint32_t)sizeof(E));
+  return reinterpret_cast<E*>(reinterpret_cast<B*>(base) + at * (uint32_t)sizeof(E));
 }
 
 // STREAM (with VEC): past the caches.
@@ -100,13 +102,13 @@ __device__ __forceinline__ void load_f(const float* p, uint32_t at, int n, float
   if constexpr (VEC) {
     typename Vec<N>::F x;
     if constexpr (STREAM)
-      x = __builtin_nontemporal_load(&lane_at<const typename Vec<N>::F>(p, at));
+      x = __builtin_nontemporal_load(reinterpret_cast<const typename Vec<N>::F*>(lane_at(p, at)));
     else
-      x = lane_at<const typename Vec<N>::F>(p, at);
+      x = *reinterpret_cast<const typename Vec<N>::F*>(lane_at(p, at));
     __builtin_memcpy(v, &x, N * 4);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane_at<const float>(p, at + clamp_at(i, n));
+    for (int i = 0; i < N; ++i) v[i] = *lane_at(p, at + clamp_at(i, n));
   }
 }
 template <bool VEC, int N>
@@ -115,18 +117,18 @@ __device__ __forceinline__ void load_h(const uint16_t* p, uint32_t at, int n, Ha
     // 4 and 2 bytes: the compiler reads a vector of three as four, which past a
     // matrix's last three is past the end of G; and a copy of 6 bytes into two
     // registers goes through scratch memory
-    const typename Vec<2>::H x = lane_at<const typename Vec<2>::H>(p, at);
+    const typename Vec<2>::H x = *reinterpret_cast<const typename Vec<2>::H*>(lane_at(p, at));
     __builtin_memcpy(v.w, &x, 4);
-    v.w[1] = lane_at<const uint16_t>(p, at + 2);
+    v.w[1] = *lane_at(p, at + 2);
   } else if constexpr (VEC) {
-    const typename Vec<N>::H x = lane_at<const typename Vec<N>::H>(p, at);
+    const typename Vec<N>::H x = *reinterpret_cast<const typename Vec<N>::H*>(lane_at(p, at));
     v.w[(N - 1) / 2] = 0;
     __builtin_memcpy(v.w, &x, N * 2);
   } else {
 #pragma unroll
     for (int i = 0; i < (N + 1) / 2; ++i)
-      v.w[i] = (uint32_t)lane_at<const uint16_t>(p, at + clamp_at(2 * i, n)) |
-               (uint32_t)lane_at<const uint16_t>(p, at + clamp_at(2 * i + 1, n)) << 16;
+      v.w[i] = (uint32_t)*lane_at(p, at + clamp_at(2 * i, n)) |
+               (uint32_t)*lane_at(p, at + clamp_at(2 * i + 1, n)) << 16;
   }
 }
 template <bool VEC, bool STREAM, int N>
@@ -136,14 +138,14 @@ __device__ __forceinline__ void store_f(float* p, uint32_t at, int n, const floa
       typename Vec<N>::F x;
       __builtin_memcpy(&x, v, N * 4);
       if constexpr (STREAM)
-        __builtin_nontemporal_store(x, &lane_at<typename Vec<N>::F>(p, at));
+        __builtin_nontemporal_store(x, reinterpret_cast<typename Vec<N>::F*>(lane_at(p, at)));
       else
-        lane_at<typename Vec<N>::F>(p, at) = x;
+        *reinterpret_cast<typename Vec<N>::F*>(lane_at(p, at)) = x;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) lane_at<float>(p, at + i) = v[i];
+      if (i < n) *lane_at(p, at + i) = v[i];
   }
 }
 template <bool VEC, bool STREAM, int N>
@@ -156,14 +158,14 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, uint32_t at, int n, cons
       typename Vec<N>::H x;
       __builtin_memcpy(&x, h, N * 2);
       if constexpr (STREAM)
-        __builtin_nontemporal_store(x, &lane_at<typename Vec<N>::H>(p, at));
+        __builtin_nontemporal_store(x, reinterpret_cast<typename Vec<N>::H*>(lane_at(p, at)));
       else
-        lane_at<typename Vec<N>::H>(p, at) = x;
+        *reinterpret_cast<typename Vec<N>::H*>(lane_at(p, at)) = x;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) lane_at<uint16_t>(p, at + i) = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
+      if (i < n) *lane_at(p, at + i) = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
   }
 }
 __device__ __forceinline__ int room(int end, int at) { return at < end ? end - at : 0; }

@@ -46,3 +46,11 @@ def test_three_values_are_read_as_three(muon_ir):
     bits = {n * int(e[1:]) for o, n, e, _ in seen if o == "load" and e[0] == "i"}
     assert bits == {16, 32}, bits
     assert "alloca" not in muon_ir[name]
+
+
+def test_no_access_claims_more_than_an_elements_alignment(muon_ir):
+    # rows of an odd length start at any multiple of their element's size: 4 bytes for fp32, 2 for bf16 (which the IR
+    # has as integers); the partial sums are fp64
+    most = {"float": 4, "double": 8}
+    wrong = {(name, *a) for name, body in muon_ir.items() for a in _accesses(body) if a[3] > most.get(a[2], 2)}
+    assert not wrong, sorted(wrong)[:5]

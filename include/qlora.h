@@ -463,7 +463,9 @@ int qlora_preference_loss(const float *logp, const float *ref_logp, const int32_
  * and 0 for tokens that are not counted.
  *
  *   old_logp device, T fp32, or NULL: the policy itself (r = 1).
- *   ref_logp device, T fp32, or NULL: no KL term (kl is then 0).
+ *   ref_logp device, T fp32, or NULL: no KL term (kl is then 0).  With
+ *            kl_coef 0 the term takes no part in loss and gradient whatever
+ *            kl is (exp(x) past fp32 is an infinite one).
  *   weight   device, T fp32, or NULL (ones): 1/n of a token's mean, say.
  *   loss, logp  device, T fp32, written.   kl  T fp32, written, or NULL.
  *   dlogits, ldd as in qlora_token_logprobs_backward; NULL: no gradient.

@@ -470,8 +470,10 @@ __device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, do
     const float d = (float)((double)a.ref_logp[t] - lp);
     const float e = expm1f(d);
     kl = exp_less_two_terms(d, e);
-    loss = fmaf(a.kl_coef, kl, loss);
-    g = fmaf(-a.kl_coef, e, g);
+    if (a.kl_coef != 0.0f) {  // a kl that is only watched may be infinite
+      loss = fmaf(a.kl_coef, kl, loss);
+      g = fmaf(-a.kl_coef, e, g);
+    }
   }
   if (a.weight == nullptr) return g;
   const float w = a.weight[t];

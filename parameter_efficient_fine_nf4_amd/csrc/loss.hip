@@ -461,7 +461,7 @@ __device__ __forceinline__ float policy_token(const PolicyArgs& a, int64_t t, do
   const float A = a.adv[t];
   const float r = a.old_logp != nullptr ? expf((float)(lp - (double)a.old_logp[t])) : (lp == lp ? 1.0f : (float)lp);
   const float rc = fminf(fmaxf(r, a.lo), a.hi);
-  const float x = r * A, y = rc * A;
+  const float x = A == 0.0f && r == r ? 0.0f : r * A, y = rc * A;  // (r may be infinite: 0 times it is still 0)
   const bool clipped = y < x;  // the clipped branch is the smaller one, and flat
   loss = -(clipped ? y : x);
   float g = clipped ? 0.0f : -x;

@@ -8,20 +8,21 @@
 //   t_v = tau (z_v - max z),  S = sum_v exp t_v,  logp = t_y - ln S,
 //   d logp / d z_v = tau ([v = y] - exp(t_v) / S).
 //
-// Exponentials are e_v = 2^(fma(z_v, c, -k)) with c = fl(tau log2 e) and k =
-// fl(c max z): one rounding each, and k's own rounding is the same factor in
-// every e_v and in their sum s, so that p_v = e_v / s is free of it and only
-// ln S takes it back, ln S = ln s + ln 2 (k - c max z), in fp64.  From |k| =
-// 2^20 on, where its rounding is no longer a small exponent (and up to where k
-// is infinite, as in a row of the type's lowest value), the difference z - max
-// z is taken first.  Sums are fp32 and go through a fixed tree, so results do
-// not depend on the schedule.
-//
-// c's rounding is the same for every row too, and it stays: with the exponents
-// x_v as formed and c (1 + d) unrounded, ln S is off by -ln 2 d E_p[x], some
-// 4e-8 that has one sign in all of a sequence's tokens (4096 of them: 1.5e-4
-// in its sum, where fp32 log-probabilities leave 2e-5).  E_p[x] is needed to a
-// digit only, so it is taken from one element of a 16-byte piece, or of a few.
+// Exponentials are e_v = 2^(z_v c - k) with c = tau log2 e and k = fl(c max z):
+// k's rounding is the same factor in every e_v and in their sum s, so that p_v =
+// e_v / s is free of it and only ln S takes it back, ln S = ln s + ln 2 (k - c
+// max z), in fp64.  c is held in two parts, hi of 16 bits and lo of 24, and the
+// exponent is fma(z, lo, fma(z, hi, -k)).  In one part c's rounding (up to 2^-24
+// of it) puts ln S off by ln 2 of it times E_p|x|, some 4e-8, the same way in
+// all of a sequence's tokens (4096 of them: 1.5e-4 in its sum, where fp32
+// log-probabilities leave 2e-5); the two roundings here fall either way.  From
+// |k| = 2^7 on (logits of 88 at tau = 1; and up to where k is infinite, as in a
+// row of the type's lowest value) the difference d = z - max z is taken first,
+// fma(d, hi, d lo).  The pieces of a bf16 gradient take c in one part, fma(z, fl(c),
+// -k): below 2^7 that moves e_v by less than 2^-18 of it, and they are rounded to
+// 2^-9 (4096 x 131072, policy loss and gradient: 393 us with one part everywhere,
+// 410 with two; fp32 gradients take two).  Sums are fp32 and go through a fixed
+// tree, so results do not depend on the schedule.
 //
 // A row is a work-group's, read 16 bytes a lane.  Where it fits the
 // work-group's registers it is read once: all of its loads are in flight
@@ -30,6 +31,7 @@
 // for the gradient.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <limits>
 
 #include "common.hpp"
@@ -94,9 +96,6 @@ __device__ __forceinline__ void put16(void* out, const u32x4& v) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// 2^x's share e x of a mean of x: 0 for x = -inf, as for any x whose e is 0.
-__device__ __forceinline__ float weigh(float e, float x) { return e * fmaxf(x, -200.0f); }
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
@@ -117,57 +116,47 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return r;
 }
 
-// The sum of a row's exponentials e = 2^x, and of e x over the sampled ones.
-struct RowSum {
-  float e, ex;
-};
-// Over the work-group: e for every thread; of ex each wave leaves its sum in
-// `part`, for wave 0 to join (join_ex, after the barrier here).
 template <int T>
-__device__ __forceinline__ float block_sum(const RowSum& v, float* red, float* part) {
-  const float e = wave_sum(v.e), ex = wave_sum(v.ex);
-  if (T == 64) {
-    part[0] = ex;
-    return e;
-  }
-  if ((threadIdx.x & 63) == 0) {
-    red[threadIdx.x >> 6] = e;
-    part[threadIdx.x >> 6] = ex;
-  }
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (T == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float r = red[0];
 #pragma unroll
   for (int i = 1; i < T / 64; ++i) r += red[i];
   return r;
 }
-template <int T>
-__device__ __forceinline__ float join_ex(const float* part) {
-  float v = part[T == 64 ? 0 : threadIdx.x & (T / 64 - 1)];
-#pragma unroll
-  for (int o = T / 128; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
+
+// c = tau log2 e = hi + lo, lo > 0: a masked word's -inf stays -inf in either.
+struct Scale {
+  double c;
+  float one, hi, lo;  // one: fl(c)
+  __device__ __forceinline__ float times(float d) const { return fmaf(d, hi, d * lo); }
+};
 
 // How a row's exponentials are formed from its maximum m.
 struct RowExp {
-  float c, k, m;
+  Scale c;
+  float k, m;
   bool far;
-  __device__ __forceinline__ RowExp(float m_, float c_)
-      : c(c_), k((float)((double)m_ * (double)c_)), m(m_), far(!(fabsf(k) < 1048576.0f)) {}
-  __device__ __forceinline__ float near_x(float z) const { return fmaf(z, c, -k); }
-  __device__ __forceinline__ float far_x(float z) const { return (z - m) * c; }
-  __device__ __forceinline__ float near_e(float z) const { return exp2_hw(near_x(z)); }
-  __device__ __forceinline__ float far_e(float z) const { return exp2_hw(far_x(z)); }
+  __device__ __forceinline__ RowExp(float m_, const Scale& c_)
+      : c(c_), k((float)((double)m_ * c_.c)), m(m_), far(!(fabsf(k) < 128.0f)) {}
+  __device__ __forceinline__ float near_e(float z) const { return exp2_hw(fmaf(z, c.lo, fmaf(z, c.hi, -k))); }
+  __device__ __forceinline__ float far_e(float z) const { return exp2_hw(c.times(z - m)); }
+  // for a gradient of type E
+  template <typename E>
+  __device__ __forceinline__ float near_g(float z) const {
+    return sizeof(E) == 2 ? exp2_hw(fmaf(z, c.one, -k)) : near_e(z);
+  }
   __device__ __forceinline__ float e(float z) const { return far ? far_e(z) : near_e(z); }
   // factor of near_e over far_e: what k's rounding is
   __device__ __forceinline__ float shift() const {
-    return far ? 1.0f : exp2_hw((float)((double)m * (double)c - (double)k));
+    return far ? 1.0f : exp2_hw((float)((double)m * c.c - (double)k));
   }
-  // ln of the sum of exp(tau (z - m)), from the sum s of e(); drift: ln 2 d
-  // times the sum of e x
-  __device__ __forceinline__ double ln_sum(float s, float drift) const {
-    return log((double)s) + (far ? 0.0 : kLn2 * ((double)k - (double)m * (double)c)) +
-           (double)(drift * __builtin_amdgcn_rcpf(s));
+  // ln of the sum of exp(tau (z - m)), from the sum s of e()
+  __device__ __forceinline__ double ln_sum(float s) const {
+    return log((double)s) + (far ? 0.0 : kLn2 * ((double)k - (double)m * c.c));
   }
 };
 
@@ -231,39 +220,27 @@ struct RowRegs {
     return m;
   }
   template <bool FAR>
-  __device__ __forceinline__ RowSum sum_of(const RowExp& x) const {
-    float s[2] = {FAR ? x.far_e(last) : x.near_e(last), 0.0f}, ex = 0.0f;
+  __device__ __forceinline__ float sum_of(const RowExp& x) const {
+    float s[2] = {FAR ? x.far_e(last) : x.near_e(last), 0.0f};
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float f[kPer];
       Elem<E>::unpack(anew<1 + FAR>(w[j]), f);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const float xq = FAR ? x.far_x(f[q]) : x.near_x(f[q]), e = exp2_hw(xq);
-        s[q & 1] += e;
-        if (q == 0) ex += weigh(e, xq);
-      }
+      for (int q = 0; q < kPer; ++q) s[q & 1] += FAR ? x.far_e(f[q]) : x.near_e(f[q]);
     }
-    return RowSum{s[0] + s[1], ex};
+    return s[0] + s[1];
   }
-  __device__ __forceinline__ RowSum sum(const RowExp& x) const { return x.far ? sum_of<true>(x) : sum_of<false>(x); }
+  __device__ __forceinline__ float sum(const RowExp& x) const { return x.far ? sum_of<true>(x) : sum_of<false>(x); }
 };
 
 // Running maximum and sum of exp2((z - m) c), for rows read in pieces.  A
 // maximum of -inf (nothing but masked values so far) is read as 0 in the
 // exponents: -inf - (-inf) would make a NaN of it.
-// One of PER elements is sampled: the first that add() takes of so many.
-template <int PER>
 struct Online {
-  float m = kNegInf;
-  RowSum s{0.0f, 0.0f};
-  // the sums with x + shift for x
-  __device__ __forceinline__ RowSum shifted(float shift) const {
-    const float f = exp2_hw(shift);
-    return RowSum{s.e * f, s.ex * f + weigh(s.e * f, shift) * (1.0f / PER)};
-  }
+  float m = kNegInf, s = 0.0f;
   template <typename E, int N>
-  __device__ __forceinline__ void add(const u32x4 (&w)[N], float c) {
+  __device__ __forceinline__ void add(const u32x4 (&w)[N], const Scale& c) {
     constexpr int kPer = Elem<E>::kPer16;
     float f[kPer], mx = m;
 #pragma unroll
@@ -273,33 +250,28 @@ struct Online {
       for (int q = 0; q < kPer; ++q) mx = fmaxf(mx, f[q]);
     }
     const float ref = mx == kNegInf ? 0.0f : mx;
-    RowSum sum = shifted((m - ref) * c);
+    float sum = s * exp2_hw(c.times(m - ref));
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       Elem<E>::unpack(anew<2>(w[j]), f);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const float x = (f[q] - ref) * c, e = exp2_hw(x);
-        sum.e += e;
-        if (j == 0 && q == 0) sum.ex += weigh(e, x);
-      }
+      for (int q = 0; q < kPer; ++q) sum += exp2_hw(c.times(f[q] - ref));
     }
     m = mx;
     s = sum;
   }
-  __device__ __forceinline__ void add_one(float f, float c) {
+  __device__ __forceinline__ void add_one(float f, const Scale& c) {
     const float mx = fmaxf(m, f), ref = mx == kNegInf ? 0.0f : mx;
-    s = shifted((m - ref) * c);
-    s.e += exp2_hw((f - ref) * c);
+    s = s * exp2_hw(c.times(m - ref)) + exp2_hw(c.times(f - ref));
     m = mx;
   }
 };
 
 // Maximum and sum of a row of any length, in pieces.
 template <typename E, int T, int N>
-__device__ __forceinline__ Online<N * Elem<E>::kPer16> row_pieces(const E* z, int V, const RowSpan& at, float c) {
+__device__ __forceinline__ Online row_pieces(const E* z, int V, const RowSpan& at, const Scale& c) {
   constexpr int kPer = Elem<E>::kPer16;
-  Online<N * kPer> o;
+  Online o;
   for (int i0 = threadIdx.x; i0 < at.nv; i0 += N * T) {
     u32x4 w[N];
 #pragma unroll
@@ -322,7 +294,7 @@ __device__ __forceinline__ u32x4 grad_piece(const u32x4& w, const RowExp& x, flo
   float f[kPer];
   Elem<E>::unpack(w, f);
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) f[q] = (FAR ? x.far_e(f[q]) : x.near_e(f[q])) * kappa;
+  for (int q = 0; q < kPer; ++q) f[q] = (FAR ? x.far_e(f[q]) : x.template near_g<E>(f[q])) * kappa;
   return Elem<E>::pack(f);
 }
 
@@ -487,7 +459,8 @@ struct RowArgs {
   int64_t first, T, ld, ldd;  // rows first to T - 1
   int V;
   const int32_t* labels;
-  float tau, c, drift;  // c = fl(tau log2 e) = tau log2 e / (1 + d), drift = ln 2 d
+  float tau;
+  Scale c;
   float* logp;
   float* stats;  // (max z, sum of e) per row
   void* dlogits;
@@ -505,7 +478,7 @@ struct RowArgs {
 template <typename E, int T, int N, bool POLICY>
 __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
   __shared__ float maxima[T / 64];
-  __shared__ float sums[T / 64], sampled[T / 64];
+  __shared__ float sums[T / 64];
   __shared__ float gsh;
   const E* logits = reinterpret_cast<const E*>(a.logits);
   const int64_t t = a.first + blockIdx.x;
@@ -533,8 +506,7 @@ __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
   const float zy = Elem<E>::get(z + label);
   RowRegs<E, T, N < 0 ? 1 : N> r;
   const RowSpan at(z, a.V);
-  constexpr int kSample = (N < 0 ? -N : 1) * Elem<E>::kPer16;
-  Online<kSample> o;
+  Online o;
   float m;
   if constexpr (N > 0) {
     r.load(z, a.V, at);
@@ -548,12 +520,12 @@ __global__ __launch_bounds__(T) void k_rows(RowArgs a, PolicyArgs pa) {
   // row of nothing but -inf has no distribution and gives NaN)
   float s;
   if constexpr (N > 0)
-    s = block_sum<T>(r.sum(x), sums, sampled);
+    s = block_sum<T>(r.sum(x), sums);
   else
-    s = block_sum<T>(o.shifted(x.far_x(o.m)), sums, sampled) * x.shift();
+    s = block_sum<T>(o.s * x.far_e(o.m), sums) * x.shift();
   float g = 0.0f;
   if (threadIdx.x < 64) {  // fp64, once: one wave
-    const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s, a.drift * kSample * join_ex<T>(sampled));
+    const double lp = ((double)zy - (double)m) * (double)a.tau - x.ln_sum(s);
     float loss, kl;
     if (POLICY) g = policy_token(pa, t, lp, loss, kl);
     if (threadIdx.x == 0) {
@@ -826,16 +798,23 @@ static hipError_t launch_grad(const RowArgs& a, const float* dlogp, hipStream_t 
 // Half of the 256 MB last-level cache.
 static bool past_cache(int64_t T, int64_t ldd, int f32) { return T * ldd * (f32 ? 4 : 2) > ((int64_t)128 << 20); }
 
-// (finite for every finite tau: the row's maximum has 0 times it)
-static float exp2_scale(float tau) { return std::min((float)((double)tau * kLog2e), std::numeric_limits<float>::max()); }
-static float exp2_drift(float tau) {
-  const double c = exp2_scale(tau), off = (double)tau * kLog2e / c - 1.0;
-  return off < 1e-6 ? (float)(kLn2 * off) : 0.0f;
+// Finite for every finite tau (the row's maximum has 0 times it), and lo above 0
+// where c has no bits left for it.
+static Scale exp2_scale(float tau) {
+  const double c = std::min((double)tau * kLog2e, (double)std::numeric_limits<float>::max());
+  float hi = (float)c;
+  if ((double)hi > c) hi = std::nextafter(hi, 0.0f);
+  uint32_t bits;
+  std::memcpy(&bits, &hi, 4);
+  if (std::isnormal(hi)) bits &= 0xFFFFFF00u;
+  std::memcpy(&hi, &bits, 4);
+  const float lo = std::max((float)(c - (double)hi), std::numeric_limits<float>::denorm_min());
+  return Scale{(double)hi + (double)lo, (float)((double)hi + (double)lo), hi, lo};
 }
 
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                           float* logp, float* stats, hipStream_t st) {
-  const RowArgs a{logits, 0, T, ld, 0, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, stats, nullptr, false};
+  const RowArgs a{logits, 0, T, ld, 0, V, labels, tau, exp2_scale(tau), logp, stats, nullptr, false};
   return f32 ? launch_rows<float, false>("logprob", a, PolicyArgs{}, st)
              : launch_rows<uint16_t, false>("logprob", a, PolicyArgs{}, st);
 }
@@ -843,7 +822,7 @@ hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t
 hipError_t launch_logprob_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels,
                                float tau, const float* stats, const float* dlogp, void* dlogits, int64_t ldd,
                                hipStream_t st) {
-  const RowArgs a{logits,  0, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), nullptr,
+  const RowArgs a{logits,  0, T, ld, ldd, V, labels, tau, exp2_scale(tau), nullptr,
                   const_cast<float*>(stats), dlogits, past_cache(T, ldd, f32)};
   return f32 ? launch_grad<float>(a, dlogp, st) : launch_grad<uint16_t>(a, dlogp, st);
 }
@@ -853,7 +832,7 @@ hipError_t launch_policy(const void* logits, int f32, int64_t T, int V, int64_t 
                          float clip_low, float clip_high, float kl_coef, float* loss, float* kl, float* logp,
                          void* dlogits, int64_t ldd, hipStream_t st) {
   const PolicyArgs pa{adv, old_logp, ref_logp, weight, 1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, kl};
-  const RowArgs a{logits, 0, T, ld, ldd, V, labels, tau, exp2_scale(tau), exp2_drift(tau), logp, nullptr, dlogits,
+  const RowArgs a{logits, 0, T, ld, ldd, V, labels, tau, exp2_scale(tau), logp, nullptr, dlogits,
                   past_cache(T, ldd, f32)};
   return f32 ? launch_rows<float, true>("policy", a, pa, st) : launch_rows<uint16_t, true>("policy", a, pa, st);
 }

@@ -731,7 +731,8 @@ static void rows_kernel(const char* name, const RowArgs& a, const PolicyArgs& pa
 //   bf16, V = 40000, 5000 pieces:   512 x 10 56 / 119, 512 x 16 70 / 120, in
 //                                   pieces 1024 x 4 78 / 150;
 //   bf16, V = 65536, 8192 pieces:   512 x 16 90 / 196, in pieces 87 / 227;
-//   bf16, V = 70000, 8750 pieces:   1024 x 12 - / 264, in pieces 107 / 250;
+//   bf16, V = 70000, 8750 pieces:   1024 x 12 - / 255, in pieces 112 / 251;
+//   bf16, V = 73000, 9125 pieces:   1024 x 12 - / 266, in pieces 113 / 273;
 //   fp32, V = 50000, 12500 pieces:  1024 x 16 - / 312, in pieces 134 / 353;
 //   bf16, V = 131072, 16384 pieces: 1024 x 16 220 / 437, 512 x 32 230 / 440,
 //                                   in pieces 1024 x 4 176 / 456, 1024 x 8 178
@@ -761,9 +762,9 @@ static hipError_t launch_rows(const char* name, const RowArgs& a, const PolicyAr
     rows_kernel<E, 512, 12, POLICY>(name, a, pa, st);
   else if (pieces <= 512 * 16)
     rows_kernel<E, 512, 16, POLICY>(name, a, pa, st);
-  else if (POLICY && pieces > 1024 * 9 && pieces <= 1024 * 12)
+  else if (POLICY && pieces > 8960 && pieces <= 1024 * 12)
     rows_kernel<E, 1024, 12, true>(name, a, pa, st);
-  else if (POLICY && pieces > 1024 * 9 && pieces <= 1024 * 16)
+  else if (POLICY && pieces > 8960 && pieces <= 1024 * 16)
     rows_kernel<E, 1024, 16, true>(name, a, pa, st);
   else
     rows_kernel<E, 1024, -4, POLICY>(name, a, pa, st);

@@ -424,14 +424,36 @@ def _run(call: str, dev, *args) -> None:
             _check(getattr(_lib, call)(*args, _stream(dev)), call)
 
 
+def _room(t: torch.Tensor) -> int:
+    """Elements from t's first to the end of its storage."""
+    return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+
+
+def _own_stride(t: torch.Tensor):
+    """The longest row stride of t whose gaps are t's own, by the tensor that t
+    is a view of: from t's first column to the end of that tensor's row.  None
+    where there is no such row (a flat buffer, or a tensor of its own)."""
+    base = t._base
+    if base is None:  # views are not known of in inference mode: less than another row of V
+        return 2 * t.shape[1] - 1 if t.is_inference() else None
+    steps = sorted(s for n, s in zip(base.shape, base.stride()) if n > 1)
+    if base.dim() < 2 or steps[:1] != [1]:
+        return None
+    row = steps[1] if len(steps) > 1 else base.numel()
+    row = row * base.element_size() // t.element_size()
+    first = t.storage_offset() - base.storage_offset() * base.element_size() // t.element_size()
+    return row - first % row
+
+
 def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a T x V tensor.  A single row's is the matrix's that it
-    was sliced from, or says nothing."""
+    """Row stride of a T x V tensor.  A single row's is that of the padded
+    matrix that it was sliced from, or says nothing."""
     T, V = t.shape
     ld = t.stride(0)
     if T > 1:
         return ld
-    return ld if V <= ld <= t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() else V
+    own = _own_stride(t)
+    return ld if V <= ld <= min(_room(t), 2 * V - 1 if own is None else own) else V
 
 
 def _rows(logits: torch.Tensor):
@@ -466,9 +488,10 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
         raise ValueError("out has the shape, type and device of the logits")
     if V > 1 and out.stride(1) != 1:
         raise ValueError("the gradient of one token has to be contiguous")
-    ldd = _row_stride(out)
-    room = out.untyped_storage().nbytes() // out.element_size() - out.storage_offset()
-    if T * ldd > room:
+    ldd, own = _row_stride(out), _own_stride(out)
+    if T > 1 and own is not None and ldd > own:
+        raise ValueError("between out's rows lie other rows or columns of its tensor: the rows are written whole")
+    if T * ldd > _room(out):
         raise ValueError("out's last row ends before its stride: the rows are written whole")
     return out, ldd
 
@@ -494,7 +517,9 @@ def token_logprobs_backward(dlogp: torch.Tensor, logits: torch.Tensor, labels: t
     """Gradient in the logits for ``dlogp`` = d loss / d logp (fp32 [T]).
     ``out`` may be the logits themselves.  Rows of ``out`` are written to
     their whole stride: of a slice ``dY[:, :V]`` the columns from V on get
-    zeros, so dY is ready for the head's backward."""
+    zeros, so dY is ready for the head's backward.  A slice between whose rows
+    others of its tensor lie (``d[:, 0]`` of B x S x V, ``d[::2]``) is refused
+    for that; a single row has no stride and leaves its neighbours."""
     T, V, ld = _rows(logits)
     dev = logits.device
     g = _per("dlogp", dlogp, T, torch.float32, dev)

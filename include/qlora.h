@@ -507,7 +507,8 @@ int qlora_policy_loss(const void *logits, int32_t dtype, int64_t T, int64_t V, i
  * cols >= 1, fewer than 2^29 elements a matrix and 2^31 in all
  * (QLORA_ERR_SHAPE); all pointers
  * 16-byte aligned and disjoint; momentum in [0, 1), lr and weight_decay >= 0,
- * eps > 0, all of them and scale and coef finite (QLORA_ERR_ALPHA otherwise).
+ * eps >= 1e-30 (X's factor 1 / (|u|_F + eps) is held in fp32), all of them and
+ * scale and coef finite (QLORA_ERR_ALPHA otherwise).
  */
 size_t qlora_muon_workspace_bytes(int64_t nmat, int64_t rows, int64_t cols);
 int qlora_muon_step(uint16_t *P, float *W, const uint16_t *G, float *m, int64_t nmat, int64_t rows,

@@ -842,7 +842,7 @@ int qlora_muon_step(uint16_t* P, float* W, const uint16_t* G, float* m, int64_t 
   if (int s = check_muon_shape(nmat, rows, cols)) return s;
   if (ns_steps < 1 || ns_steps > kMaxMuonSteps) return QLORA_ERR_SHAPE;
   if (!(lr >= 0.0f) || !std::isfinite(lr) || !(momentum >= 0.0f && momentum < 1.0f) || !(weight_decay >= 0.0f) ||
-      !std::isfinite(weight_decay) || !std::isfinite(scale) || !(eps > 0.0f) || !std::isfinite(eps))
+      !std::isfinite(weight_decay) || !std::isfinite(scale) || !(eps >= 1e-30f) || !std::isfinite(eps))
     return QLORA_ERR_ALPHA;
   MuonCoef co;
   co.n = ns_steps;

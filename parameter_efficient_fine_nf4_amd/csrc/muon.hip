@@ -457,7 +457,8 @@ __device__ __forceinline__ int poly_index(int e, int S) {
   return e < S / NT * NT ? e % NT * 16 + e / NT : (e - (S - NT)) * 16 + S / NT;
 }
 
-// G (in LDS) -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S.
+// G (in LDS) -> Q / (|u| + eps), rounded to fp32: N x N, zeros past S, and
+// zeros for u = 0 (whose X is 0 also where a^n / eps is past fp32).
 template <int NT, bool TALL>
 __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double* R, const MuonCoef& co, float eps,
                                          float* out, int S) {
@@ -503,7 +504,9 @@ __device__ __forceinline__ void poly_run(double* G, double* P, double* Q, double
   }
   for (int e = threadIdx.x; e < N * N; e += kThreads) {
     const int i = e / N, k = e % N;
-    out[e] = i < S && k < S ? (float)(Q[At::at(poly_index<NT, TALL>(i, S), poly_index<NT, TALL>(k, S))] * inv) : 0.0f;
+    out[e] = i < S && k < S && trace != 0.0
+                 ? (float)(Q[At::at(poly_index<NT, TALL>(i, S), poly_index<NT, TALL>(k, S))] * inv)
+                 : 0.0f;
   }
 }
 
@@ -541,7 +544,7 @@ __device__ __forceinline__ void poly_run16(f64x4 G, const MuonCoef& co, float ep
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    out[64 * q + lane] = lane / 16 + 4 * q < S && (lane & 15) < S ? (float)(Q[q] * inv) : 0.0f;
+    out[64 * q + lane] = lane / 16 + 4 * q < S && (lane & 15) < S && trace != 0.0 ? (float)(Q[q] * inv) : 0.0f;
 }
 
 // A wave's share of the sum of the splits' partials.

@@ -150,7 +150,7 @@ hipError_t launch_adam(float* W, const uint16_t* G, float* m, float* v, uint16_t
 // loss.hip: logits are T rows of V (stride ld elements), fp32 (f32 != 0) or
 // bf16; tau is the inverse temperature.  A token whose label lies outside
 // [0, V) does not count: log-probability 0 and no gradient.
-// stats (T x 2, optional): row maximum and log2 of the exponentials' sum.
+// stats (T x 2, optional): the row's maximum and the sum of its exponentials.
 hipError_t launch_logprob(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* labels, float tau,
                           float* logp, float* stats, hipStream_t st);
 // dlogits = dlogp d logp / d logits: T whole rows of ldd elements (zeros

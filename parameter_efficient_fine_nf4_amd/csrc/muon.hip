@@ -182,15 +182,14 @@ constexpr int mu_tiles(int nt) { return nt * (nt + 1) / 2; }
 // steps from `rest` on.
 struct Steps {
   int i, n, first, rest, stride, step;
-  __device__ __forceinline__ Steps(const MuShape& s, int64_t mat, int wave, int waves, int step_, bool vec)
-      : i(wave), n(vec ? s.L / step_ : 0), stride(waves), step(step_) {
+  __device__ __forceinline__ Steps(const MuShape& s, int64_t mat, int wave, int waves, int step_)
+      : i(wave), n(s.L / step_), stride(waves), step(step_) {
     first = (int)(mat * n / s.nmat);
     // (past the axis for every wave but the one whose turn it is; L + step
     // fits an int as a matrix has fewer than 2^29 elements)
     rest = n * step < s.L ? (int)min((int64_t)s.L, ((int64_t)n + (i + stride - n % stride) % stride) * step) : s.L;
   }
   __device__ __forceinline__ bool valid() const { return i < n; }
-  __device__ __forceinline__ bool next_valid() const { return i + stride < n; }
   __device__ __forceinline__ int j0(int at) const { return (first + at < n ? first + at : first + at - n) * step; }
 };
 
@@ -304,7 +303,7 @@ __device__ __forceinline__ void gram_sums(const uint16_t* G, float* M, const MuS
                                           int lane, float mu, int nesterov, f64x4 (&acc)[mu_tiles(NT)]) {
 #pragma unroll
   for (int u = 0; u < mu_tiles(NT); ++u) acc[u] = f64x4{0.0, 0.0, 0.0, 0.0};
-  Steps at(s, mat, wave, waves, 32, true);
+  Steps at(s, mat, wave, waves, 32);
   GramLoad<NT, TALL> x;
 #pragma unroll 1
   for (; at.valid(); at.i += at.stride) {
@@ -872,7 +871,7 @@ template <int NT, bool TALL, bool STREAM>
 __device__ __forceinline__ void apply_steps(const ApplyArgs& p, const MuShape& s, int64_t mat, int wave, int waves,
                                             int lane, const float* qs, float* scratch) {
   constexpr int kStep = ApplyShape<NT, TALL>::kStep;
-  Steps at(s, mat, wave, waves, kStep, true);
+  Steps at(s, mat, wave, waves, kStep);
   if constexpr (TALL) {
     const TallLds<NT> x(scratch, s.S, lane);
 #pragma unroll 1

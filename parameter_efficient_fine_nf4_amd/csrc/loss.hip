@@ -16,10 +16,10 @@
 // of it) puts ln S off by ln 2 of it times E_p|x|, some 4e-8, the same way in
 // all of a sequence's tokens (4096 of them: 1.5e-4 in its sum, where fp32
 // log-probabilities leave 2e-5); the two roundings here fall either way.  From
-// |k| = 2^7 on (logits of 88 at tau = 1; and up to where k is infinite, as in a
+// |k| = 2^9 on (logits of 355 at tau = 1; and up to where k is infinite, as in a
 // row of the type's lowest value) the difference d = z - max z is taken first,
 // fma(d, hi, d lo).  The pieces of a bf16 gradient take c in one part, fma(z, fl(c),
-// -k): below 2^7 that moves e_v by less than 2^-18 of it, and they are rounded to
+// -k): below 2^9 that moves e_v by less than 2^-16 of it, and they are rounded to
 // 2^-9 (4096 x 131072, policy loss and gradient: 393 us with one part everywhere,
 // 410 with two; fp32 gradients take two).  Sums are fp32 and go through a fixed
 // tree, so results do not depend on the schedule.
@@ -141,7 +141,7 @@ struct RowExp {
   float k, m;
   bool far;
   __device__ __forceinline__ RowExp(float m_, const Scale& c_)
-      : c(c_), k((float)((double)m_ * c_.c)), m(m_), far(!(fabsf(k) < 128.0f)) {}
+      : c(c_), k((float)((double)m_ * c_.c)), m(m_), far(!(fabsf(k) < 512.0f)) {}
   __device__ __forceinline__ float near_e(float z) const { return exp2_hw(fmaf(z, c.lo, fmaf(z, c.hi, -k))); }
   __device__ __forceinline__ float far_e(float z) const { return exp2_hw(c.times(z - m)); }
   // for a gradient of type E
@@ -170,6 +170,7 @@ __device__ __forceinline__ u32x4 anew(u32x4 w) {
   if (PASS == 1) asm volatile("; near" : "+v"(w));
   if (PASS == 2) asm volatile("; far" : "+v"(w));
   if (PASS == 3) asm volatile("; near, streamed" : "+v"(w));
+  if (PASS == 4) asm volatile("; far, streamed" : "+v"(w));
   return w;
 }
 
@@ -342,12 +343,11 @@ __device__ __forceinline__ void row_grad(const E* z, float zy, E* out, int V, in
   const float kappa = -gt / s;
   float last = kNegInf;
   if (at.rest < V) last = Elem<E>::get(z + at.rest);
-  if (x.far)
-    row_grad_of<E, T, B, true, false>(z, out, at, x, kappa);
-  else if (stream)
-    row_grad_of<E, T, B, false, true>(z, out, at, x, kappa);
+  if (stream)
+    x.far ? row_grad_of<E, T, B, true, true>(z, out, at, x, kappa) : row_grad_of<E, T, B, false, true>(z, out, at, x, kappa);
   else
-    row_grad_of<E, T, B, false, false>(z, out, at, x, kappa);
+    x.far ? row_grad_of<E, T, B, true, false>(z, out, at, x, kappa)
+          : row_grad_of<E, T, B, false, false>(z, out, at, x, kappa);
   row_end<E, T>(last, zy, out, V, cols, at, label, x, kappa, gt);
 }
 
@@ -360,7 +360,7 @@ __device__ __forceinline__ void regs_grad_of(const RowRegs<E, T, N>& r, E* out, 
     const int i = j * T + threadIdx.x;
     if (i < at.nv)
       put16<STREAM>(out + at.head + i * Elem<E>::kPer16,
-                    grad_piece<E, FAR>(anew<FAR ? 2 : STREAM ? 3 : 1>(r.w[j]), x, kappa));
+                    grad_piece<E, FAR>(anew<1 + FAR + 2 * STREAM>(r.w[j]), x, kappa));
   }
 }
 template <typename E, int T, int N>
@@ -368,12 +368,11 @@ __device__ __forceinline__ void regs_grad(const RowRegs<E, T, N>& r, float zy, E
                                           const RowSpan& at, int label, const RowExp& x, float s, float gt,
                                           bool stream) {
   const float kappa = -gt / s;
-  if (x.far)
-    regs_grad_of<E, T, N, true, false>(r, out, at, x, kappa);
-  else if (stream)
-    regs_grad_of<E, T, N, false, true>(r, out, at, x, kappa);
+  if (stream)
+    x.far ? regs_grad_of<E, T, N, true, true>(r, out, at, x, kappa) : regs_grad_of<E, T, N, false, true>(r, out, at, x, kappa);
   else
-    regs_grad_of<E, T, N, false, false>(r, out, at, x, kappa);
+    x.far ? regs_grad_of<E, T, N, true, false>(r, out, at, x, kappa)
+          : regs_grad_of<E, T, N, false, false>(r, out, at, x, kappa);
   row_end<E, T>(r.last, zy, out, V, cols, at, label, x, kappa, gt);
 }
 

@@ -53,3 +53,35 @@ def test_masked_words_at_every_scale(lib, V, dtype, tau):
     want[0, 5], want[0, V - 1], want[1, V - 1], want[1, 5] = t, -t, -t, t
     # four half steps, one to the output's type, and at the lower end of its range a step of that
     assert ((dz - want).abs() <= (4 * U + torch.finfo(dtype).eps / 2) * want.abs() + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.6934478282928467])
+@pytest.mark.parametrize("V,T,dtype", [(32000, 4096, BF), (140000, 500, BF), (32000, 40, BF), (32003, 1100, F32), (8191, 5, F32)],
+                         ids=lambda x: str(x).split(".")[-1])
+def test_logits_around_any_level(lib, V, T, dtype, tau):
+    # a level that all logits share changes no probability: both ways of forming exponents (the largest logit's is 2^9
+    # at 355 or 512), gradients above and below what is written past the cache.  The bounds are those of
+    # test_gpu_logprobs.py, from the logits as the type holds them
+    print("case: level", V, T, dtype, tau, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z, adv = torch.empty(T, V, dtype=dtype, device=DEV), torch.randn(T, device=DEV, generator=g)
+    y = torch.randint(0, V, (T,), device=DEV, generator=g, dtype=torch.int32)
+    for level in (-600.0, -120.0, 80.0, 340.0, 500.0, 5000.0):
+        for part in z.split(256):
+            part.copy_(2 * torch.randn(len(part), V, device=DEV, generator=g) + level)
+        logp, stats = lib.token_logprobs(z, y, tau, save_stats=True)
+        dz = lib.token_logprobs_backward(adv, z, y, stats, tau)
+        pdz = lib.policy_loss(z, y, -adv, inv_temperature=tau)[3]
+        t32 = float(np.float32(tau))
+        for i in (0, 1, T // 2, T - 1):
+            t = t32 * (z[i].double() - z[i].double().max())
+            p, label = t.softmax(0), int(y[i])
+            want = float(t[label] - t.logsumexp(0))
+            b = U * (12 * (np.log(V) + 1) + V / 256 + 32 + 3 * abs(float(t[label])) + abs(want))
+            assert abs(float(logp[i]) - want) <= b, (level, i)
+            d = -p
+            d[label] += 1
+            a = float(adv[i]) * t32
+            d *= a
+            bound = abs(a) * (3 * U + p * b) + (4 * U + torch.finfo(dtype).eps / 2) * d.abs() + 1e-37
+            assert ((dz[i].double() - d).abs() <= bound).all() and ((pdz[i].double() - d).abs() <= bound).all(), (level, i)

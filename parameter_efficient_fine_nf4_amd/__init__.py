@@ -431,28 +431,30 @@ def _room(t: torch.Tensor) -> int:
 
 def _own_stride(t: torch.Tensor):
     """The longest row stride of t whose gaps are t's own, by the tensor that t
-    is a view of: from t's first column to the end of that tensor's row.  None
-    where there is no such row (a flat buffer, or a tensor of its own)."""
-    base = t._base
+    is a view of: that tensor's row, where t starts with one.  None where there
+    is no such row (a flat buffer, or a tensor of its own)."""
+    V, base = t.shape[1], t._base
     if base is None:  # views are not known of in inference mode: less than another row of V
-        return 2 * t.shape[1] - 1 if t.is_inference() else None
+        return 2 * V - 1 if t.is_inference() else None
     steps = sorted(s for n, s in zip(base.shape, base.stride()) if n > 1)
     if base.dim() < 2 or steps[:1] != [1]:
         return None
-    row = steps[1] if len(steps) > 1 else base.numel()
-    row = row * base.element_size() // t.element_size()
-    first = t.storage_offset() - base.storage_offset() * base.element_size() // t.element_size()
-    return row - first % row
+    size = t.element_size()
+    row = (steps[1] if len(steps) > 1 else base.numel()) * base.element_size() // size
+    first = t.storage_offset() - base.storage_offset() * base.element_size() // size
+    if row < V:  # a buffer's shape
+        return None
+    return row if first % row == 0 else V
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a T x V tensor.  A single row's is that of the padded
-    matrix that it was sliced from, or says nothing."""
+    """Row stride of a T x V tensor.  A single row has none of its own: that of
+    the padded matrix that it was sliced from, or says nothing."""
     T, V = t.shape
-    ld = t.stride(0)
     if T > 1:
-        return ld
+        return t.stride(0)
     own = _own_stride(t)
+    ld = t.stride(0) if own is None or t._base is None else own
     return ld if V <= ld <= min(_room(t), 2 * V - 1 if own is None else own) else V
 
 
@@ -489,7 +491,7 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
     if V > 1 and out.stride(1) != 1:
         raise ValueError("the gradient of one token has to be contiguous")
     ldd, own = _row_stride(out), _own_stride(out)
-    if T > 1 and own is not None and ldd > own:
+    if T > 1 and own is not None and ldd > max(own, V):
         raise ValueError("between out's rows lie other rows or columns of its tensor: the rows are written whole")
     if T * ldd > _room(out):
         raise ValueError("out's last row ends before its stride: the rows are written whole")

@@ -15,8 +15,9 @@ BF, F32 = torch.bfloat16, torch.float32
 
 # (T, V, row stride, first element): ordinary batches, odd strides, rows in registers and in pieces
 CASES = [(4096, 32000, 32000, 0, BF), (2200, 32003, 32003, 0, BF), (4100, 20011, 20011, 3, BF),
-         (600, 131071, 131071, 0, BF), (520, 140000, 140001, 1, BF), (1000, 70001, 70008, 5, BF), (1100, 32003, 32003, 0, F32),
-         (1100, 32000, 32064, 0, F32), (600, 70001, 70001, 1, F32), (530, 66001, 66001, 0, F32), (40000, 1001, 1001, 0, F32)]
+         (600, 131071, 131071, 0, BF), (520, 140000, 140001, 1, BF), (1000, 70001, 70008, 5, BF),
+         (1100, 32003, 32003, 0, F32), (1100, 32000, 32064, 0, F32), (600, 70001, 70001, 1, F32),
+         (530, 66001, 66001, 0, F32), (40000, 1001, 1001, 0, F32)]
 
 
 @pytest.mark.parametrize("T,V,ld,offset,dtype", CASES, ids=lambda x: str(x).split(".")[-1])

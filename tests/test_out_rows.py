@@ -45,7 +45,9 @@ def test_paddings_are_taken(lib):
             torch.zeros(T * 4000).view(T, 4000)[:, :V], torch.zeros(1100 * T).as_strided((T, V), (1100, 1)),
             torch.zeros(T, 2048, dtype=torch.bfloat16).view(torch.float32)[:, :V], torch.zeros(T, 1, 1024)[:, 0, :V],
             torch.zeros(3, T, 1024)[1, :, :V], torch.zeros(T, V, 1)[:, :, 0], torch.zeros(T, 1024).detach()[:, :V],
-            torch.nn.Parameter(torch.zeros(T, 1024)).data[:, :V]]
+            torch.nn.Parameter(torch.zeros(T, 1024)).data[:, :V], torch.zeros(1000, 64).view(-1)[:T * V].view(T, V),
+            torch.zeros(1000, 64).view(-1)[:T * 1024].view(T, 1024)[:, :V],
+            torch.zeros(2 * T, 2 * V).view(-1)[77:77 + T * V].view(T, V)]
     with torch.inference_mode():
         outs.append(torch.zeros(T, 1024)[:, :V])
     for out in outs:
@@ -74,6 +76,25 @@ def test_one_row_leaves_its_neighbours(lib, in_place):
         out.copy_(z)
     lib.policy_loss(src, y, -one, out=out)
     assert torch.equal(out, want) and (full[0, 1:] == 3).all()
+
+
+@pytest.mark.gpu
+def test_one_row_of_a_padded_head_is_written_whole(lib):
+    # ... whatever else the tensor holds that it is a row of: the first position of a batch of one
+    V, S = 1000, 4
+    z, y = torch.randn(1, V, device="cuda"), torch.tensor([7], dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    logp, stats = lib.token_logprobs(z, y, save_stats=True)
+    want = lib.token_logprobs_backward(one, z, y, stats)
+    for at in (0, 2):
+        full = torch.full((1, S, 1024), 3.0, device="cuda")
+        lib.token_logprobs_backward(one, z, y, stats, out=full[:, at, :V])
+        assert torch.equal(full[0, at, :V], want[0]) and (full[0, at, V:] == 0).all()
+        assert (full[0, :at] == 3).all() and (full[0, at + 1:] == 3).all()
+    full = torch.full((3, 2000), 3.0, device="cuda")
+    lib.token_logprobs_backward(one, z, y, stats, out=full[1:2, 100:100 + V])    # amid a row: nothing but its words
+    assert torch.equal(full[1:2, 100:100 + V], want) and (full[1, :100] == 3).all() and (full[1, 100 + V:] == 3).all()
+    assert (full[::2] == 3).all()
 
 
 @pytest.mark.gpu

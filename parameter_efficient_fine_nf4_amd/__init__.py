@@ -450,11 +450,12 @@ def _own_stride(t: torch.Tensor):
 def _row_stride(t: torch.Tensor) -> int:
     """Row stride of a T x V tensor.  A single row has none of its own: that of
     the padded matrix that it was sliced from, or says nothing."""
-    T, V = t.shape
-    if T > 1:
-        return t.stride(0)
+    (T, V), ld = t.shape, t.stride(0)
+    if T > 1 or ld == V:
+        return ld
     own = _own_stride(t)
-    ld = t.stride(0) if own is None or t._base is None else own
+    if own is not None and t._base is not None:
+        ld = own
     return ld if V <= ld <= min(_room(t), 2 * V - 1 if own is None else own) else V
 
 
@@ -490,8 +491,9 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
         raise ValueError("out has the shape, type and device of the logits")
     if V > 1 and out.stride(1) != 1:
         raise ValueError("the gradient of one token has to be contiguous")
-    ldd, own = _row_stride(out), _own_stride(out)
-    if T > 1 and own is not None and ldd > max(own, V):
+    ldd = _row_stride(out)
+    own = _own_stride(out) if T > 1 and ldd > V else None
+    if own is not None and ldd > own:
         raise ValueError("between out's rows lie other rows or columns of its tensor: the rows are written whole")
     if T * ldd > _room(out):
         raise ValueError("out's last row ends before its stride: the rows are written whole")

@@ -337,6 +337,54 @@ int qlora_forward_multi(const uint16_t *X, int64_t M, const qlora_nf4_t *W0, int
                         float alpha, uint16_t *Y, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * qlora_checkpoint_save, qlora_checkpoint_load, qlora_forward_checkpoint,
+ * qlora_backward_checkpoint -- the adapted linear with its input kept at 8
+ * bits between forward and backward (page "LoRA and QLoRA fine-tuning:
+ * mechanics, ...", "What QLoRA freezes, and in how many bits": with the
+ * weights at 4 bits it is the activations that a step's memory goes to).
+ * Of the input the backward needs dA = s U^T X alone.  With a block's
+ * constant a, the largest |x| of 64 consecutive columns of a token,
+ *
+ *   c  = rint(127 x / a)                       (ties to even; 0 if a = 0)
+ *   x^ = bf16(fl32(c fl32(a fl32(1/127))))     what the codes stand for
+ *
+ * so |x^ - x| <= a (1/254 + 2^-8), and 8.25 bits are kept of each 16.  A
+ * block with an infinity or a NaN stands for NaN throughout.
+ *
+ *   codes   device, M x k int8, row-major as X.
+ *   absmax  device, bf16: k/64 rows of roundup(M, 64), row b holding the
+ *           constants of columns 64 b .. 64 b + 63 for tokens 0 .. M-1; its
+ *           padding is left unspecified and never used.
+ *           qlora_checkpoint_sizes gives the bytes of both.
+ *
+ * qlora_checkpoint_load writes x^ (M x k bf16).  qlora_forward_checkpoint is
+ * qlora_forward_sections (nsec = 1: qlora_forward) and saves its X in the
+ * same call; outputs are those calls' own.  qlora_backward_checkpoint is
+ * qlora_backward_sections with dA = s U^T x^ in place of s U^T X: T_saved, which
+ * the forward made of X itself, is required (dB = s dY^T T is not affected by
+ * the 8 bits), as is everything else of the adapter; r == 0 ignores both and
+ * the checkpoint.  With keep (nsec == 1; NULL: no dropout) the layer is
+ * qlora_backward_dropout's, and the checkpoint is that of the dropped input
+ * (qlora_checkpoint_save of the forward's Xd_save).  Workspaces:
+ * qlora_forward_workspace_bytes and qlora_backward_workspace_bytes of nsec*r
+ * ranks.  dX, if NULL, is skipped.
+ */
+int qlora_checkpoint_sizes(int64_t M, int64_t k, size_t *codes_bytes, size_t *absmax_bytes);
+int qlora_checkpoint_save(const uint16_t *X, int64_t M, int64_t k, int8_t *codes,
+                          uint16_t *absmax, void *stream);
+int qlora_checkpoint_load(const int8_t *codes, const uint16_t *absmax, int64_t M, int64_t k,
+                          uint16_t *X, void *stream);
+int qlora_forward_checkpoint(const uint16_t *X, int64_t M, const qlora_nf4_t *W0, int32_t nsec,
+                             const uint16_t *A, const uint16_t *B, int32_t r, float alpha,
+                             uint16_t *Y, uint16_t *T_save, int8_t *codes, uint16_t *absmax,
+                             void *ws, size_t ws_bytes, void *stream);
+int qlora_backward_checkpoint(const uint16_t *dY, const int8_t *codes, const uint16_t *absmax,
+                              int64_t M, const qlora_nf4_t *W0, int32_t nsec, const uint16_t *A,
+                              const uint16_t *B, int32_t r, float alpha, const uint8_t *keep,
+                              float p, const uint16_t *T_saved, uint16_t *dX, uint16_t *dA,
+                              uint16_t *dB, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * qlora_adam_step -- one Adam step on n adapter parameters (A and B, in one
  * buffer or one call each) with an fp32 master copy (page "Fine-Tuning on a
  * Budget", "Why full fine-tuning costs so much": a trained parameter keeps
@@ -479,6 +527,53 @@ int qlora_policy_loss(const void *logits, int32_t dtype, int64_t T, int64_t V, i
                       const float *old_logp, const float *ref_logp, const float *weight,
                       float clip_low, float clip_high, float kl_coef, float *loss, float *kl,
                       float *logp, void *dlogits, int64_t ldd, void *stream);
+
+/*
+ * qlora_token_scores, qlora_token_scores_backward -- what a head's logits say
+ * of each token: the log-probabilities of m given tokens a row (the label, a
+ * teacher's alternatives), the distribution's entropy, and its n best words;
+ * and the gradient of a loss on log-probabilities and entropy.  With p the
+ * row's distribution at tau = inv_temperature:
+ *
+ *   logp[t, j]     = ln p_y,  y = tokens[t, j]         if 0 <= y < V
+ *   logp[t, j]     = 0                                 otherwise (not counted)
+ *   entropy[t]     = -sum_v p_v ln p_v                 (p ln p = 0 at p = 0)
+ *   top_ids[t, i], top_logp[t, i]   the word of the i-th largest logit and its
+ *                    ln p; equal logits by the lowest index first.  A masked
+ *                    word (-inf) is no alternative: past the last word with a
+ *                    finite logit the id is -1 and its value -inf.
+ *   dlogits[t, v]  = tau (sum_j dlogp[t, j] ([v = y_j] - p_v)
+ *                    - dentropy[t] p_v (ln p_v + entropy[t]))
+ *
+ *   logits, dtype, T, V, ld   as in qlora_token_logprobs; a row with a NaN,
+ *            +inf or nothing but -inf gives NaN (and ids of -1).
+ *   tokens   device, T x m int32, each in any place, the same one more than
+ *            once too (NULL if m == 0).  Where m > 0, a row none of whose
+ *            tokens counts is not read: entropy 0, ids -1 with -inf, and no
+ *            gradient, from its entropy either.
+ *   m, n     0 .. 64 each, n <= V.
+ *   logp     device, T x m fp32, written (NULL if m == 0).
+ *   entropy  device, T fp32, written.
+ *   top_ids, top_logp   device, T x n int32 and fp32, written (NULL if n == 0).
+ *   stats    device, T x 3 fp32, written (may be NULL in the forward): what
+ *            the backward needs of each row.
+ *   dlogp    device, T x m fp32 (not read where a token does not count).
+ *   dentropy device, T fp32, or NULL: the loss has no entropy term.
+ *   dlogits, ldd   as in qlora_token_logprobs_backward: whole rows, may be the
+ *            logits themselves.  A row whose coefficients are all 0 has zero
+ *            gradient whatever its logits hold.
+ *
+ * Sums are fp32 in a fixed order: results are deterministic.  QLORA_ERR_SHAPE
+ * for m or n out of range.
+ */
+int qlora_token_scores(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                       const int32_t *tokens, int32_t m, int32_t n, float inv_temperature,
+                       float *logp, float *entropy, int32_t *top_ids, float *top_logp,
+                       float *stats, void *stream);
+int qlora_token_scores_backward(const float *dlogp, const float *dentropy, const void *logits,
+                                int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                const int32_t *tokens, int32_t m, float inv_temperature,
+                                const float *stats, void *dlogits, int64_t ldd, void *stream);
 
 /*
  * qlora_muon_step -- one step of momentum with an orthogonalised update

@@ -14,6 +14,9 @@ The calls mirror include/qlora.h:
 * ``unmerge(W, A, B, alpha)``          -> bf16 ``W0``
 * ``token_logprobs(logits, labels)``   -> fp32 ``logp`` (and row statistics)
 * ``preference_loss(logp, ...)``, ``policy_loss(logits, ...)`` -> losses and gradients
+* ``token_scores(logits, tokens, top)`` -> log-probabilities, entropy, best words
+* ``checkpoint_save(X)``, ``forward_checkpoint``, ``backward_checkpoint`` -> the
+  layer with its input kept at 8 bits
 * ``adam_step``, ``muon_step``         -> the adapters' optimiser steps
 """
 
@@ -84,6 +87,17 @@ _sigs = {
                                              _vp, _vp, _vp, _vp]),
     "qlora_policy_loss": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _vp, _vp, _f32, _f32, _f32,
                                          _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qlora_checkpoint_sizes": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "qlora_checkpoint_save": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "qlora_checkpoint_load": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "qlora_forward_checkpoint": (ctypes.c_int, [_vp, _i64, _P, _i32, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp, _vp,
+                                                _sz, _vp]),
+    "qlora_backward_checkpoint": (ctypes.c_int, [_vp, _vp, _vp, _i64, _P, _i32, _vp, _vp, _i32, _f32, _vp, _f32, _vp,
+                                                 _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_token_scores": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp,
+                                          _vp]),
+    "qlora_token_scores_backward": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _f32, _vp, _vp,
+                                                   _i64, _vp]),
     "qlora_muon_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "qlora_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _f32, _i32, _f32, _f32, _f32, _i32,
                                        ctypes.POINTER(ctypes.c_float), _vp, _sz, _vp]),
@@ -390,6 +404,143 @@ def backward_sections(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A=None, B
     return dX, dA, dB
 
 
+# ------------------------------------------- 8-bit activation checkpoints ----
+
+@dataclass
+class Checkpoint:
+    """An M x k bf16 activation kept at 8 bits (caller-owned device buffers).
+
+    Column block b of 64 columns has one constant per token, in ``absmax[b]``
+    (bf16; rows of M rounded up to 64, the padding unspecified)."""
+    M: int
+    k: int
+    codes: torch.Tensor   # int8 [M, k]
+    absmax: torch.Tensor  # bfloat16 [k/64, roundup(M, 64)]
+
+    @staticmethod
+    def empty(M: int, k: int, device) -> "Checkpoint":
+        if M < 0 or k < 64 or k % 64:
+            raise ValueError("a checkpoint has M >= 0 tokens of k columns, a multiple of 64")
+        return Checkpoint(M, k, torch.empty((M, k), dtype=torch.int8, device=device),
+                          torch.empty((k // 64, -(-M // 64) * 64), dtype=torch.bfloat16, device=device))
+
+    def check(self, M: int, k: int, device) -> None:
+        """Raise unless this is the checkpoint of an M x k tensor on ``device``."""
+        if (self.M, self.k) != (M, k):
+            raise ValueError(f"the checkpoint is of {self.M} x {self.k}, not {M} x {k}")
+        for name, t, dtype, shape in (("codes", self.codes, torch.int8, (M, k)),
+                                      ("absmax", self.absmax, torch.bfloat16, (k // 64, -(-M // 64) * 64))):
+            if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"{name} is contiguous, {dtype}, of shape {shape}, on {device}")
+
+
+def _activation(name: str, t: torch.Tensor, cols: int | None = None) -> torch.device:
+    if t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous() or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} is a contiguous bfloat16 matrix" + (f" of {cols} columns" if cols is not None else ""))
+    return _on_gpu(t)
+
+
+def checkpoint_save(X: torch.Tensor, out: Checkpoint | None = None) -> Checkpoint:
+    """X (M x k bf16, k a multiple of 64) at 8 bits: int8 codes and a bf16
+    constant for every 64 columns of a token."""
+    M, k = X.shape if X.dim() == 2 else (0, 0)
+    dev = _activation("X", X)
+    ck = out if out is not None else Checkpoint.empty(M, k, dev)
+    ck.check(M, k, dev)
+    _run("qlora_checkpoint_save", dev, X.data_ptr(), M, k, ck.codes.data_ptr(), ck.absmax.data_ptr())
+    return ck
+
+
+def checkpoint_load(ck: Checkpoint, out: torch.Tensor | None = None) -> torch.Tensor:
+    """What the checkpoint stands for (M x k bf16)."""
+    dev = _on_gpu(ck.codes)
+    ck.check(ck.M, ck.k, dev)
+    X = out if out is not None else torch.empty((ck.M, ck.k), dtype=torch.bfloat16, device=dev)
+    if _activation("out", X, ck.k) != dev or X.shape[0] != ck.M:
+        raise ValueError(f"out is {ck.M} x {ck.k} on {dev}")
+    _run("qlora_checkpoint_load", dev, ck.codes.data_ptr(), ck.absmax.data_ptr(), ck.M, ck.k, X.data_ptr())
+    return X
+
+
+def _adapter(w: NF4Weight, A, B, device) -> int:
+    """Ranks of each of w's sections."""
+    if A is None and B is None:
+        return 0
+    if A is None or B is None:
+        raise ValueError("A and B come together")
+    rt = A.shape[0] if A.dim() == 2 else -1
+    for name, t, shape in (("A", A, (rt, w.k)), ("B", B, (w.d, rt // w.nsec))):
+        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} is contiguous, torch.bfloat16, of shape {shape}, on {device}")
+    if rt % w.nsec:
+        raise ValueError("A holds the same number of ranks for every section")
+    return rt // w.nsec
+
+
+def forward_checkpoint(X: torch.Tensor, w: NF4Weight, A=None, B=None, alpha: float = 0.0,
+                       out: torch.Tensor | None = None, ck: Checkpoint | None = None):
+    """(Y, T, checkpoint): ``forward`` (``forward_sections`` for a weight with
+    sections) that keeps what ``backward_checkpoint`` needs: T and, in place
+    of X, its checkpoint (written into ``ck`` if given).  T is None without an
+    adapter."""
+    dev = _activation("X", X, w.k)
+    M = X.shape[0]
+    r = _adapter(w, A, B, dev)
+    rt = r * w.nsec
+    Y = out if out is not None else torch.empty((M, w.d), dtype=torch.bfloat16, device=dev)
+    if _activation("out", Y, w.d) != dev or Y.shape[0] != M or w.device != dev:
+        raise ValueError(f"the weight and out ({M} x {w.d}) are on {dev}")
+    T = torch.empty((rt, -(-M // 64) * 64), dtype=torch.bfloat16, device=dev) if r > 0 else None
+    if ck is None:
+        ck = Checkpoint.empty(M, w.k, dev)
+    ck.check(M, w.k, dev)
+    if M == 0:  # empty tensors have no address
+        return Y, T, ck
+    ws = _workspace(_lib.qlora_forward_workspace_bytes(M, w.d, w.k, rt), dev)
+    desc = w.desc()
+    _run("qlora_forward_checkpoint", dev, X.data_ptr(), M, ctypes.byref(desc), w.nsec, _ptr(A), _ptr(B), r,
+         float(alpha), Y.data_ptr(), _ptr(T), ck.codes.data_ptr(), ck.absmax.data_ptr(), _ptr(ws),
+         0 if ws is None else ws.numel())
+    return Y, T, ck
+
+
+def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, B=None, alpha: float = 0.0,
+                        T_saved: torch.Tensor | None = None, need_dx: bool = True, keep: torch.Tensor | None = None,
+                        p: float = 0.0):
+    """(dX, dA, dB) of ``forward_checkpoint``: dA from what the checkpoint
+    stands for, dX and dB as ``backward`` gives them.  T_saved is required
+    with an adapter.  With ``keep`` and ``p`` the gradients are
+    ``backward_dropout``'s, ck being the checkpoint of the dropped input
+    (``forward_dropout``'s xd_out)."""
+    dev = _activation("dY", dY, w.d)
+    M = dY.shape[0]
+    r = _adapter(w, A, B, dev)
+    rt = r * w.nsec
+    if w.device != dev:
+        raise ValueError(f"the weight is on {dev}")
+    if r > 0:
+        ck.check(M, w.k, dev)
+        if T_saved is None or T_saved.dtype != torch.bfloat16 or T_saved.numel() < rt * (-(-M // 64) * 64) \
+                or not T_saved.is_contiguous() or T_saved.device != dev:
+            raise ValueError("T_saved is the T that the forward returned")
+        if keep is not None and (keep.dtype != torch.uint8 or keep.shape != (M, w.k) or not keep.is_contiguous()
+                                 or keep.device != dev):
+            raise ValueError(f"keep is a contiguous uint8 mask of {M} x {w.k} on {dev}")
+    dX = torch.empty((M, w.k), dtype=torch.bfloat16, device=dev) if need_dx else None
+    new = torch.empty if M else torch.zeros  # without a token the sums are empty and nothing is launched
+    dA = new((rt, w.k), dtype=torch.bfloat16, device=dev) if r else None
+    dB = new((w.d, r), dtype=torch.bfloat16, device=dev) if r else None
+    if M == 0:
+        return dX, dA, dB
+    ws = _workspace(_lib.qlora_backward_workspace_bytes(M, w.d, w.k, rt), dev)
+    desc = w.desc()
+    _run("qlora_backward_checkpoint", dev, dY.data_ptr(), _ptr(ck.codes) if r else None,
+         _ptr(ck.absmax) if r else None, M, ctypes.byref(desc), w.nsec, _ptr(A), _ptr(B), r, float(alpha),
+         _ptr(keep) if r else None, float(p), _ptr(T_saved) if r else None, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
+         0 if ws is None else ws.numel())
+    return dX, dA, dB
+
+
 def adam_step(P: torch.Tensor, W: torch.Tensor, G: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
               lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
               weight_decay: float = 0.0) -> None:
@@ -589,6 +740,72 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, advantages: torch.Te
     return loss, kl, logp, dlogits
 
 
+def _tokens(tokens, T: int, dev):
+    """(pointer, number of tokens a row, whether they came as a vector)."""
+    if tokens is None:
+        return None, 0, False
+    if tokens.dtype != torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != T \
+            or not tokens.is_contiguous() or tokens.device != dev:
+        raise ValueError(f"tokens are a contiguous vector of {T}, or matrix of {T} rows, of torch.int32 on {dev}")
+    return (tokens.data_ptr(), 1, True) if tokens.dim() == 1 else (tokens.data_ptr(), tokens.shape[1], False)
+
+
+def token_scores(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0,
+                 inv_temperature: float = 1.0, save_stats: bool = False):
+    """(logp, entropy [T], top_ids [T, top], top_logp [T, top]) of T x V logits
+    (bf16 or fp32; rows may be a slice of a wider matrix): the
+    log-probabilities of the given tokens (int32 [T] or [T, m], logp of their
+    shape, None without tokens), the distribution's entropy, and its ``top``
+    (up to 64) best words, the lowest index first among equal logits.  A token
+    outside [0, V) does not count and gives 0; of a row without one that
+    counts nothing is read (entropy 0, ids -1 at -inf).  Masked words (-inf)
+    are no alternatives: past the last finite one ids are -1 at -inf.  With
+    ``save_stats`` also returns the rows' statistics for
+    ``token_scores_backward``."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    y, m, flat = _tokens(tokens, T, dev)
+    if not 0 <= top <= 64 or top > V or m > 64:
+        raise ValueError("up to 64 tokens a row and 64 alternatives, no more than there are words")
+    entropy = torch.empty(T, dtype=torch.float32, device=_on_gpu(logits))
+    logp = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    ids = torch.empty((T, top), dtype=torch.int32, device=dev)
+    best = torch.empty((T, top), dtype=torch.float32, device=dev)
+    stats = torch.empty((T, 3), dtype=torch.float32, device=dev) if save_stats else None
+    _run("qlora_token_scores", dev, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, m, int(top),
+         float(inv_temperature), _ptr(logp), entropy.data_ptr(), ids.data_ptr(), best.data_ptr(), _ptr(stats))
+    return (logp, entropy, ids, best, stats) if save_stats else (logp, entropy, ids, best)
+
+
+def token_scores_backward(dlogp: torch.Tensor | None, dentropy: torch.Tensor | None, logits: torch.Tensor,
+                          tokens: torch.Tensor | None, stats: torch.Tensor, inv_temperature: float = 1.0,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient in the logits for ``dlogp`` = d loss / d logp (fp32, of the
+    tokens' shape; None without tokens) and ``dentropy`` = d loss / d entropy
+    (fp32 [T], None for a loss without it).  ``out`` as in
+    ``token_logprobs_backward`` (it may be the logits).  A loss on the top
+    alternatives gives their ids as tokens: an id of -1 does not count, and
+    one that is there twice gets both gradients."""
+    T, V, ld = _rows(logits)
+    dev = logits.device
+    y, m, _ = _tokens(tokens, T, dev)
+    if m > 64:
+        raise ValueError("up to 64 tokens a row")
+    if (dlogp is None) != (tokens is None):
+        raise ValueError("dlogp and tokens come together")
+    if dlogp is not None and (dlogp.dtype != torch.float32 or dlogp.shape != tokens.shape
+                              or not dlogp.is_contiguous() or dlogp.device != dev):
+        raise ValueError(f"dlogp is contiguous, torch.float32, of the tokens' shape, on {dev}")
+    ge = _per("dentropy", dentropy, T, torch.float32, dev)
+    if stats.shape != (T, 3) or stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != dev:
+        raise ValueError("stats are the T x 3 values that token_scores returned")
+    out, ldd = _grad_rows(logits, out, T, V, ld)
+    _on_gpu(logits)
+    _run("qlora_token_scores_backward", dev, _ptr(dlogp), ge, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, m,
+         float(inv_temperature), stats.data_ptr(), out.data_ptr(), ldd)
+    return out
+
+
 def muon_step(P: torch.Tensor, W: torch.Tensor, G: torch.Tensor, m: torch.Tensor, lr: float, momentum: float = 0.95,
               nesterov: bool = True, weight_decay: float = 0.0, ns_steps: int = 5, scale: float | None = None,
               coefficients=None, eps: float = 1e-7) -> None:
@@ -655,7 +872,8 @@ class kernel_timing:
              "prep_adapters", "lora_proj", "lora_proj_finish", "token_reduce",
              "token_reduce_finish", "fwd_decode", "fwd_decode_finish", "fwd_rich", "dx", "drop_input", "adam",
              "fwd_sum_splits", "dx_sum_splits", "logprob", "logprob_grad", "preference", "policy", "muon_gram",
-             "muon_sum", "muon_poly", "muon_apply", "muon_whole")
+             "muon_sum", "muon_poly", "muon_apply", "muon_whole", "ck_save", "ck_load", "token_reduce_ck", "scores",
+             "scores_grad")
 
     def __enter__(self):
         _check(_lib.qlora_timing_reset(), "qlora_timing_reset")
@@ -682,4 +900,5 @@ class kernel_timing:
 __all__ = ["kernel_timing", "NF4Weight", "QloraError", "quantize", "forward", "backward", "merge", "unmerge",
            "quantize_sections", "forward_sections", "backward_sections", "forward_multi", "forward_dropout",
            "backward_dropout", "backward_noalloc", "adam_step", "token_logprobs", "token_logprobs_backward",
-           "preference_loss", "policy_loss", "muon_step", "nf4_levels", "nf4_sizes", "lib", "EXPORTED", "LIB_PATH"]
+           "preference_loss", "policy_loss", "Checkpoint", "checkpoint_save", "checkpoint_load", "forward_checkpoint",
+           "backward_checkpoint", "token_scores", "token_scores_backward", "muon_step", "nf4_levels", "nf4_sizes", "lib", "EXPORTED", "LIB_PATH"]

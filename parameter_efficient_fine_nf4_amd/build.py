@@ -32,7 +32,7 @@ LIB = os.path.join(PKG, "libqlora.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["capi.hip", "timing.hip", "quant.hip", "merge.hip", "lora.hip", "gemm_fwd.hip", "gemm_dx.hip",
-           "optim.hip", "loss.hip", "muon.hip"]
+           "optim.hip", "loss.hip", "muon.hip", "checkpoint.hip", "scores.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -388,12 +388,21 @@ static int check_dropout(const uint8_t* keep, float p) {
 }
 static float dropout_scale(float p) { return 1.0f / (1.0f - p); }
 
+// An input to be kept at 8 bits by the forward that reads it.
+struct CkOut {
+  uint8_t* codes;
+  uint16_t* absmax;
+};
+static size_t ck_codes_bytes(int64_t M, int64_t k) { return (size_t)(M * k); }
+static size_t ck_absmax_bytes(int64_t M, int64_t k) { return (size_t)(k / 64) * tsave_ld((int)M) * 2; }
+
 static int forward_impl(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int32_t nsec, const uint16_t* A,
                         const uint16_t* B, int32_t r, float alpha, uint16_t* Y, uint16_t* T_save, void* ws,
                         size_t ws_bytes, void* stream, const uint8_t* keep = nullptr, float p = 0.0f,
-                        uint16_t* Xd_save = nullptr) {
+                        uint16_t* Xd_save = nullptr, const CkOut* ck = nullptr) {
   if (int s = check_nf4(W0)) return s;
   if (X == nullptr || Y == nullptr) return QLORA_ERR_NULL;
+  if (ck != nullptr && (ck->codes == nullptr || ck->absmax == nullptr)) return QLORA_ERR_NULL;
   if (r > 0 && (A == nullptr || B == nullptr)) return QLORA_ERR_NULL;
   const int64_t d = W0->d, k = W0->k;
   if (int s = check_mdk(M, d, k)) return s;
@@ -430,6 +439,14 @@ static int forward_impl(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int
       if (overlaps(Xd_save, xb, other[i], on[i])) return QLORA_ERR_ALIAS;
     if (overlaps_nf4(Xd_save, xb, W0, nsec)) return QLORA_ERR_ALIAS;
   }
+  if (ck != nullptr) {
+    if (!aligned16(ck->codes) || !aligned16(ck->absmax)) return QLORA_ERR_ALIGN;
+    const Region out[2] = {{ck->codes, ck_codes_bytes(M, k)}, {ck->absmax, ck_absmax_bytes(M, k)}};
+    const Region in[6] = {{X, xb}, {Y, yb}, {r > 0 ? A : nullptr, ab}, {r > 0 ? B : nullptr, bb}, {T_save, tb},
+                          {ws, need.bytes}};
+    if (any_alias(out, in) || overlaps_nf4(out[0].p, out[0].n, W0, nsec) || overlaps_nf4(out[1].p, out[1].n, W0, nsec))
+      return QLORA_ERR_ALIAS;
+  }
 
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const FwdWs w = carve_forward(ws, (int)M, (int)d, (int)k, rt, drop);
@@ -438,6 +455,8 @@ static int forward_impl(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int
   const Nf4Table& tab = nf4_table();
   const int ldt = tsave_ld((int)M);
   hipError_t e = hipSuccess;
+  if (ck != nullptr) e = launch_ck_save(X, (int)M, (int)k, ck->codes, ck->absmax, st);
+  if (e != hipSuccess) return hip_status(e);
   const uint16_t* Xa = X;  // the adapter path's input
   if (drop) {
     uint16_t* xd = Xd_save != nullptr ? Xd_save : w.Xd;
@@ -539,26 +558,38 @@ size_t qlora_backward_workspace_bytes(int64_t M, int64_t d, int64_t k, int32_t r
   return carve_backward(nullptr, (int)M, (int)d, (int)k, r).bytes;
 }
 
+// An input kept at 8 bits: its codes and block constants.
+struct Ck {
+  const uint8_t* codes;
+  const uint16_t* absmax;
+};
+
 // noalloc: the workspace is the library's static scratch array of the
 // stream's GPU, looked up after every argument has been validated (ws and
 // ws_bytes are then ignored).
+// ck: the adapter path's input as a checkpoint, X being null then.  It is the
+// dropped input under LoRA dropout, T_saved is required, and nothing else of
+// the input is read.
 static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int32_t nsec,
                          const uint16_t* A, const uint16_t* B, int32_t r, float alpha, const uint16_t* T_saved,
                          uint16_t* dX, uint16_t* dA, uint16_t* dB, void* ws, size_t ws_bytes, void* stream,
                          const uint8_t* keep = nullptr, float p = 0.0f, const uint16_t* Xd_saved = nullptr,
-                         bool noalloc = false) {
+                         bool noalloc = false, const Ck* ck = nullptr) {
   if (noalloc) {
     ws = nullptr;
     ws_bytes = 0;
   }
   if (int s = check_nf4(W0)) return s;
-  if (dY == nullptr || X == nullptr) return QLORA_ERR_NULL;
+  if (dY == nullptr || (X == nullptr && ck == nullptr)) return QLORA_ERR_NULL;
   if (r > 0 && (A == nullptr || B == nullptr || dA == nullptr || dB == nullptr)) return QLORA_ERR_NULL;
+  if (ck != nullptr && r > 0 && (ck->codes == nullptr || ck->absmax == nullptr || T_saved == nullptr))
+    return QLORA_ERR_NULL;
   const int64_t d = W0->d, k = W0->k;
   if (int s = check_mdk(M, d, k)) return s;
   if (int s = check_rank_alpha(r, alpha)) return s;
   if (int s = check_sections(W0, nsec, r)) return s;
   if (M == 0) return QLORA_OK;
+  if (ck != nullptr && r > 0 && (!aligned16(ck->codes) || !aligned16(ck->absmax))) return QLORA_ERR_ALIGN;
   if (!aligned16(dY) || !aligned16(X) || !aligned16(dX) || !aligned16(ws) || check_nf4_align(W0))
     return QLORA_ERR_ALIGN;
   if (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
@@ -566,7 +597,7 @@ static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const
     return QLORA_ERR_ALIGN;
   const int rt = nsec * r;  // ranks of T and U over all sections
   const bool drop = keep != nullptr && r > 0;
-  const BwdWs need = carve_backward(nullptr, (int)M, (int)d, (int)k, rt, drop);
+  const BwdWs need = carve_backward(nullptr, (int)M, (int)d, (int)k, rt, drop && ck == nullptr);
   if (noalloc) {
     if (need.bytes > QLORA_NOALLOC_SCRATCH_BYTES) return QLORA_ERR_WORKSPACE;
   } else if (need.bytes > 0 && (ws == nullptr || ws_bytes < need.bytes)) {
@@ -598,12 +629,19 @@ static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const
       return QLORA_ERR_ALIAS;
     if (!aligned16(Xd_saved)) return QLORA_ERR_ALIGN;
   }
+  if (ck != nullptr && r > 0) {
+    const size_t cb = ck_codes_bytes(M, k), mb = ck_absmax_bytes(M, k);
+    for (int i = 0; i < 3; ++i)
+      if (overlaps(out_p[i], out_n[i], ck->codes, cb) || overlaps(out_p[i], out_n[i], ck->absmax, mb))
+        return QLORA_ERR_ALIAS;
+    if (overlaps(ws, need.bytes, ck->codes, cb) || overlaps(ws, need.bytes, ck->absmax, mb)) return QLORA_ERR_ALIAS;
+  }
 
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (noalloc && need.bytes > 0) {
     if (int sc = scratch_for_stream(st, &ws)) return sc;
   }
-  const BwdWs w = carve_backward(ws, (int)M, (int)d, (int)k, rt, drop);
+  const BwdWs w = carve_backward(ws, (int)M, (int)d, (int)k, rt, drop && ck == nullptr);
   const Nf4Dev wd = dev_view(W0, nsec);
   const float s = lora_scale(r, alpha);
   const Nf4Table& tab = nf4_table();
@@ -626,7 +664,9 @@ static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const
   // LoRA dropout: the adapter path's input is Xd (T and dA read it) and
   // dX's LoRA term is masked and scaled like the input it came from.
   const uint16_t* Xa = X;
-  if (drop && Xd_saved != nullptr) {
+  if (ck != nullptr) {
+    // (of the input itself nothing is needed)
+  } else if (drop && Xd_saved != nullptr) {
     Xa = Xd_saved;  // the forward's dropped input, same X, mask and p
   } else if (drop && e == hipSuccess) {
     e = launch_drop_input(X, keep, M * k, dropout_scale(p), w.Xd, st);
@@ -642,7 +682,10 @@ static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const
                            st);
       Tt = w.Tt;
     }
-    if (e == hipSuccess)
+    if (e == hipSuccess && ck != nullptr)
+      e = launch_token_reduce2_ck(w.Ut, ck->codes, ck->absmax, (int)k, dA, Tt, dY, (int)d, dB, ldt, (int)M, rt, nsec, s,
+                                  st);
+    else if (e == hipSuccess)
       e = launch_token_reduce2(w.Ut, Xa, (int)k, dA, false, Tt, dY, (int)d, dB, true, ldt, (int)M, rt, nsec, s, st);
   }
   return hip_status(e);
@@ -684,6 +727,65 @@ int qlora_backward_sections(const uint16_t* dY, const uint16_t* X, int64_t M, co
                             const uint16_t* T_saved, uint16_t* dX, uint16_t* dA, uint16_t* dB, void* ws,
                             size_t ws_bytes, void* stream) {
   return backward_impl(dY, X, M, W0, nsec, A, B, r, alpha, T_saved, dX, dA, dB, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------- 8-bit checkpoints ----
+
+static int check_mk(int64_t M, int64_t k) {
+  if (k < 64 || k % 64 != 0 || k >= kMaxElems || M < 0 || M >= kMaxElems || M * k >= kMaxElems) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+int qlora_checkpoint_sizes(int64_t M, int64_t k, size_t* codes_bytes, size_t* absmax_bytes) {
+  if (int s = check_mk(M, k)) return s;
+  if (codes_bytes) *codes_bytes = ck_codes_bytes(M, k);
+  if (absmax_bytes) *absmax_bytes = ck_absmax_bytes(M, k);
+  return QLORA_OK;
+}
+
+int qlora_checkpoint_save(const uint16_t* X, int64_t M, int64_t k, int8_t* codes, uint16_t* absmax, void* stream) {
+  if (int s = check_mk(M, k)) return s;
+  if (M == 0) return QLORA_OK;
+  if (X == nullptr || codes == nullptr || absmax == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(absmax)) return QLORA_ERR_ALIGN;
+  const Region out[2] = {{codes, ck_codes_bytes(M, k)}, {absmax, ck_absmax_bytes(M, k)}};
+  const Region in[1] = {{X, (size_t)(M * k) * 2}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_ck_save(X, (int)M, (int)k, reinterpret_cast<uint8_t*>(codes), absmax,
+                                   reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_checkpoint_load(const int8_t* codes, const uint16_t* absmax, int64_t M, int64_t k, uint16_t* X,
+                          void* stream) {
+  if (int s = check_mk(M, k)) return s;
+  if (M == 0) return QLORA_OK;
+  if (X == nullptr || codes == nullptr || absmax == nullptr) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(absmax)) return QLORA_ERR_ALIGN;
+  const Region out[1] = {{X, (size_t)(M * k) * 2}};
+  const Region in[2] = {{codes, ck_codes_bytes(M, k)}, {absmax, ck_absmax_bytes(M, k)}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_ck_load(reinterpret_cast<const uint8_t*>(codes), absmax, (int)M, (int)k, X,
+                                   reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_forward_checkpoint(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int32_t nsec, const uint16_t* A,
+                             const uint16_t* B, int32_t r, float alpha, uint16_t* Y, uint16_t* T_save, int8_t* codes,
+                             uint16_t* absmax, void* ws, size_t ws_bytes, void* stream) {
+  const CkOut out{reinterpret_cast<uint8_t*>(codes), absmax};
+  return forward_impl(X, M, W0, nsec, A, B, r, alpha, Y, T_save, ws, ws_bytes, stream, nullptr, 0.0f, nullptr, &out);
+}
+
+int qlora_backward_checkpoint(const uint16_t* dY, const int8_t* codes, const uint16_t* absmax, int64_t M,
+                              const qlora_nf4_t* W0, int32_t nsec, const uint16_t* A, const uint16_t* B, int32_t r,
+                              float alpha, const uint8_t* keep, float p, const uint16_t* T_saved, uint16_t* dX,
+                              uint16_t* dA, uint16_t* dB, void* ws, size_t ws_bytes, void* stream) {
+  if (r > 0 && M > 0 && keep != nullptr) {
+    if (nsec != 1) return QLORA_ERR_SHAPE;
+    if (int s = check_dropout(keep, p)) return s;
+  }
+  const Ck ck{reinterpret_cast<const uint8_t*>(codes), absmax};
+  return backward_impl(dY, nullptr, M, W0, nsec, A, B, r, alpha, T_saved, dX, dA, dB, ws, ws_bytes, stream,
+                       r > 0 ? keep : nullptr, p, nullptr, false, &ck);
 }
 
 int qlora_adam_step(uint16_t* P, float* W, const uint16_t* G, float* m, float* v, int64_t n, float lr,
@@ -819,6 +921,52 @@ int qlora_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, i
   return hip_status(launch_policy(logits, dtype, T, (int)V, ld, labels, inv_temperature, advantages, old_logp,
                                   ref_logp, weight, clip_low, clip_high, kl_coef, loss, kl, logp, dlogits, ldd,
                                   reinterpret_cast<hipStream_t>(stream)));
+}
+
+// --------------------------------------------- scores of the logits ----
+
+static int check_scores(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                        int32_t m, float tau) {
+  if (dtype != QLORA_BF16 && dtype != QLORA_F32) return QLORA_ERR_TYPE;
+  if (m < 0 || m > kMaxScores) return QLORA_ERR_SHAPE;
+  static const int32_t none = 0;  // without tokens there is no pointer to them
+  return check_logits(logits, dtype, T, V, ld, m > 0 ? tokens : &none, tau);
+}
+
+int qlora_token_scores(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* tokens,
+                       int32_t m, int32_t n, float inv_temperature, float* logp, float* entropy, int32_t* top_ids,
+                       float* top_logp, float* stats, void* stream) {
+  if (m <= 0) tokens = nullptr;
+  if (int s = check_scores(logits, dtype, T, V, ld, tokens, m, inv_temperature)) return s;
+  if (n < 0 || n > kMaxScores || n > V) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (entropy == nullptr || (m > 0 && logp == nullptr) || (n > 0 && (top_ids == nullptr || top_logp == nullptr)))
+    return QLORA_ERR_NULL;
+  if (!aligned4(logp) || !aligned4(entropy) || !aligned4(top_ids) || !aligned4(top_logp) || !aligned4(stats))
+    return QLORA_ERR_ALIGN;
+  const size_t tb = (size_t)T * 4;
+  const Region out[5] = {{logp, m * tb}, {entropy, tb}, {top_ids, n * tb}, {top_logp, n * tb}, {stats, 3 * tb}};
+  const Region in[2] = {{logits, rows_bytes(dtype, T, V, ld)}, {tokens, m * tb}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_scores(logits, dtype, T, (int)V, ld, tokens, m, n, inv_temperature, logp, entropy, top_ids,
+                                  top_logp, stats, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_token_scores_backward(const float* dlogp, const float* dentropy, const void* logits, int32_t dtype, int64_t T,
+                                int64_t V, int64_t ld, const int32_t* tokens, int32_t m, float inv_temperature,
+                                const float* stats, void* dlogits, int64_t ldd, void* stream) {
+  if (m <= 0) tokens = nullptr;
+  if (int s = check_scores(logits, dtype, T, V, ld, tokens, m, inv_temperature)) return s;
+  if (T == 0) return QLORA_OK;
+  if (stats == nullptr || dlogits == nullptr || (m > 0 && dlogp == nullptr)) return QLORA_ERR_NULL;
+  if (!aligned4(dlogp) || !aligned4(dentropy) || !aligned4(stats)) return QLORA_ERR_ALIGN;
+  if (int s = check_dlogits(dlogits, ldd, logits, dtype, T, V, ld)) return s;
+  const size_t tb = (size_t)T * 4;
+  const Region out[1] = {{dlogits, rows_bytes(dtype, T, ldd, ldd)}};
+  const Region in[4] = {{dlogp, m * tb}, {dentropy, tb}, {tokens, m * tb}, {stats, 3 * tb}};
+  if (any_alias(out, in)) return QLORA_ERR_ALIAS;
+  return hip_status(launch_scores_grad(logits, dtype, T, (int)V, ld, tokens, m, inv_temperature, stats, dlogp, dentropy,
+                                       dlogits, ldd, reinterpret_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------- orthogonalised update ----

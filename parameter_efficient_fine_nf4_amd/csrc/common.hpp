@@ -87,6 +87,16 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
   return sign | code;
 }
 
+// ------------------------------------------------ 8-bit activations ----
+
+// A checkpoint's block constant (bf16 bits of the block's absmax) -> the step
+// between its codes, and the value of the code in the low byte of w (before
+// its rounding to bf16).
+__device__ __forceinline__ float ck_scale(uint32_t absmax) {
+  return __fmul_rn(__uint_as_float(absmax << 16), 1.0f / 127.0f);
+}
+__device__ __forceinline__ float ck_value(uint32_t w, float scale) { return __fmul_rn((float)(int8_t)w, scale); }
+
 // Double-dequantised block constant a^ = fl32(fl32(e4m3(c2) * c1) + mu):
 // two separate roundings, no fused multiply-add.
 __device__ __forceinline__ float block_scale(uint32_t c2, float c1, float mu) {

@@ -108,6 +108,12 @@ hipError_t launch_token_reduce2(const uint16_t* Zt0, const uint16_t* V0, int N0,
                                 const uint16_t* Zt1, const uint16_t* V1, int N1, uint16_t* out1, bool tr1,
                                 int ldz, int M, int r, int nsec1, float s, hipStream_t st);
 
+// The same with V0 as a checkpoint (int8 codes M x N0 and its constants); more
+// than kMaxRank ranks as above.
+hipError_t launch_token_reduce2_ck(const uint16_t* Zt0, const uint8_t* codes, const uint16_t* absmax, int N0,
+                                   uint16_t* out0, const uint16_t* Zt1, const uint16_t* V1, int N1, uint16_t* out1,
+                                   int ldz, int M, int r, int nsec1, float s, hipStream_t st);
+
 // gemm_fwd.hip
 bool forward_uses_decode(int M, int d, int k);
 // Sections (w.dsec < w.d): nsec = d / dsec row sections; T holds r ranks
@@ -168,6 +174,23 @@ hipError_t launch_preference(const float* logp, const float* ref_logp, const int
                              const int32_t* cu, int64_t P, int kind, int average, float beta, float smoothing,
                              float margin, const float* weight, float* loss, float* reward, float* dlogp,
                              hipStream_t st);
+
+// checkpoint.hip: M x k bf16 activations at 8 bits: int8 codes (M x k) and one
+// bf16 constant per token and 64 columns, k/64 rows of tsave_ld(M).
+hipError_t launch_ck_save(const uint16_t* X, int M, int k, uint8_t* codes, uint16_t* absmax, hipStream_t st);
+hipError_t launch_ck_load(const uint8_t* codes, const uint16_t* absmax, int M, int k, uint16_t* X, hipStream_t st);
+
+// scores.hip: log-probabilities of the m tokens of each row, its entropy and
+// its n best words (tokens T x m, ids and top T x n; stats T x 3, optional).
+constexpr int kMaxScores = 64;  // m and n
+hipError_t launch_scores(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* tokens, int m, int n,
+                         float tau, float* logp, float* entropy, int32_t* ids, float* top, float* stats,
+                         hipStream_t st);
+// Gradient of sum(dlogp logp) + sum(dentropy entropy): T whole rows of ldd
+// elements, may be the logits themselves; dentropy may be null.
+hipError_t launch_scores_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* tokens, int m,
+                              float tau, const float* stats, const float* dlogp, const float* dentropy, void* dlogits,
+                              int64_t ldd, hipStream_t st);
 
 // muon.hip: momentum, orthogonalised update and weights of nmat matrices.
 constexpr int kMaxMuonSteps = 16;

@@ -726,33 +726,75 @@ struct RedJob {
   int dsec;
 };
 
-// Two reductions share one launch (dA and dB of a backward): work-groups
-// [0, nstrips of job 0) serve job 0, the rest job 1.
+// LDS of a strip: the waves' rings, then their partial sums in the same place.
 template <int NJ, int R, int CB>
-__global__ __launch_bounds__(64 * kRedWaves) void k_tokred(RedJob j0, RedJob j1, int ldz, int M, int rz, float s) {
+constexpr int tokred_lds(int step_bytes) {
+  const int rings = kRedWaves * R * step_bytes, sums = (kRedWaves - 1) * CB * NJ * 64 * 16;
+  return rings > sums ? rings : sums;
+}
+
+// Fixed-order sum of the waves, (((w0 + w1) + w2) + ...), scaled and stored.
+template <int NJ, int CB>
+__device__ __forceinline__ void tokred_finish(const f32x4 (&acc)[CB][NJ], char* lds, int n0, int N, int r, float s,
+                                              int out_transposed, uint16_t* __restrict__ out) {
+  constexpr int W = kRedWaves;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, sl = lane & 15;
+  float* red = reinterpret_cast<float*>(lds);
+  if (wave > 0) {
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int jb = 0; jb < NJ; ++jb)
+        *reinterpret_cast<f32x4*>(red + ((((wave - 1) * CB + cb) * NJ + jb) * 64 + lane) * 4) = acc[cb][jb];
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  // lane holds ranks jb*16 + 4g + i of column n0 + cb*16 + sl
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) {
+    const int n = n0 + cb * 16 + sl;
+#pragma unroll
+    for (int jb = 0; jb < NJ; ++jb) {
+      f32x4 v = acc[cb][jb];
+#pragma unroll
+      for (int w = 0; w < W - 1; ++w) {
+        const f32x4 o = *reinterpret_cast<const f32x4*>(red + (((w * CB + cb) * NJ + jb) * 64 + lane) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += o[i];
+      }
+      if (n >= N) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = jb * 16 + 4 * g + i;
+        if (j >= r) continue;
+        const uint16_t h = (uint16_t)pack_bf16x2(s * v[i], 0.0f);
+        if (out_transposed) out[(size_t)n * r + j] = h;
+        else out[(size_t)j * N + n] = h;
+      }
+    }
+  }
+}
+
+// One strip of a reduction: the block-th of job J.
+template <int NJ, int R, int CB>
+__device__ __forceinline__ void tokred_strip(const RedJob& J, int block, int ldz, int M, int rz, float s, char* lds) {
   constexpr int W = kRedWaves;
   constexpr int SW = 16 * CB;                         // strip width (columns)
   constexpr int RB = 2 * SW;                          // bytes per staged token row
   constexpr int CPR = RB / 16;                        // 16-byte chunks per staged row
   constexpr int kStepB = 1024 * CB + 1024 * NJ;       // V chunk, then NJ Z pieces
   constexpr int kRing = R * kStepB;                   // per wave
-  constexpr int kRedB = (W - 1) * CB * NJ * 64 * 16;  // wave partial sums
-  constexpr int kLds = W * kRing > kRedB ? W * kRing : kRedB;
-  static_assert(kLds <= 160 * 1024, "LDS");
-  __shared__ __attribute__((aligned(16))) char lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, sl = lane & 15;
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
-  const int ns0 = (j0.N + SW - 1) / SW;
-  const bool second = (int)blockIdx.x >= ns0;
-  const RedJob& J = second ? j1 : j0;
   const uint16_t* __restrict__ Zt = J.Zt;
   const uint16_t* __restrict__ V = J.V;
   const int N = J.N, out_transposed = J.out_transposed, r = J.r;
   uint16_t* __restrict__ out = J.out;
   const int nstrips = (N + SW - 1) / SW;
   int tm, strip;
-  tile_of(second ? (int)blockIdx.x - ns0 : (int)blockIdx.x, 1, nstrips, tm, strip);
+  tile_of(block, 1, nstrips, tm, strip);
   const int n0 = strip * SW;
   const int per = ((M + W - 1) / W + kRedStep - 1) / kRedStep * kRedStep;
   const int tb = wave_s * per;
@@ -840,41 +882,182 @@ __global__ __launch_bounds__(64 * kRedWaves) void k_tokred(RedJob j0, RedJob j1,
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
-  // Fixed-order sum of the waves: (((w0 + w1) + w2) + ...).
-  float* red = reinterpret_cast<float*>(lds);
-  if (wave > 0) {
+  tokred_finish<NJ, CB>(acc, lds, n0, N, r, s, out_transposed, out);
+}
+
+// Two reductions share one launch (dA and dB of a backward): work-groups
+// [0, nstrips of job 0) serve job 0, the rest job 1.
+template <int NJ, int R, int CB>
+__global__ __launch_bounds__(64 * kRedWaves) void k_tokred(RedJob j0, RedJob j1, int ldz, int M, int rz, float s) {
+  constexpr int kLds = tokred_lds<NJ, R, CB>(1024 * CB + 1024 * NJ);
+  static_assert(kLds <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  const int ns0 = (j0.N + 16 * CB - 1) / (16 * CB);
+  const bool second = (int)blockIdx.x >= ns0;
+  tokred_strip<NJ, R, CB>(second ? j1 : j0, second ? (int)blockIdx.x - ns0 : (int)blockIdx.x, ldz, M, rz, s, lds);
+}
+
+// ---- the same from a checkpoint: V is int8 codes (M x N) and constants ----
+//
+// A step's 32 tokens of a strip are CB / 2 KB of codes, the constants of their
+// one column block (a strip lies inside a block) 64 bytes.  The transposing
+// read of bytes hands a lane its column's eight tokens, which take their
+// constants in fp32 and are rounded to bf16 as a restored activation is.  The
+// 16-byte pieces of a staged row are XOR-ed with bits of the row so that the
+// 16 rows that 32 lanes read lie in distinct banks.
+struct RedJobCk {
+  const uint16_t* Zt;
+  const uint8_t* V;
+  const uint16_t* absmax;
+  int N;
+  uint16_t* out;
+  int r;
+};
+
+// Two transposing byte reads and the wait for them (as in tr_reads4).
+__device__ __forceinline__ void tr8_reads2(const char* slot, uint32_t off0, uint32_t off1, u32x2& a, u32x2& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t base = (uint32_t)(uintptr_t)slot;
+  asm volatile(
+      "ds_read_b64_tr_b8 %0, %2\n\t"
+      "ds_read_b64_tr_b8 %1, %3\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b)
+      : "v"(base + off0), "v"(base + off1)
+      : "memory");
+#else
+  (void)slot; (void)off0; (void)off1;
+  a = b = u32x2{0u, 0u};
+#endif
+}
+
+// Bytes of a step: codes, 256 of constants (64 used), NJ pieces of Z^T.
+template <int NJ, int CB>
+constexpr int tokred_ck_step() { return 512 * CB + 256 + 1024 * NJ; }
+
+template <int NJ, int R, int CB>
+__device__ __forceinline__ void tokred_strip_ck(const RedJobCk& J, int block, int ldz, int M, int rz, float s,
+                                                char* lds) {
+  constexpr int W = kRedWaves;
+  constexpr int RB = 16 * CB;     // bytes per staged token row
+  constexpr int FV = CB / 2;      // 1 KB fetches of codes per step
+  constexpr int kStepB = tokred_ck_step<NJ, CB>();
+  constexpr int kRing = R * kStepB;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, sl = lane & 15;
+  const int wave_s = __builtin_amdgcn_readfirstlane(wave);
+  const int N = J.N, r = J.r, nstrips = N / (16 * CB);
+  int tm, strip;
+  tile_of(block, 1, nstrips, tm, strip);
+  const int n0 = strip * 16 * CB;
+  const int per = ((M + W - 1) / W + kRedStep - 1) / kRedStep * kRedStep;
+  const int tb = wave_s * per;
+  const int nsw = max(0, (min(M, tb + per) - tb + kRedStep - 1) / kRedStep);  // this wave's steps
+  const BufRsrc rv = make_rsrc(J.V, (uint64_t)M * N);
+  const BufRsrc ra = make_rsrc(J.absmax, (uint64_t)(N / kBlock) * ldz * 2);
+  const BufRsrc rzb = make_rsrc(J.Zt, (uint64_t)rz * ldz * 2);
+  // rows whose 16-byte pieces meet the same banks are 256 bytes apart
+  auto fsw = [](int t) { return CB == 4 ? (t >> 2) & 3 : (t >> 3) & 1; };
+  int vrow[FV];
+  uint32_t vcol[FV];
+#pragma unroll
+  for (int u = 0; u < FV; ++u) {
+    vrow[u] = (1024 / RB) * u + lane / CB;
+    vcol[u] = (uint32_t)(n0 + ((lane % CB) ^ fsw(vrow[u])) * 16);
+  }
+  uint32_t zrow[NJ];
+#pragma unroll
+  for (int jb = 0; jb < NJ; ++jb) zrow[jb] = (uint32_t)min(jb * 16 + sl, r - 1) * (uint32_t)ldz * 2u;
+  const uint32_t arow = (uint32_t)(n0 / kBlock) * (uint32_t)ldz * 2u;
+
+  char* ring = lds + wave_s * kRing;
+  auto fetch = [&](int i) {
+    i = min(i, nsw > 0 ? nsw - 1 : 0);
+    char* slot = ring + (i % R) * kStepB;
+    const int t0 = tb + i * kRedStep;
+#pragma unroll
+    for (int u = 0; u < FV; ++u)
+      dma_lds16(rv, (uint32_t)min(t0 + vrow[u], M - 1) * (uint32_t)N + vcol[u], slot + u * 1024);
+    dma_lds4(ra, arow + (uint32_t)min(t0 + 2 * sl, ldz - 2) * 2u, slot + 512 * CB);
+    const int mz = min(t0 + 8 * g, ldz - 8);
+#pragma unroll
+    for (int jb = 0; jb < NJ; ++jb)
+      dma_lds16(rzb, zrow[jb] + (uint32_t)mz * 2u, slot + 512 * CB + 256 + jb * 1024);
+  };
+  constexpr int kPer = FV + 1 + NJ;
+
+  // transposing-read byte offsets: block cb, tokens 8g .. 8g+7; lane sl points
+  // at row 8g + sl/2, bytes cb*16 + 8*(sl%2) .. +7
+  uint32_t troff[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) {
+    const int row = 8 * g + (sl >> 1);
+    troff[cb] = (uint32_t)(row * RB + ((cb ^ fsw(row)) << 4) + (sl & 1) * 8);
+  }
+
+  f32x4 acc[CB][NJ];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int jb = 0; jb < NJ; ++jb) acc[cb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int p = 0; p < R - 1; ++p) fetch(p);
+  for (int i = 0; i < nsw; ++i) {
+    // the slot refilled now was read in the previous step
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    fetch(i + R - 1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 1) * kPer) : "memory");
+    const char* slot = ring + (i % R) * kStepB;
+    u32x2 q8[CB];
+#pragma unroll
+    for (int cb = 0; cb < CB; cb += 2) tr8_reads2(slot, troff[cb], troff[cb + 1], q8[cb], q8[cb + 1]);
+    const u32x4 am = *reinterpret_cast<const u32x4*>(slot + 512 * CB + 16 * g);  // tokens 8g .. 8g+7
+    const bool tail = tb + (i + 1) * kRedStep > M;
+    const int nvalid = M - (tb + i * kRedStep + 8 * g);  // valid tokens of this lane's operands
+    float sc[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      sc[p] = ck_scale((am[p >> 1] >> (16 * (p & 1))) & 0xFFFFu);
+      // the padding of the constants is unspecified
+      if (tail && p >= nvalid) sc[p] = 0.0f;
+    }
+    u32x4 vb[CB];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-      for (int jb = 0; jb < NJ; ++jb)
-        *reinterpret_cast<f32x4*>(red + ((((wave - 1) * CB + cb) * NJ + jb) * 64 + lane) * 4) = acc[cb][jb];
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  // lane holds ranks jb*16 + 4g + i of column n0 + cb*16 + sl
-#pragma unroll
-  for (int cb = 0; cb < CB; ++cb) {
-    const int n = n0 + cb * 16 + sl;
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t w = q8[cb][p >> 1] >> (16 * (p & 1));
+        vb[cb][p] = pack_bf16x2(ck_value(w, sc[2 * p]), ck_value(w >> 8, sc[2 * p + 1]));
+      }
 #pragma unroll
     for (int jb = 0; jb < NJ; ++jb) {
-      f32x4 v = acc[cb][jb];
+      u32x4 zz = *reinterpret_cast<const u32x4*>(slot + 512 * CB + 256 + jb * 1024 + lane * 16);
+      if (tail) {
 #pragma unroll
-      for (int w = 0; w < W - 1; ++w) {
-        const f32x4 o = *reinterpret_cast<const f32x4*>(red + (((w * CB + cb) * NJ + jb) * 64 + lane) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += o[i];
+        for (int p = 0; p < 4; ++p)
+          zz[p] &= 2 * p + 1 < nvalid ? 0xFFFFFFFFu : (2 * p < nvalid ? 0x0000FFFFu : 0u);
       }
-      if (n >= N) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = jb * 16 + 4 * g + i;
-        if (j >= r) continue;
-        const uint16_t h = (uint16_t)pack_bf16x2(s * v[i], 0.0f);
-        if (out_transposed) out[(size_t)n * r + j] = h;
-        else out[(size_t)j * N + n] = h;
-      }
+      for (int cb = 0; cb < CB; ++cb) acc[cb][jb] = mfma16(zz, vb[cb], acc[cb][jb]);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  tokred_finish<NJ, CB>(acc, lds, n0, N, r, s, 0, J.out);
+}
+
+template <int NJ, int R, int CB>
+__global__ __launch_bounds__(64 * kRedWaves) void k_tokred_ck(RedJobCk j0, RedJob j1, int ldz, int M, int rz0, int rz1,
+                                                              float s) {
+  constexpr int kLds = tokred_lds<NJ, R, CB>(1024 * CB + 1024 * NJ);  // of the bf16 strips, which take more
+  static_assert(kLds <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  const int ns0 = j0.N / (16 * CB);
+  if ((int)blockIdx.x >= ns0)
+    tokred_strip<NJ, R, CB>(j1, (int)blockIdx.x - ns0, ldz, M, rz1, s, lds);
+  else
+    tokred_strip_ck<NJ, R, CB>(j0, (int)blockIdx.x, ldz, M, rz0, s, lds);
 }
 
 static hipError_t token_reduce_launch(const RedJob& j0, const RedJob& j1, bool has1, int ldz, int M, int r,
@@ -934,6 +1117,55 @@ hipError_t launch_token_reduce2(const uint16_t* Zt0, const uint16_t* V0, int N0,
     const RedJob j1{Zt1 + (size_t)j * ldz, V1 + (size_t)p0 * dsec1, np * dsec1, N1,
                     out1 + (size_t)p0 * dsec1 * r1, 1, r1, r1, dsec1};
     e = token_reduce_launch(j0, j1, true, ldz, M, rg, s, st);
+  }
+  return e;
+}
+
+static hipError_t token_reduce_ck_launch(const RedJobCk& j0, const RedJob& j1, int ldz, int M, int r, float s,
+                                         hipStream_t st) {
+  const int rp = padded_rank(r);
+  const bool cb4 = j0.N / 64 + (j1.N + 63) / 64 >= 256;
+  const int sw = cb4 ? 64 : 32;
+  dim3 grid((unsigned)(j0.N / sw + (j1.N + sw - 1) / sw));
+#define QLORA_RED(NJ, R, CB)                                                                                     \
+  QLORA_LAUNCH("token_reduce_ck", st, (k_tokred_ck<NJ, R, CB>), grid, dim3(64 * kRedWaves), 0, st, j0, j1, ldz, M, \
+               r, r, s)
+  if (cb4) {
+    switch (rp / 16) {
+      case 1: QLORA_RED(1, 3, 4); break;
+      case 2: QLORA_RED(2, 3, 4); break;
+      case 3: QLORA_RED(3, 2, 4); break;
+      default: QLORA_RED(4, 2, 4); break;
+    }
+  } else {
+    switch (rp / 16) {
+      case 1: QLORA_RED(1, 3, 2); break;
+      case 2: QLORA_RED(2, 3, 2); break;
+      case 3: QLORA_RED(3, 3, 2); break;
+      default: QLORA_RED(4, 3, 2); break;
+    }
+  }
+#undef QLORA_RED
+  return hipGetLastError();
+}
+
+hipError_t launch_token_reduce2_ck(const uint16_t* Zt0, const uint8_t* codes, const uint16_t* absmax, int N0,
+                                   uint16_t* out0, const uint16_t* Zt1, const uint16_t* V1, int N1, uint16_t* out1,
+                                   int ldz, int M, int r, int nsec1, float s, hipStream_t st) {
+  if (nsec1 < 1 || nsec1 > kMaxSections || r % nsec1 != 0 || N1 % nsec1 != 0 || N0 % kBlock != 0)
+    return hipErrorInvalidValue;
+  const int r1 = r / nsec1, dsec1 = N1 / nsec1;
+  if (nsec1 > 1 && dsec1 % 64 != 0) return hipErrorInvalidValue;  // strips stay inside one section
+  if (r1 > kMaxRank || r > kMaxSections * kMaxRank) return hipErrorInvalidValue;
+  const int per = padded_rank(r) <= kMaxRank ? nsec1 : kMaxRank / r1;  // sections of a launch, as above
+  hipError_t e = hipSuccess;
+  for (int p0 = 0; p0 < nsec1 && e == hipSuccess; p0 += per) {
+    const int np = min(per, nsec1 - p0);
+    const int j = p0 * r1, rg = np * r1;
+    const RedJobCk j0{Zt0 + (size_t)j * ldz, codes, absmax, N0, out0 + (size_t)j * N0, rg};
+    const RedJob j1{Zt1 + (size_t)j * ldz, V1 + (size_t)p0 * dsec1, np * dsec1, N1,
+                    out1 + (size_t)p0 * dsec1 * r1, 1, r1, r1, dsec1};
+    e = token_reduce_ck_launch(j0, j1, ldz, M, rg, s, st);
   }
   return e;
 }

@@ -13,10 +13,10 @@
 // -inf counts as -256: times its e_v = 0.  k's rounding moves every x_v and their
 // mean alike, so H = ln s - ln 2 (mean x) is free of it.
 //
-// The n best words.  Every word belongs to one of 64 groups, its 16-byte
-// piece's lane.  The n-th largest of the groups' maxima is a bound L that at
-// least n words reach, and few more do (n = 20 of independent words: some 25;
-// n = 64, where L is the least of the maxima: some 300).  The maxima are formed
+// The n best words.  Every word belongs to one of 128 groups, its 16-byte
+// piece's lane and the parity of its wave.  The n-th largest of the groups'
+// maxima is a bound L that at least n words reach, and few more do (of
+// independent words, n = 20: some 22, n = 64: some 90).  The maxima are formed
 // for the row's maximum anyway; words from L on go to a list, whose order by
 // (logit, then lowest index) is counted out.  Where equal logits make the list
 // too long (a row of one value), the bound comes from counting the digits of
@@ -50,71 +50,104 @@ struct ScoreArgs {
   bool stream;
 };
 
-// Exponents and sums of a row in registers.
+// Sums are taken with c in one part, c1 = fl(c), and put right afterwards: with
+// lo = c - c1 every exponent lacks z lo (below 2^-16), so that to first order (1e-10
+// are left)
+//
+//   s = s1 (1 + ln 2 lo E z),    mean x = mean x1 + lo E z,    E z = (mean x1 + k) / c1
+//
+// (the change of the mean by lo times the exponents' variance is left out: it is
+// 2^-25 of that variance).  An exponent then takes one fused step in place of two.
+//
+// 0 times a masked word's -inf makes a sum of e x NaN where that of e is none;
+// only then are its terms taken again with the exponents held at -256.
 struct Sums {
   float s, u;  // of e and of e x
 };
 template <bool FAR>
-__device__ __forceinline__ float exponent(const RowExp& x, float z) {
-  return FAR ? x.c.times(z - x.m) : fmaf(z, x.c.lo, fmaf(z, x.c.hi, -x.k));
+__device__ __forceinline__ float exponent1(const Scale& c, float k, float ref, float z) {
+  return FAR ? (z - ref) * c.one : fmaf(z, c.one, -k);
 }
-template <typename E, int T, int N, bool FAR>
-__device__ __forceinline__ Sums regs_sums_of(const RowRegs<E, T, N>& r, const RowExp& x) {
+// PART: of the first `have` pieces (the others hold no words).
+template <typename E, int N, bool FAR, bool CLAMP, bool PART>
+__device__ __forceinline__ Sums pieces_sums_of(const u32x4 (&w)[N], int have, const Scale& c, float k, float ref) {
   constexpr int kPer = Elem<E>::kPer16;
-  const float xl = exponent<FAR>(x, r.last), el = exp2_hw(xl);
-  float s[2] = {el, 0.0f}, u[2] = {el * fmaxf(xl, kFloor), 0.0f};
+  float s[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < N; ++j) {
+    if (PART && j >= have) break;
     float f[kPer];
-    Elem<E>::unpack(anew<1 + FAR>(r.w[j]), f);
+    Elem<E>::unpack(anew<1 + PART + 2 * CLAMP>(w[j]), f);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const float xv = exponent<FAR>(x, f[q]), e = exp2_hw(xv);
+      const float x = exponent1<FAR>(c, k, ref, f[q]), e = exp2_hw(x);
       s[q & 1] += e;
-      u[q & 1] = fmaf(e, fmaxf(xv, kFloor), u[q & 1]);
+      u[q & 1] = fmaf(e, CLAMP ? fmaxf(x, kFloor) : x, u[q & 1]);
     }
   }
   return Sums{s[0] + s[1], u[0] + u[1]};
 }
+template <typename E, int N>
+__device__ __forceinline__ Sums pieces_sums(const u32x4 (&w)[N], int have, const Scale& c, float k, float ref,
+                                            bool far) {
+  if (far) return pieces_sums_of<E, N, true, true, true>(w, have, c, k, ref);
+  Sums o = have == N ? pieces_sums_of<E, N, false, false, false>(w, have, c, k, ref)
+                     : pieces_sums_of<E, N, false, false, true>(w, have, c, k, ref);
+  if (o.u != o.u && o.s == o.s) o = pieces_sums_of<E, N, false, true, true>(w, have, c, k, ref);
+  return o;
+}
+__device__ __forceinline__ Sums one_sum(float z, const Scale& c, float k, float ref, bool far) {
+  const float x = far ? exponent1<true>(c, k, ref, z) : exponent1<false>(c, k, ref, z), e = exp2_hw(x);
+  return Sums{e, e * fmaxf(x, kFloor)};
+}
 
-// Running maximum m, sum of e = exp2((z - m) c) and of e x, as Online.
+// Running maximum m of the row's pieces, with the sums of e = 2^(z c1 - K) and of
+// e x.  K is the maximum's fl(m c1) (or m c1 itself from 2^9 on).
 struct OnlineSums {
-  float m = kNegInf, s = 0.0f, u = 0.0f;
-  __device__ __forceinline__ void rescale(float ref, const Scale& c) {
-    const float d = fmaxf(c.times(m - ref), kFloor), f = exp2_hw(d);
-    u = f * fmaf(d, s, u);
-    s *= f;
+  float m = kNegInf;
+  double K = 0.0;
+  Sums sum{0.0f, 0.0f};
+  // the sums so far, relative to another K
+  __device__ __forceinline__ Sums at(double to) const {
+    const float d = fmaxf((float)(K - to), kFloor), f = exp2_hw(d);
+    return m == kNegInf ? Sums{0.0f, 0.0f} : Sums{sum.s * f, f * fmaf(d, sum.s, sum.u)};
   }
-  __device__ __forceinline__ void term(float d, const Scale& c) {
-    const float x = c.times(d), e = exp2_hw(x);
-    s += e;
-    u = fmaf(e, fmaxf(x, kFloor), u);
+  // raises the maximum; k, ref and far of the terms to come
+  __device__ __forceinline__ void raise(float mx, const Scale& c, float& k, float& ref, bool& far) {
+    ref = mx == kNegInf ? 0.0f : mx;
+    const double exact = (double)ref * (double)c.one;
+    k = (float)exact;
+    far = !(fabsf(k) < 512.0f);
+    const double to = far ? exact : (double)k;
+    sum = at(to);
+    m = mx;
+    K = to;
   }
+  // returns the pieces' own maximum
   template <typename E, int N>
-  __device__ __forceinline__ void add(const u32x4 (&w)[N], const Scale& c) {
+  __device__ __forceinline__ float add(const u32x4 (&w)[N], int have, const Scale& c) {
     constexpr int kPer = Elem<E>::kPer16;
-    float f[kPer], mx = m;
+    float f[kPer], mx = kNegInf, k, ref;
+    bool far;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       Elem<E>::unpack(anew<0>(w[j]), f);
 #pragma unroll
       for (int q = 0; q < kPer; ++q) mx = fmaxf(mx, f[q]);
     }
-    const float ref = mx == kNegInf ? 0.0f : mx;
-    rescale(ref, c);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      Elem<E>::unpack(anew<2>(w[j]), f);
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) term(f[q] - ref, c);
-    }
-    m = mx;
+    raise(fmaxf(m, mx), c, k, ref, far);
+    const Sums o = pieces_sums<E>(w, have, c, k, ref, far);
+    sum.s += o.s;
+    sum.u += o.u;
+    return mx;
   }
-  __device__ __forceinline__ void add_one(float f, const Scale& c) {
-    const float mx = fmaxf(m, f), ref = mx == kNegInf ? 0.0f : mx;
-    rescale(ref, c);
-    term(f - ref, c);
-    m = mx;
+  __device__ __forceinline__ void add_one(float z, const Scale& c) {
+    float k, ref;
+    bool far;
+    raise(fmaxf(m, z), c, k, ref, far);
+    const Sums o = one_sum(z, c, k, ref, far);
+    sum.s += o.s;
+    sum.u += o.u;
   }
 };
 
@@ -125,6 +158,11 @@ __device__ __forceinline__ void load_pieces(const E* z, const RowSpan& at, int i
     w[j] = u32x4{Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill, Elem<E>::kFill};
     if (i0 + j * T < at.nv) w[j] = *reinterpret_cast<const u32x4*>(z + at.head + (size_t)(i0 + j * T) * Elem<E>::kPer16);
   }
+}
+
+// How many of a thread's N pieces i0, i0 + T, ... there are.
+__device__ __forceinline__ int pieces_there(const RowSpan& at, int i0, int T, int N) {
+  return i0 < at.nv ? min(N, (at.nv - 1 - i0) / T + 1) : 0;
 }
 
 // ------------------------------------------------------ the best words ----
@@ -140,25 +178,28 @@ __device__ __forceinline__ float float_of(uint32_t k) {
 // A word's place in the order: by logit, then the lowest index.
 __device__ __forceinline__ uint64_t place_of(float f, int i) { return (uint64_t)order_of(f) << 32 | (uint32_t)~i; }
 
-// Largest value of 16 leading bits that at least n of the lanes' maxima reach,
-// finite: a masked word is no alternative.
-__device__ __forceinline__ float bound_of(float lane_max, int n) {
-  const uint32_t key = order_of(lane_max) >> 16;
+// Largest value of 16 leading bits that at least n of the 128 maxima (two a lane)
+// reach, finite: a masked word is no alternative.
+__device__ __forceinline__ float bound_of(float a, float b, int n) {
+  const uint32_t ka = order_of(a) >> 16, kb = order_of(b) >> 16;
   uint32_t k = 0u;
 #pragma unroll
-  for (int b = 15; b >= 0; --b) {
-    const uint32_t t = k | (1u << b);
-    if (__popcll(__ballot(key >= t)) >= n) k = t;
+  for (int i = 15; i >= 0; --i) {
+    const uint32_t t = k | (1u << i);
+    if (__popcll(__ballot(ka >= t)) + __popcll(__ballot(kb >= t)) >= n) k = t;
   }
   return k <= 0x007Fu ? kLowest : float_of(k << 16);
 }
 
-constexpr int kList = 1024;  // words that the list holds
+// words, and parts of a row, that a list holds (fewer than 64 pieces, which may leave
+// n = 64 no bound, have up to 526 words)
+constexpr int kList = 640;
 
 struct Best {
-  uint64_t list[kList];
-  int count;
-  int need, above;      // of the counting by digits
+  __attribute__((aligned(16))) uint64_t list[kList + 32];
+  uint16_t part[kList];  // parts with words from the bound on: step * threads + thread
+  int parts, count;
+  int need;  // of the counting by digits
   uint64_t prefix;
   int bins[256];
 };
@@ -168,19 +209,23 @@ __device__ __forceinline__ void best_add(Best& b, float f, int i) {
   if (at < kList) b.list[at] = place_of(f, i);
 }
 
+// One piece's words from the bound on, with one addition to the list's length.
 template <typename E>
 __device__ __forceinline__ void best_piece(Best& b, const u32x4& w, int i0, float bound) {
   constexpr int kPer = Elem<E>::kPer16;
   float f[kPer];
   Elem<E>::unpack(w, f);
-  float mx = f[0];
+  int c = 0;
 #pragma unroll
-  for (int q = 1; q < kPer; ++q) mx = fmaxf(mx, f[q]);
-  if (mx >= bound) {
+  for (int q = 0; q < kPer; ++q) c += f[q] >= bound ? 1 : 0;
+  if (c == 0) return;
+  int at = atomicAdd(&b.count, c);
 #pragma unroll
-    for (int q = 0; q < kPer; ++q)
-      if (f[q] >= bound) best_add(b, f[q], i0 + q);
-  }
+  for (int q = 0; q < kPer; ++q)
+    if (f[q] >= bound) {
+      if (at < kList) b.list[at] = place_of(f[q], i0 + q);
+      ++at;
+    }
 }
 
 // Every finite word of the row, by whole work-groups' steps: fn(value, index).
@@ -243,16 +288,32 @@ __device__ void best_by_digits(const E* z, int V, int n, Best& b) {
 
 // ------------------------------------------------------------- forward ----
 
+// The leading half of a float, an order that comparisons of floats imply.
+__device__ __forceinline__ uint16_t half_of(float f) { return (uint16_t)(__float_as_uint(f) >> 16); }
+__device__ __forceinline__ bool half_reaches(uint16_t h, float bound) {
+  return bf16_to_f32(h) >= __uint_as_float(__float_as_uint(bound) & 0xFFFF0000u);
+}
+
+// Steps of a row read in pieces whose maxima are kept apart; the last one's stands
+// for all that follow.
+template <int T>
+constexpr int kept_steps() { return T <= 256 ? 4 : 16; }
+
 // A row a work-group, as in the losses: N > 0 pieces a thread in registers, N <
-// 0: -N pieces a thread at a time.
+// 0: -N pieces a thread at a time.  The maxima of a row's parts (a thread's pieces,
+// or its steps) stay in LDS, so that the words from the bound on are looked for in
+// few of them.
 template <typename E, int T, int N>
 __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
-  constexpr int W = T / 64;
+  constexpr int W = T / 64, P = N < 0 ? -N : N;
+  constexpr int Q = N < 0 ? P : 1;  // pieces of a part
   __shared__ float maxima[W][64];
   __shared__ float sums[W], means[W];
   __shared__ float bound_sh;
   __shared__ double ln_sh;
   __shared__ Best best;
+  constexpr int kSteps = kept_steps<T>();
+  __shared__ uint16_t part_max[N < 0 ? kSteps : N][T];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = a.first + blockIdx.x;
   const int token = lane < a.m ? a.tokens[t * a.m + lane] : -1;
@@ -279,44 +340,64 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
   RowRegs<E, T, N < 0 ? 1 : N> r;
   const RowSpan at(z, a.V);
   OnlineSums o;
-  float own;  // this thread's largest
+  float own, even, odd = kNegInf;  // this thread's largest, those of its even and its odd pieces
   if constexpr (N > 0) {
     r.load(z, a.V, at);
-    own = r.max();
+    even = r.last;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float f[Elem<E>::kPer16], mx = kNegInf;
+      Elem<E>::unpack(anew<0>(r.w[j]), f);
+#pragma unroll
+      for (int q = 0; q < Elem<E>::kPer16; ++q) mx = fmaxf(mx, f[q]);
+      if (a.n > 0) part_max[j][threadIdx.x] = half_of(mx);
+      (j % 2 != 0 ? odd : even) = fmaxf(j % 2 != 0 ? odd : even, mx);
+    }
+    own = fmaxf(even, odd);
   } else {
-    for (int i0 = threadIdx.x; i0 < at.nv; i0 += -N * T) {
-      u32x4 w[N < 0 ? -N : 1];
+    float rest = kNegInf;  // of the last steps together
+    int step = 0;
+    for (int i0 = threadIdx.x; i0 < at.nv; i0 += P * T, ++step) {
+      u32x4 w[P];
       load_pieces<E>(z, at, i0, T, w);
-      o.template add<E>(w, a.c);
+      const float mx = o.template add<E>(w, pieces_there(at, i0, T, P), a.c);
+      if (step >= kSteps - 1) rest = fmaxf(rest, mx);
+      part_max[min(step, kSteps - 1)][threadIdx.x] = half_of(step >= kSteps - 1 ? rest : mx);
     }
     if (at.rest < a.V) o.add_one(Elem<E>::get(z + at.rest), a.c);
     own = o.m;
   }
-  float group = own;
+  // the two groups of this lane: its words in the even and in the odd waves (with
+  // one wave, in its even and odd pieces)
+  static_assert(N > 0 || T > 64, "one wave holds its row");
   if (T > 64) {
     maxima[wave][lane] = own;
     __syncthreads();
-    group = maxima[0][lane];
+    even = maxima[0][lane];
+    odd = maxima[W > 1 ? 1 : 0][lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) group = fmaxf(group, maxima[w][lane]);
+    for (int w = 2; w < W; w += 2) {
+      even = fmaxf(even, maxima[w][lane]);
+      odd = fmaxf(odd, maxima[w + 1][lane]);
+    }
   }
-  const float m = wave_max(group);
+  const float m = wave_max(fmaxf(even, odd));
   if (a.n > 0 && wave == 0) {
-    const float bound = bound_of(group, a.n);
+    const float bound = bound_of(even, odd, a.n);
     if (lane == 0) {
       bound_sh = bound;
-      best.count = 0;
+      best.count = best.parts = 0;
     }
   }
   const RowExp x(m, a.c);
   Sums sum;
   if constexpr (N > 0) {
-    sum = x.far ? regs_sums_of<E, T, N, true>(r, x) : regs_sums_of<E, T, N, false>(r, x);
+    sum = pieces_sums<E>(r.w, pieces_there(at, threadIdx.x, T, N), a.c, x.k, m, x.far);
+    const Sums l = one_sum(r.last, a.c, x.k, m, x.far);
+    sum.s += l.s;
+    sum.u += l.u;
   } else {
-    // from a thread's own maximum to the row's (a row of nothing but -inf has
-    // no distribution: NaN)
-    const float d = a.c.times(o.m - m), f = exp2_hw(d);
-    sum = Sums{o.s * f, f * fmaf(fmaxf(d, kFloor), o.s, o.u)};
+    sum = o.at(x.far ? (double)m * (double)a.c.one : (double)x.k);
   }
   float s = wave_sum(sum.s), u = wave_sum(sum.u);
   if (T > 64) {
@@ -333,13 +414,35 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
       u += means[w];
     }
   }
-  float mean = u / s;
-  if constexpr (N < 0) {
-    s *= x.shift();
-    if (!x.far) mean += (float)((double)m * a.c.c - (double)x.k);
+  const bool real = s == s && fabsf(m) < __builtin_inff();  // else no distribution: a NaN, +inf, nothing but -inf
+  if (a.n > 0 && real) {
+    if (T == 64) __syncthreads();  // the bound (with more waves, before the sums)
+    const float bound = bound_sh;
+    if (own >= bound) {  // which of this thread's parts
+      uint32_t mask = 0u;
+      const int parts = N > 0 ? N : min((at.nv - 1 - (int)threadIdx.x) / (P * T) + 1, kSteps);
+      if (N > 0 || (int)threadIdx.x < at.nv)
+        for (int j = 0; j < parts; ++j) mask |= half_reaches(part_max[j][threadIdx.x], bound) ? 1u << j : 0u;
+      if (mask != 0u) {
+        int to = atomicAdd(&best.parts, (int)__popc(mask));
+        for (; mask != 0u; mask &= mask - 1u, ++to)
+          if (to < kList) best.part[to] = (uint16_t)((__ffs(mask) - 1) * T + (int)threadIdx.x);
+      }
+      if (at.rest < a.V) {
+        const float f = N > 0 ? r.last : Elem<E>::get(z + at.rest);
+        if (f >= bound) best_add(best, f, at.rest);
+      }
+    }
   }
-  const bool real = s == s;
   if (wave == 0) {  // fp64, once: one wave
+    float mean = u / s;
+    {
+      const double lo = a.c.c - (double)a.c.one;
+      const float off = (float)(lo / (double)a.c.one * ((double)mean + (x.far ? 0.0 : (double)x.k)));
+      s = fmaf(s, (float)kLn2 * off, s);
+      mean += off;
+    }
+    if (!real) s = mean = __builtin_nanf("");
     const double ln_sum = x.ln_sum(s);
     if (lane < a.m)
       a.logp[t * a.m + lane] = counted ? (float)(((double)zy - (double)m) * (double)a.tau - ln_sum) : 0.0f;
@@ -357,42 +460,40 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
   if (a.n == 0) return;
   __syncthreads();
   if (real) {
+    // the parts' pieces again, dealt out anew: a piece a thread
+    const int units = min(best.parts, kList) * Q;
     const float bound = bound_sh;
-    if (own >= bound) {
-      if constexpr (N > 0) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          best_piece<E>(best, anew<3>(r.w[j]), at.head + (j * T + (int)threadIdx.x) * Elem<E>::kPer16, bound);
-      } else {
-        for (int i0 = threadIdx.x; i0 < at.nv; i0 += 4 * T) {
-          u32x4 w[4];
-          load_pieces<E>(z, at, i0, T, w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) best_piece<E>(best, w[j], at.head + (i0 + j * T) * Elem<E>::kPer16, bound);
-        }
-      }
-      if (at.rest < a.V) {
-        const float f = N > 0 ? r.last : Elem<E>::get(z + at.rest);
-        if (f >= bound) best_add(best, f, at.rest);
-      }
+    for (int i = threadIdx.x; i < units; i += T) {
+      const int part = best.part[i / Q], step = part / T;
+      int piece = step * Q * T + part % T + i % Q * T;
+      const int last = N < 0 && step == kSteps - 1 ? at.nv : min(at.nv, piece + 1);
+      for (; piece < last; piece += Q * T)
+        best_piece<E>(best, *reinterpret_cast<const u32x4*>(z + at.head + (size_t)piece * Elem<E>::kPer16),
+                      at.head + piece * Elem<E>::kPer16, bound);
     }
     __syncthreads();
-    if (best.count > kList) best_by_digits<E, T>(z, a.V, a.n, best);
+    if (best.parts > kList || best.count > kList) best_by_digits<E, T>(z, a.V, a.n, best);
   }
+  // a word's rank is the number of those before it; four threads count it
   const int count = real ? best.count : 0;
   const double ln_sum = ln_sh;
-  for (int i = threadIdx.x; i < count; i += T) {
-    const uint64_t p = best.list[i];
+  for (int i = threadIdx.x; i < 4 * count; i += T) {
+    const uint64_t p = best.list[i >> 2];
     int rank = 0;
-    for (int j = 0; j < count; ++j) rank += best.list[j] > p ? 1 : 0;
-    if (rank < a.n) {
+    for (int j = i & 3; j < count; j += 32) {
+#pragma unroll
+      for (int q = 0; q < 32; q += 4) rank += best.list[j + q] > p && j + q < count ? 1 : 0;
+    }
+    rank += __builtin_amdgcn_mov_dpp(rank, 0xB1, 0xF, 0xF, true);  // lanes 1, 0, 3, 2
+    rank += __builtin_amdgcn_mov_dpp(rank, 0x4E, 0xF, 0xF, true);  // lanes 2, 3, 0, 1
+    if ((i & 3) == 0 && rank < a.n) {
       a.ids[t * a.n + rank] = (int)~(uint32_t)p;
       a.top[t * a.n + rank] = (float)(((double)float_of((uint32_t)(p >> 32)) - (double)m) * (double)a.tau - ln_sum);
     }
   }
   for (int i = count + (int)threadIdx.x; i < a.n; i += T) {
     a.ids[t * a.n + i] = -1;
-    a.top[t * a.n + i] = real ? kNegInf : s;
+    a.top[t * a.n + i] = real ? kNegInf : __builtin_nanf("");
   }
 }
 
@@ -407,7 +508,9 @@ struct GradOf {
 template <typename E, bool FAR, bool ENT>
 __device__ __forceinline__ float grad_value(float z, const RowExp& x, const GradOf& g) {
   if (!ENT) return (FAR ? x.far_e(z) : x.template near_g<E>(z)) * g.A;
-  const float xv = exponent<FAR>(x, z);
+  // (one part of c for bf16, as in near_g)
+  const float xv = FAR ? x.c.times(z - x.m)
+                       : (sizeof(E) == 2 ? fmaf(z, x.c.one, -x.k) : fmaf(z, x.c.lo, fmaf(z, x.c.hi, -x.k)));
   return exp2_hw(xv) * fmaf(fmaxf(xv, kFloor) - g.mean, g.B, g.A);
 }
 template <typename E, bool FAR, bool ENT>
@@ -488,7 +591,7 @@ __global__ __launch_bounds__(T) void k_scores_grad(ScoreArgs a) {
   __syncthreads();
   if (first) {
     const float v = x.far ? (gh != 0.0f ? grad_value<E, true, true>(zy, x, go) : grad_value<E, true, false>(zy, x, go))
-                          : (gh != 0.0f ? grad_value<E, false, true>(zy, x, go) : grad_value<float, false, false>(zy, x, go));
+                          : (gh != 0.0f ? grad_value<float, false, true>(zy, x, go) : grad_value<float, false, false>(zy, x, go));
     Elem<E>::put(out + token, fmaf(sum, a.tau, v));
   }
 }
@@ -512,20 +615,10 @@ static hipError_t launch_scores_of(const ScoreArgs& a, hipStream_t st) {
   else if (a.T <= 256 && pieces > 1024 && pieces <= 1024 * 16)
     pieces <= 1024 * 4 ? scores_kernel<E, 1024, 4>(a, st)
                        : (pieces <= 1024 * 8 ? scores_kernel<E, 1024, 8>(a, st) : scores_kernel<E, 1024, 16>(a, st));
-  else if (pieces <= 256 * 4)
-    scores_kernel<E, 256, 4>(a, st);
-  else if (pieces <= 256 * 8)
-    scores_kernel<E, 256, 8>(a, st);
-  else if (pieces <= 256 * 12)
-    scores_kernel<E, 256, 12>(a, st);
-  else if (pieces <= 512 * 8)
-    scores_kernel<E, 512, 8>(a, st);
-  else if (pieces <= 512 * 12)
-    scores_kernel<E, 512, 12>(a, st);
-  else if (pieces <= 512 * 16)
-    scores_kernel<E, 512, 16>(a, st);
+  else if (pieces <= 4096)
+    scores_kernel<E, 256, -4>(a, st);
   else
-    scores_kernel<E, 1024, -4>(a, st);
+    scores_kernel<E, 512, -4>(a, st);
   return hipGetLastError();
 }
 

@@ -147,7 +147,7 @@ def _check_grad(lib, z, y, g, gh, stats, tau, dtype, out=None, zh=None):
 SIZES = [(1, 1, 1, 1), (2, 2, 3, 2), (3, 7, 2, 7), (5, 8, 1, 5), (9, 64, 4, 64), (33, 200, 1, 20), (4, 255, 5, 64),
          (7, 513, 2, 64), (9, 2048, 64, 64), (7, 2049, 2, 33), (6, 4099, 1, 20), (5, 8191, 9, 5), (4, 16385, 3, 20),
          (3, 32000, 33, 20), (3, 32769, 1, 64), (2, 50021, 2, 1), (2, 65537, 1, 20), (2, 131072, 1, 20),
-         (2, 131077, 4, 64), (1, 262147, 1, 20), (300, 9001, 1, 20), (300, 33000, 2, 8), (270, 70001, 1, 5)]
+         (2, 131077, 4, 64), (1, 262147, 1, 20), (2, 600011, 2, 64), (300, 9001, 1, 20), (300, 33000, 2, 8), (270, 70001, 1, 5)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])

@@ -422,44 +422,52 @@ class Checkpoint:
         if M < 0 or k < 64 or k % 64:
             raise ValueError("a checkpoint has M >= 0 tokens of k columns, a multiple of 64")
         return Checkpoint(M, k, torch.empty((M, k), dtype=torch.int8, device=device),
-                          torch.empty((k // 64, -(-M // 64) * 64), dtype=torch.bfloat16, device=device))
+                          torch.empty((k // 64, (M + 63) // 64 * 64), dtype=torch.bfloat16, device=device))
 
     def check(self, M: int, k: int, device) -> None:
         """Raise unless this is the checkpoint of an M x k tensor on ``device``."""
-        if (self.M, self.k) != (M, k):
+        if self.M != M or self.k != k:
             raise ValueError(f"the checkpoint is of {self.M} x {self.k}, not {M} x {k}")
-        for name, t, dtype, shape in (("codes", self.codes, torch.int8, (M, k)),
-                                      ("absmax", self.absmax, torch.bfloat16, (k // 64, -(-M // 64) * 64))):
-            if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-                raise ValueError(f"{name} is contiguous, {dtype}, of shape {shape}, on {device}")
+        _dense("codes", self.codes, torch.int8, (M, k), device)
+        _dense("absmax", self.absmax, torch.bfloat16, (k // 64, (M + 63) // 64 * 64), device)
 
 
-def _activation(name: str, t: torch.Tensor, cols: int | None = None) -> torch.device:
-    if t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous() or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} is a contiguous bfloat16 matrix" + (f" of {cols} columns" if cols is not None else ""))
+def _dense(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    """Raise unless t is a contiguous tensor of that type and shape on ``device``."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} is contiguous, {dtype}, of shape {tuple(shape)}, on {device}")
+
+
+def _activation(name: str, t: torch.Tensor) -> torch.device:
+    """The GPU of a contiguous bf16 matrix."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous bfloat16 matrix")
     return _on_gpu(t)
 
 
 def checkpoint_save(X: torch.Tensor, out: Checkpoint | None = None) -> Checkpoint:
     """X (M x k bf16, k a multiple of 64) at 8 bits: int8 codes and a bf16
     constant for every 64 columns of a token."""
-    M, k = X.shape if X.dim() == 2 else (0, 0)
     dev = _activation("X", X)
-    ck = out if out is not None else Checkpoint.empty(M, k, dev)
-    ck.check(M, k, dev)
-    _run("qlora_checkpoint_save", dev, X.data_ptr(), M, k, ck.codes.data_ptr(), ck.absmax.data_ptr())
-    return ck
+    M, k = X.shape
+    if out is None:
+        out = Checkpoint.empty(M, k, dev)
+    else:
+        out.check(M, k, dev)
+    _run("qlora_checkpoint_save", dev, X.data_ptr(), M, k, out.codes.data_ptr(), out.absmax.data_ptr())
+    return out
 
 
 def checkpoint_load(ck: Checkpoint, out: torch.Tensor | None = None) -> torch.Tensor:
     """What the checkpoint stands for (M x k bf16)."""
     dev = _on_gpu(ck.codes)
     ck.check(ck.M, ck.k, dev)
-    X = out if out is not None else torch.empty((ck.M, ck.k), dtype=torch.bfloat16, device=dev)
-    if _activation("out", X, ck.k) != dev or X.shape[0] != ck.M:
-        raise ValueError(f"out is {ck.M} x {ck.k} on {dev}")
-    _run("qlora_checkpoint_load", dev, ck.codes.data_ptr(), ck.absmax.data_ptr(), ck.M, ck.k, X.data_ptr())
-    return X
+    if out is None:
+        out = torch.empty((ck.M, ck.k), dtype=torch.bfloat16, device=dev)
+    else:
+        _dense("out", out, torch.bfloat16, (ck.M, ck.k), dev)
+    _run("qlora_checkpoint_load", dev, ck.codes.data_ptr(), ck.absmax.data_ptr(), ck.M, ck.k, out.data_ptr())
+    return out
 
 
 def _adapter(w: NF4Weight, A, B, device) -> int:
@@ -468,13 +476,12 @@ def _adapter(w: NF4Weight, A, B, device) -> int:
         return 0
     if A is None or B is None:
         raise ValueError("A and B come together")
-    rt = A.shape[0] if A.dim() == 2 else -1
-    for name, t, shape in (("A", A, (rt, w.k)), ("B", B, (w.d, rt // w.nsec))):
-        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} is contiguous, torch.bfloat16, of shape {shape}, on {device}")
-    if rt % w.nsec:
+    rt, nsec = A.shape[0], w.nsec
+    if rt % nsec:
         raise ValueError("A holds the same number of ranks for every section")
-    return rt // w.nsec
+    _dense("A", A, torch.bfloat16, (rt, w.k), device)
+    _dense("B", B, torch.bfloat16, (w.d, rt // nsec), device)
+    return rt // nsec
 
 
 def forward_checkpoint(X: torch.Tensor, w: NF4Weight, A=None, B=None, alpha: float = 0.0,
@@ -483,25 +490,29 @@ def forward_checkpoint(X: torch.Tensor, w: NF4Weight, A=None, B=None, alpha: flo
     sections) that keeps what ``backward_checkpoint`` needs: T and, in place
     of X, its checkpoint (written into ``ck`` if given).  T is None without an
     adapter."""
-    dev = _activation("X", X, w.k)
-    M = X.shape[0]
+    dev = _activation("X", X)
+    M, k = X.shape
+    if k != w.k or w.codes.device != dev:
+        raise ValueError(f"X and the weight have the same {w.k} columns and are on one GPU")
     r = _adapter(w, A, B, dev)
     rt = r * w.nsec
-    Y = out if out is not None else torch.empty((M, w.d), dtype=torch.bfloat16, device=dev)
-    if _activation("out", Y, w.d) != dev or Y.shape[0] != M or w.device != dev:
-        raise ValueError(f"the weight and out ({M} x {w.d}) are on {dev}")
-    T = torch.empty((rt, -(-M // 64) * 64), dtype=torch.bfloat16, device=dev) if r > 0 else None
+    if out is None:
+        out = torch.empty((M, w.d), dtype=torch.bfloat16, device=dev)
+    else:
+        _dense("out", out, torch.bfloat16, (M, w.d), dev)
+    T = torch.empty((rt, (M + 63) // 64 * 64), dtype=torch.bfloat16, device=dev) if r > 0 else None
     if ck is None:
-        ck = Checkpoint.empty(M, w.k, dev)
-    ck.check(M, w.k, dev)
+        ck = Checkpoint.empty(M, k, dev)
+    else:
+        ck.check(M, k, dev)
     if M == 0:  # empty tensors have no address
-        return Y, T, ck
-    ws = _workspace(_lib.qlora_forward_workspace_bytes(M, w.d, w.k, rt), dev)
+        return out, T, ck
+    nws = _lib.qlora_forward_workspace_bytes(M, w.d, k, rt)
+    ws = _workspace(nws, dev)
     desc = w.desc()
     _run("qlora_forward_checkpoint", dev, X.data_ptr(), M, ctypes.byref(desc), w.nsec, _ptr(A), _ptr(B), r,
-         float(alpha), Y.data_ptr(), _ptr(T), ck.codes.data_ptr(), ck.absmax.data_ptr(), _ptr(ws),
-         0 if ws is None else ws.numel())
-    return Y, T, ck
+         float(alpha), out.data_ptr(), _ptr(T), ck.codes.data_ptr(), ck.absmax.data_ptr(), _ptr(ws), nws)
+    return out, T, ck
 
 
 def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, B=None, alpha: float = 0.0,
@@ -512,32 +523,33 @@ def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, 
     with an adapter.  With ``keep`` and ``p`` the gradients are
     ``backward_dropout``'s, ck being the checkpoint of the dropped input
     (``forward_dropout``'s xd_out)."""
-    dev = _activation("dY", dY, w.d)
-    M = dY.shape[0]
+    dev = _activation("dY", dY)
+    M, k, d = dY.shape[0], w.k, w.d
+    if dY.shape[1] != d or w.codes.device != dev:
+        raise ValueError(f"dY has the weight's {d} columns and is on its GPU")
     r = _adapter(w, A, B, dev)
     rt = r * w.nsec
-    if w.device != dev:
-        raise ValueError(f"the weight is on {dev}")
+    codes = absmax = mask = dA = dB = T = None
     if r > 0:
-        ck.check(M, w.k, dev)
-        if T_saved is None or T_saved.dtype != torch.bfloat16 or T_saved.numel() < rt * (-(-M // 64) * 64) \
-                or not T_saved.is_contiguous() or T_saved.device != dev:
+        ck.check(M, k, dev)
+        codes, absmax, T = ck.codes.data_ptr(), ck.absmax.data_ptr(), T_saved
+        if T is None or T.dtype is not torch.bfloat16 or T.numel() < rt * ((M + 63) // 64 * 64) \
+                or not T.is_contiguous() or T.device != dev:
             raise ValueError("T_saved is the T that the forward returned")
-        if keep is not None and (keep.dtype != torch.uint8 or keep.shape != (M, w.k) or not keep.is_contiguous()
-                                 or keep.device != dev):
-            raise ValueError(f"keep is a contiguous uint8 mask of {M} x {w.k} on {dev}")
-    dX = torch.empty((M, w.k), dtype=torch.bfloat16, device=dev) if need_dx else None
-    new = torch.empty if M else torch.zeros  # without a token the sums are empty and nothing is launched
-    dA = new((rt, w.k), dtype=torch.bfloat16, device=dev) if r else None
-    dB = new((w.d, r), dtype=torch.bfloat16, device=dev) if r else None
+        if keep is not None:
+            _dense("keep", keep, torch.uint8, (M, k), dev)
+            mask = keep.data_ptr()
+        new = torch.empty if M else torch.zeros  # without a token the sums are empty and nothing is launched
+        dA = new((rt, k), dtype=torch.bfloat16, device=dev)
+        dB = new((d, r), dtype=torch.bfloat16, device=dev)
+    dX = torch.empty((M, k), dtype=torch.bfloat16, device=dev) if need_dx else None
     if M == 0:
         return dX, dA, dB
-    ws = _workspace(_lib.qlora_backward_workspace_bytes(M, w.d, w.k, rt), dev)
+    nws = _lib.qlora_backward_workspace_bytes(M, d, k, rt)
+    ws = _workspace(nws, dev)
     desc = w.desc()
-    _run("qlora_backward_checkpoint", dev, dY.data_ptr(), _ptr(ck.codes) if r else None,
-         _ptr(ck.absmax) if r else None, M, ctypes.byref(desc), w.nsec, _ptr(A), _ptr(B), r, float(alpha),
-         _ptr(keep) if r else None, float(p), _ptr(T_saved) if r else None, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
-         0 if ws is None else ws.numel())
+    _run("qlora_backward_checkpoint", dev, dY.data_ptr(), codes, absmax, M, ctypes.byref(desc), w.nsec, _ptr(A),
+         _ptr(B), r, float(alpha), mask, float(p), _ptr(T), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), nws)
     return dX, dA, dB
 
 
@@ -756,7 +768,8 @@ def token_scores(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: 
     (bf16 or fp32; rows may be a slice of a wider matrix): the
     log-probabilities of the given tokens (int32 [T] or [T, m], logp of their
     shape, None without tokens), the distribution's entropy, and its ``top``
-    (up to 64) best words, the lowest index first among equal logits.  A token
+    (up to 64) best words, the lowest index first among equal logits (both
+    None for top = 0).  A token
     outside [0, V) does not count and gives 0; of a row without one that
     counts nothing is read (entropy 0, ids -1 at -inf).  Masked words (-inf)
     are no alternatives: past the last finite one ids are -1 at -inf.  With
@@ -769,11 +782,14 @@ def token_scores(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: 
         raise ValueError("up to 64 tokens a row and 64 alternatives, no more than there are words")
     entropy = torch.empty(T, dtype=torch.float32, device=_on_gpu(logits))
     logp = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    ids = torch.empty((T, top), dtype=torch.int32, device=dev)
-    best = torch.empty((T, top), dtype=torch.float32, device=dev)
-    stats = torch.empty((T, 3), dtype=torch.float32, device=dev) if save_stats else None
+    ids = best = stats = None
+    if top:
+        ids = torch.empty((T, top), dtype=torch.int32, device=dev)
+        best = torch.empty((T, top), dtype=torch.float32, device=dev)
+    if save_stats:
+        stats = torch.empty((T, 3), dtype=torch.float32, device=dev)
     _run("qlora_token_scores", dev, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, m, int(top),
-         float(inv_temperature), _ptr(logp), entropy.data_ptr(), ids.data_ptr(), best.data_ptr(), _ptr(stats))
+         float(inv_temperature), _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(best), _ptr(stats))
     return (logp, entropy, ids, best, stats) if save_stats else (logp, entropy, ids, best)
 
 

@@ -497,10 +497,10 @@ def forward_checkpoint(X: torch.Tensor, w: NF4Weight, A=None, B=None, alpha: flo
     r = _adapter(w, A, B, dev)
     rt = r * w.nsec
     if out is None:
-        out = torch.empty((M, w.d), dtype=torch.bfloat16, device=dev)
+        out = X.new_empty((M, w.d))
     else:
         _dense("out", out, torch.bfloat16, (M, w.d), dev)
-    T = torch.empty((rt, (M + 63) // 64 * 64), dtype=torch.bfloat16, device=dev) if r > 0 else None
+    T = X.new_empty((rt, (M + 63) // 64 * 64)) if r > 0 else None
     if ck is None:
         ck = Checkpoint.empty(M, k, dev)
     else:
@@ -539,10 +539,9 @@ def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, 
         if keep is not None:
             _dense("keep", keep, torch.uint8, (M, k), dev)
             mask = keep.data_ptr()
-        new = torch.empty if M else torch.zeros  # without a token the sums are empty and nothing is launched
-        dA = new((rt, k), dtype=torch.bfloat16, device=dev)
-        dB = new((d, r), dtype=torch.bfloat16, device=dev)
-    dX = torch.empty((M, k), dtype=torch.bfloat16, device=dev) if need_dx else None
+        new = dY.new_empty if M else dY.new_zeros  # without a token the sums are empty and nothing is launched
+        dA, dB = new((rt, k)), new((d, r))
+    dX = dY.new_empty((M, k)) if need_dx else None
     if M == 0:
         return dX, dA, dB
     nws = _lib.qlora_backward_workspace_bytes(M, d, k, rt)

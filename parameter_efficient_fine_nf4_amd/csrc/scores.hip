@@ -607,14 +607,27 @@ static void scores_kernel(const ScoreArgs& a, hipStream_t st) {
     QLORA_LAUNCH("scores", st, (k_scores<E, T, N>), row_grid(b), dim3(T), 0, st, b);
 }
 
+// Threads a row and what each holds, by the row's number of 16-byte pieces.  One
+// wave takes a short row without a barrier.  Up to one row per CU a row's own
+// latency counts: the most threads, with as many loads in flight as 64 registers
+// leave (with more a work-group of 1024 runs at half the speed).  With more rows,
+// 256 or 512 threads: several rows a CU, one of which computes while others load.
+// Measured with 20 alternatives (us):
+//   200 rows, bf16, V = 32000:   1024 x 4 in registers 9.5, 256 in pieces 11.4;
+//   200 rows, bf16, V = 131072:  1024 x 8 in pieces 17.2, x 4 17.4, 512 x 4 18.9,
+//                                1024 x 16 in registers 32; one row 13.3, 14.3,
+//                                15.3, 27.8;
+//   400 rows, bf16, V = 32000:   1024 x 4 in registers 13.3, 256 in pieces 13.2;
+//   2048 rows, bf16, V = 32000:  43.7 and 33.3;
+//   4096 rows, bf16, V = 64000:  512 in pieces 115, 256 114 (without alternatives
+//                                93 and 99); V = 131072: 198 and 210.
 template <typename E>
 static hipError_t launch_scores_of(const ScoreArgs& a, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
   if (pieces <= 64 * 4)
     scores_kernel<E, 64, 4>(a, st);
-  else if (a.T <= 256 && pieces > 1024 && pieces <= 1024 * 16)
-    pieces <= 1024 * 4 ? scores_kernel<E, 1024, 4>(a, st)
-                       : (pieces <= 1024 * 8 ? scores_kernel<E, 1024, 8>(a, st) : scores_kernel<E, 1024, 16>(a, st));
+  else if (a.T <= 256 && pieces > 1024)
+    pieces <= 1024 * 4 ? scores_kernel<E, 1024, 4>(a, st) : scores_kernel<E, 1024, -8>(a, st);
   else if (pieces <= 4096)
     scores_kernel<E, 256, -4>(a, st);
   else

@@ -455,8 +455,7 @@ static int forward_impl(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int
   const Nf4Table& tab = nf4_table();
   const int ldt = tsave_ld((int)M);
   hipError_t e = hipSuccess;
-  if (ck != nullptr) e = launch_ck_save(X, (int)M, (int)k, ck->codes, ck->absmax, st);
-  if (e != hipSuccess) return hip_status(e);
+  const CkJob job = ck != nullptr ? CkJob{X, (int)M, (int)k, ldt, ck->codes, ck->absmax} : CkJob{};
   const uint16_t* Xa = X;  // the adapter path's input
   if (drop) {
     uint16_t* xd = Xd_save != nullptr ? Xd_save : w.Xd;
@@ -466,9 +465,10 @@ static int forward_impl(const uint16_t* X, int64_t M, const qlora_nf4_t* W0, int
   if (e != hipSuccess) return hip_status(e);
   if (forward_uses_decode((int)M, (int)d, (int)k)) {
     e = launch_forward_decode(X, (int)M, wd, nsec, A, B, r, s, Y, r > 0 ? T_save : nullptr, ldt, w.dec, tab, st,
-                              nullptr, Xa);
+                              nullptr, Xa, job);
   } else {
-    if (r > 0)
+    if (ck != nullptr) e = launch_ck_save(job, st);
+    if (r > 0 && e == hipSuccess)
       e = launch_lora_proj(Xa, (int)M, (int)k, A, false, rt, 1, w.T, T_save, ldt, w.proj, nullptr, 0, 0.0f, nullptr,
                            st);
     if (e == hipSuccess) e = launch_forward(X, (int)M, wd, nsec, w.T, B, r, s, Y, tab, st, w.dec);
@@ -751,8 +751,8 @@ int qlora_checkpoint_save(const uint16_t* X, int64_t M, int64_t k, int8_t* codes
   const Region out[2] = {{codes, ck_codes_bytes(M, k)}, {absmax, ck_absmax_bytes(M, k)}};
   const Region in[1] = {{X, (size_t)(M * k) * 2}};
   if (any_alias(out, in)) return QLORA_ERR_ALIAS;
-  return hip_status(launch_ck_save(X, (int)M, (int)k, reinterpret_cast<uint8_t*>(codes), absmax,
-                                   reinterpret_cast<hipStream_t>(stream)));
+  const CkJob job{X, (int)M, (int)k, tsave_ld((int)M), reinterpret_cast<uint8_t*>(codes), absmax};
+  return hip_status(launch_ck_save(job, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int qlora_checkpoint_load(const int8_t* codes, const uint16_t* absmax, int64_t M, int64_t k, uint16_t* X,

@@ -34,6 +34,7 @@
 //   fixed order, adds s T B^T and rounds to bf16.
 #include <string.h>
 
+#include "checkpoint.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -1549,12 +1550,10 @@ __global__ __launch_bounds__(64 * kD1Waves) void k_fwd_dec1s(
 // added after, eight at a time, in split order).
 constexpr int kFinBatch = 8;
 
-__global__ __launch_bounds__(256) void k_fwd_decode_finish(const float* __restrict__ part, int nsplit,
-                                                          int M, int d, int ldp,
-                                                          const uint16_t* __restrict__ B, int r, int rt,
-                                                          int dsec, const int* __restrict__ idx, float s,
-                                                          uint16_t* __restrict__ Y,
-                                                          uint16_t* __restrict__ Tsave, int ldt) {
+__device__ __forceinline__ void decode_finish(const float* __restrict__ part, int nsplit, int M, int d, int ldp,
+                                              const uint16_t* __restrict__ B, int r, int rt, int dsec,
+                                              const int* __restrict__ idx, float s, uint16_t* __restrict__ Y,
+                                              uint16_t* __restrict__ Tsave, int ldt) {
   __shared__ float tsh[kMaxSections * kMaxRank];  // all sections' ranks (one per thread)
   static_assert(kMaxSections * kMaxRank <= 256, "one rank of T per thread");
   const int m = blockIdx.y;
@@ -1621,6 +1620,32 @@ __global__ __launch_bounds__(256) void k_fwd_decode_finish(const float* __restri
     y = fmaf(s, l, y);
   }
   Y[(size_t)m * d + n] = (uint16_t)pack_bf16x2(y, 0.0f);
+}
+
+__global__ __launch_bounds__(256) void k_fwd_decode_finish(const float* __restrict__ part, int nsplit,
+                                                          int M, int d, int ldp,
+                                                          const uint16_t* __restrict__ B, int r, int rt,
+                                                          int dsec, const int* __restrict__ idx, float s,
+                                                          uint16_t* __restrict__ Y,
+                                                          uint16_t* __restrict__ Tsave, int ldt) {
+  decode_finish(part, nsplit, M, d, ldp, B, r, rt, dsec, idx, s, Y, Tsave, ldt);
+}
+
+// The same with the input's checkpoint: work-groups past the outputs' take a tile
+// each.
+__global__ __launch_bounds__(256) void k_fwd_decode_finish_ck(const float* __restrict__ part, int nsplit, int M, int d,
+                                                              int ldp, const uint16_t* __restrict__ B, int r, int rt,
+                                                              int dsec, float s, uint16_t* __restrict__ Y,
+                                                              uint16_t* __restrict__ Tsave, int ldt, CkJob ck,
+                                                              int ntiles) {
+  const int nout = (d + 255) / 256;
+  if ((int)blockIdx.x < nout) {
+    decode_finish(part, nsplit, M, d, ldp, B, r, rt, dsec, nullptr, s, Y, Tsave, ldt);
+    return;
+  }
+  __shared__ __attribute__((aligned(16))) CkConstants as;
+  const int tile = ((int)blockIdx.x - nout) * (int)gridDim.y + (int)blockIdx.y;
+  if (tile < ntiles) ck_save_tile(ck, tile, as);
 }
 
 // ---------------------------------------------------------------- launch --
@@ -1736,10 +1761,14 @@ size_t forward_gemm_ws_bytes(int M, int d, int k, int r, bool split_only) {
 hipError_t launch_forward_decode(const uint16_t* X, int M, const Nf4Dev& w, int nsec, const uint16_t* A,
                                  const uint16_t* B, int r, float s, uint16_t* Y, uint16_t* Tsave,
                                  int ldt, float* part, const Nf4Table& t, hipStream_t st, const int* idx,
-                                 const uint16_t* Xa) {
+                                 const uint16_t* Xa, const CkJob& ck) {
   const bool xad = Xa != nullptr && Xa != X;  // the adapter path reads its own input
   if (Xa == nullptr) Xa = X;
   if (decode_single(M, w.k, r, idx != nullptr || xad)) {
+    if (ck.X != nullptr) {
+      const hipError_t e = launch_ck_save(ck, st);
+      if (e != hipSuccess) return e;
+    }
     // 16, 32 or 48 rows per work-group: the fewest that keep the grid
     // within one work-group per CU (a work-group holds 128 KB of LDS)
     const int nb = d1_row_blocks(w.d, w.dsec, w.d != w.dsec);
@@ -1823,8 +1852,16 @@ hipError_t launch_forward_decode(const uint16_t* X, int M, const Nf4Dev& w, int 
 #undef QLORA_DEC_M
 #undef QLORA_DEC
   }
-  QLORA_LAUNCH("fwd_decode_finish", st, k_fwd_decode_finish, dim3((unsigned)((w.d + 255) / 256), (unsigned)M), dim3(256),
-                     0, st, part, ns, M, w.d, ldp, B, r, rt, w.dsec, idx, s, Y, Tsave, ldt);
+  const unsigned nout = (unsigned)((w.d + 255) / 256);
+  if (ck.X != nullptr) {
+    const int tiles = ck_tiles(ck.M, ck.k);
+    QLORA_LAUNCH("fwd_decode_finish", st, k_fwd_decode_finish_ck,
+                 dim3(nout + (unsigned)((tiles + M - 1) / M), (unsigned)M), dim3(256), 0, st, part, ns, M, w.d, ldp, B, r,
+                 rt, w.dsec, s, Y, Tsave, ldt, ck, tiles);
+  } else {
+    QLORA_LAUNCH("fwd_decode_finish", st, k_fwd_decode_finish, dim3(nout, (unsigned)M), dim3(256), 0, st, part, ns, M,
+                 w.d, ldp, B, r, rt, w.dsec, idx, s, Y, Tsave, ldt);
+  }
   return hipGetLastError();
 }
 

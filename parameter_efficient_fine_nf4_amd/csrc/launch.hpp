@@ -114,6 +114,17 @@ hipError_t launch_token_reduce2_ck(const uint16_t* Zt0, const uint8_t* codes, co
                                    uint16_t* out0, const uint16_t* Zt1, const uint16_t* V1, int N1, uint16_t* out1,
                                    int ldz, int M, int r, int nsec1, float s, hipStream_t st);
 
+// checkpoint.hip: M x k bf16 activations at 8 bits: int8 codes (M x k) and one
+// bf16 constant per token and 64 columns, k/64 rows of tsave_ld(M).
+struct CkJob {
+  const uint16_t* X;  // nullptr: nothing to save
+  int M, k, ldm;
+  uint8_t* codes;
+  uint16_t* absmax;
+};
+hipError_t launch_ck_save(const CkJob& job, hipStream_t st);
+hipError_t launch_ck_load(const uint8_t* codes, const uint16_t* absmax, int M, int k, uint16_t* X, hipStream_t st);
+
 // gemm_fwd.hip
 bool forward_uses_decode(int M, int d, int k);
 // Sections (w.dsec < w.d): nsec = d / dsec row sections; T holds r ranks
@@ -129,10 +140,13 @@ hipError_t launch_forward(const uint16_t* X, int M, const Nf4Dev& w, int nsec, c
 // the weight has one section.
 // Xa (optional): the adapter path's input (the dropped input under LoRA
 // dropout) in place of X for T.
+// ck: a checkpoint to write beside (in the last of the call's kernels where
+// that one has work-groups of its size).
 hipError_t launch_forward_decode(const uint16_t* X, int M, const Nf4Dev& w, int nsec, const uint16_t* A,
                                  const uint16_t* B, int r, float s, uint16_t* Y, uint16_t* Tsave,
                                  int ldt, float* part, const Nf4Table& t, hipStream_t st,
-                                 const int* idx = nullptr, const uint16_t* Xa = nullptr);
+                                 const int* idx = nullptr, const uint16_t* Xa = nullptr,
+                                 const CkJob& ck = CkJob{});
 // split_only: per-token adapters or LoRA dropout (those always take the
 // split-K decode kernels).
 size_t forward_gemm_ws_bytes(int M, int d, int k, int r, bool split_only = false);
@@ -174,11 +188,6 @@ hipError_t launch_preference(const float* logp, const float* ref_logp, const int
                              const int32_t* cu, int64_t P, int kind, int average, float beta, float smoothing,
                              float margin, const float* weight, float* loss, float* reward, float* dlogp,
                              hipStream_t st);
-
-// checkpoint.hip: M x k bf16 activations at 8 bits: int8 codes (M x k) and one
-// bf16 constant per token and 64 columns, k/64 rows of tsave_ld(M).
-hipError_t launch_ck_save(const uint16_t* X, int M, int k, uint8_t* codes, uint16_t* absmax, hipStream_t st);
-hipError_t launch_ck_load(const uint8_t* codes, const uint16_t* absmax, int M, int k, uint16_t* X, hipStream_t st);
 
 // scores.hip: log-probabilities of the m tokens of each row, its entropy and
 // its n best words (tokens T x m, ids and top T x n; stats T x 3, optional).

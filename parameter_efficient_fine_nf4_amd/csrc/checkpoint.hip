@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kCkThreads) void k_ck_save(CkJob job) {
 __global__ __launch_bounds__(kCkThreads) void k_ck_load(const uint8_t* __restrict__ codes,
                                                         const uint16_t* __restrict__ absmax, int M, int k, int ldm,
                                                         uint16_t* __restrict__ X) {
-  const int nct = (k + kCkCols - 1) / kCkCols;
+  const int nct = ((k - 1) / kCkCols + 1);
   const int col = (int)blockIdx.x % nct * kCkCols + ((int)threadIdx.x & 31) * 16;
   const int m = (int)blockIdx.x / nct * kCkTokens + ((int)threadIdx.x >> 5);
   if (m >= M || col >= k) return;

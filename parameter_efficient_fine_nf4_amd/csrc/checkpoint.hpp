@@ -65,7 +65,7 @@ __device__ __forceinline__ u32x4 encode16(const u32x4& lo, const u32x4& hi, uint
 typedef uint16_t CkConstants[kCkCols / kBlock][kCkTokens];
 __device__ __forceinline__ void ck_save_tile(const CkJob& job, int tile, CkConstants& as) {
   const int M = job.M, k = job.k;
-  const int nct = (k + kCkCols - 1) / kCkCols, ct = tile % nct;
+  const int nct = ((k - 1) / kCkCols + 1), ct = tile % nct;
   const int col = ct * kCkCols + ((int)threadIdx.x & 31) * 16, row = (int)threadIdx.x >> 5;
   const int m0 = tile / nct * kCkTokens, m = m0 + row;
   u32x4 lo = {0u, 0u, 0u, 0u}, hi = lo;
@@ -89,6 +89,6 @@ __device__ __forceinline__ void ck_save_tile(const CkJob& job, int tile, CkConst
     *reinterpret_cast<u32x4*>(job.absmax + (size_t)kb * job.ldm + m0) = *reinterpret_cast<const u32x4*>(&as[b][0]);
 }
 
-inline int ck_tiles(int M, int k) { return (k + kCkCols - 1) / kCkCols * ((M + kCkTokens - 1) / kCkTokens); }
+inline int ck_tiles(int M, int k) { return ((k - 1) / kCkCols + 1) * ((M + kCkTokens - 1) / kCkTokens); }
 
 }  // namespace qlora

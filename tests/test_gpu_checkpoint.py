@@ -286,3 +286,19 @@ def test_more_than_2_31_bytes(lib):
     back = lib.checkpoint_load(ck)
     assert torch.equal(back[-100:], lib.checkpoint_load(small))
     assert torch.equal(back[16384 * 2000:16384 * 2001], lib.checkpoint_load(first))
+
+
+def test_the_longest_row(lib):
+    # a single token of as many columns as there may be: its constants take twice the codes' bytes
+    _case("longest row")
+    k = (1 << 31) - 64
+    X = torch.ones(1, k, dtype=BF, device=DEV)
+    last = torch.randn(1, 4096, device=DEV).to(BF)
+    X[:, -4096:] = last
+    ck = lib.checkpoint_save(X)
+    small = lib.checkpoint_save(last)
+    assert torch.equal(ck.codes[:, -4096:], small.codes) and torch.equal(ck.absmax[-64:, 0], small.absmax[:, 0])
+    assert bool((ck.codes[:, :1 << 20] == 127).all()) and bool((ck.codes[:, (k - 8192) // 64 * 64:-4096] == 127).all())
+    X.zero_()
+    lib.checkpoint_load(ck, out=X)
+    assert torch.equal(X[:, -4096:], lib.checkpoint_load(small)) and bool((X[:, :1 << 20] == 1).all())

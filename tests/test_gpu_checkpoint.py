@@ -288,6 +288,22 @@ def test_more_than_2_31_bytes(lib):
     assert torch.equal(back[16384 * 2000:16384 * 2001], lib.checkpoint_load(first))
 
 
+def test_many_tokens(lib):
+    # 2^30 codes of narrow rows: the reduction's offsets and its last, ragged tokens
+    _case("many tokens")
+    M, d, k, r = (1 << 24) - 37, 16, 64, 4
+    g = torch.Generator().manual_seed(4)
+    w = lib.quantize((torch.randn(d, k, generator=g) * 0.02).to(DEV))
+    A, B = torch.randn(r, k, generator=g).to(BF).to(DEV), torch.randn(d, r, generator=g).to(BF).to(DEV)
+    X = torch.randn(M, k, device=DEV).to(BF)
+    dY = torch.randn(M, d, device=DEV).to(BF)
+    Y, T, ck = lib.forward_checkpoint(X, w, A, B, 4.0)
+    lib.checkpoint_load(ck, out=X)
+    want = lib.backward(dY, X, w, A, B, 4.0, T_saved=T, need_dx=False)
+    got = lib.backward_checkpoint(dY, ck, w, A, B, 4.0, T, need_dx=False)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]) and torch.isfinite(got[1].float()).all()
+
+
 def test_the_longest_row(lib):
     # a single token of as many columns as there may be: its constants take twice the codes' bytes
     _case("longest row")

@@ -1047,17 +1047,40 @@ __device__ __forceinline__ void tokred_strip_ck(const RedJobCk& J, int block, in
   tokred_finish<NJ, CB>(acc, lds, n0, N, r, s, 0, J.out);
 }
 
+// Both reductions of all of a call's sections.  A group (blockIdx.y) is `per`
+// whole sections, at most kMaxRank ranks: ranks p0 r .. of both jobs, rows of dA,
+// and of dB the sections' columns of dY.  (As launches of their own, with few
+// strips each: 5569 tokens, 3 sections of 256 x 64 at r = 48: 78 us; in one 27.)
+struct RedCk {
+  const uint16_t* Ut;      // nsec r x ldz
+  const uint8_t* codes;    // M x k
+  const uint16_t* absmax;
+  int k;
+  uint16_t* dA;            // nsec r x k
+  const uint16_t* Tt;      // nsec r x ldz
+  const uint16_t* dY;      // M x d
+  int d;
+  uint16_t* dB;            // d x r
+  int r, nsec, per;
+};
+
 template <int NJ, int R, int CB>
-__global__ __launch_bounds__(64 * kRedWaves) void k_tokred_ck(RedJobCk j0, RedJob j1, int ldz, int M, int rz0, int rz1,
-                                                              float s) {
+__global__ __launch_bounds__(64 * kRedWaves) void k_tokred_ck(RedCk a, int ldz, int M, float s) {
+  constexpr int SW = 16 * CB;
   constexpr int kLds = tokred_lds<NJ, R, CB>(1024 * CB + 1024 * NJ);  // of the bf16 strips, which take more
   static_assert(kLds <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(16))) char lds[kLds];
-  const int ns0 = j0.N / (16 * CB);
-  if ((int)blockIdx.x >= ns0)
-    tokred_strip<NJ, R, CB>(j1, (int)blockIdx.x - ns0, ldz, M, rz1, s, lds);
-  else
-    tokred_strip_ck<NJ, R, CB>(j0, (int)blockIdx.x, ldz, M, rz0, s, lds);
+  const int p0 = blockIdx.y * a.per, np = min(a.per, a.nsec - p0);
+  const int j = p0 * a.r, rg = np * a.r, dsec = a.d / a.nsec;
+  const int ns0 = a.k / SW, strip = (int)blockIdx.x - ns0;
+  if (strip >= 0) {
+    const RedJob job{a.Tt + (size_t)j * ldz, a.dY + (size_t)p0 * dsec, np * dsec, a.d, a.dB + (size_t)p0 * dsec * a.r, 1,
+                     a.r, a.r, dsec};
+    if (strip < (job.N + SW - 1) / SW) tokred_strip<NJ, R, CB>(job, strip, ldz, M, rg, s, lds);
+  } else {
+    const RedJobCk job{a.Ut + (size_t)j * ldz, a.codes, a.absmax, a.k, a.dA + (size_t)j * a.k, rg};
+    tokred_strip_ck<NJ, R, CB>(job, (int)blockIdx.x, ldz, M, rg, s, lds);
+  }
 }
 
 static hipError_t token_reduce_launch(const RedJob& j0, const RedJob& j1, bool has1, int ldz, int M, int r,
@@ -1121,34 +1144,6 @@ hipError_t launch_token_reduce2(const uint16_t* Zt0, const uint16_t* V0, int N0,
   return e;
 }
 
-static hipError_t token_reduce_ck_launch(const RedJobCk& j0, const RedJob& j1, int ldz, int M, int r, float s,
-                                         hipStream_t st) {
-  const int rp = padded_rank(r);
-  const bool cb4 = j0.N / 64 + (j1.N + 63) / 64 >= 256;
-  const int sw = cb4 ? 64 : 32;
-  dim3 grid((unsigned)(j0.N / sw + (j1.N + sw - 1) / sw));
-#define QLORA_RED(NJ, R, CB)                                                                                     \
-  QLORA_LAUNCH("token_reduce_ck", st, (k_tokred_ck<NJ, R, CB>), grid, dim3(64 * kRedWaves), 0, st, j0, j1, ldz, M, \
-               r, r, s)
-  if (cb4) {
-    switch (rp / 16) {
-      case 1: QLORA_RED(1, 3, 4); break;
-      case 2: QLORA_RED(2, 3, 4); break;
-      case 3: QLORA_RED(3, 2, 4); break;
-      default: QLORA_RED(4, 2, 4); break;
-    }
-  } else {
-    switch (rp / 16) {
-      case 1: QLORA_RED(1, 3, 2); break;
-      case 2: QLORA_RED(2, 3, 2); break;
-      case 3: QLORA_RED(3, 3, 2); break;
-      default: QLORA_RED(4, 3, 2); break;
-    }
-  }
-#undef QLORA_RED
-  return hipGetLastError();
-}
-
 hipError_t launch_token_reduce2_ck(const uint16_t* Zt0, const uint8_t* codes, const uint16_t* absmax, int N0,
                                    uint16_t* out0, const uint16_t* Zt1, const uint16_t* V1, int N1, uint16_t* out1,
                                    int ldz, int M, int r, int nsec1, float s, hipStream_t st) {
@@ -1156,18 +1151,27 @@ hipError_t launch_token_reduce2_ck(const uint16_t* Zt0, const uint8_t* codes, co
     return hipErrorInvalidValue;
   const int r1 = r / nsec1, dsec1 = N1 / nsec1;
   if (nsec1 > 1 && dsec1 % 64 != 0) return hipErrorInvalidValue;  // strips stay inside one section
-  if (r1 > kMaxRank || r > kMaxSections * kMaxRank) return hipErrorInvalidValue;
-  const int per = padded_rank(r) <= kMaxRank ? nsec1 : kMaxRank / r1;  // sections of a launch, as above
-  hipError_t e = hipSuccess;
-  for (int p0 = 0; p0 < nsec1 && e == hipSuccess; p0 += per) {
-    const int np = min(per, nsec1 - p0);
-    const int j = p0 * r1, rg = np * r1;
-    const RedJobCk j0{Zt0 + (size_t)j * ldz, codes, absmax, N0, out0 + (size_t)j * N0, rg};
-    const RedJob j1{Zt1 + (size_t)j * ldz, V1 + (size_t)p0 * dsec1, np * dsec1, N1,
-                    out1 + (size_t)p0 * dsec1 * r1, 1, r1, r1, dsec1};
-    e = token_reduce_ck_launch(j0, j1, ldz, M, rg, s, st);
+  if (r1 < 1 || r1 > kMaxRank) return hipErrorInvalidValue;
+  const int per = padded_rank(r) <= kMaxRank ? nsec1 : kMaxRank / r1, groups = (nsec1 + per - 1) / per;
+  const RedCk a{Zt0, codes, absmax, N0, out0, Zt1, V1, N1, out1, r1, nsec1, per};
+  const int rp = padded_rank(per * r1), n1 = per * dsec1;
+  const bool cb4 = (N0 / 64 + (n1 + 63) / 64) * groups >= 256;  // as in token_reduce_launch
+  const int sw = cb4 ? 64 : 32;
+  const dim3 grid((unsigned)(N0 / sw + (n1 + sw - 1) / sw), (unsigned)groups);
+#define QLORA_RED(NJ, R, CB) \
+  QLORA_LAUNCH("token_reduce_ck", st, (k_tokred_ck<NJ, R, CB>), grid, dim3(64 * kRedWaves), 0, st, a, ldz, M, s)
+  switch (rp / 16 + (cb4 ? 4 : 0)) {
+    case 1: QLORA_RED(1, 3, 2); break;
+    case 2: QLORA_RED(2, 3, 2); break;
+    case 3: QLORA_RED(3, 3, 2); break;
+    case 4: QLORA_RED(4, 3, 2); break;
+    case 5: QLORA_RED(1, 3, 4); break;
+    case 6: QLORA_RED(2, 3, 4); break;
+    case 7: QLORA_RED(3, 2, 4); break;
+    default: QLORA_RED(4, 2, 4); break;
   }
-  return e;
+#undef QLORA_RED
+  return hipGetLastError();
 }
 
 }  // namespace qlora

@@ -445,13 +445,19 @@ def _activation(name: str, t: torch.Tensor) -> torch.device:
     return _on_gpu(t)
 
 
+def _new_checkpoint(X: torch.Tensor, M: int, k: int) -> Checkpoint:
+    if k < 64 or k % 64:
+        raise ValueError("a checkpoint's columns are a multiple of 64")
+    return Checkpoint(M, k, torch.empty_like(X, dtype=torch.int8), X.new_empty(k // 64, (M + 63) // 64 * 64))
+
+
 def checkpoint_save(X: torch.Tensor, out: Checkpoint | None = None) -> Checkpoint:
     """X (M x k bf16, k a multiple of 64) at 8 bits: int8 codes and a bf16
     constant for every 64 columns of a token."""
     dev = _activation("X", X)
     M, k = X.shape
     if out is None:
-        out = Checkpoint.empty(M, k, dev)
+        out = _new_checkpoint(X, M, k)
     else:
         out.check(M, k, dev)
     _run("qlora_checkpoint_save", dev, X.data_ptr(), M, k, out.codes.data_ptr(), out.absmax.data_ptr())
@@ -463,7 +469,7 @@ def checkpoint_load(ck: Checkpoint, out: torch.Tensor | None = None) -> torch.Te
     dev = _on_gpu(ck.codes)
     ck.check(ck.M, ck.k, dev)
     if out is None:
-        out = torch.empty((ck.M, ck.k), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(ck.codes, dtype=torch.bfloat16)
     else:
         _dense("out", out, torch.bfloat16, (ck.M, ck.k), dev)
     _run("qlora_checkpoint_load", dev, ck.codes.data_ptr(), ck.absmax.data_ptr(), ck.M, ck.k, out.data_ptr())
@@ -497,12 +503,12 @@ def forward_checkpoint(X: torch.Tensor, w: NF4Weight, A=None, B=None, alpha: flo
     r = _adapter(w, A, B, dev)
     rt = r * w.nsec
     if out is None:
-        out = X.new_empty((M, w.d))
+        out = X.new_empty(M, w.d)
     else:
         _dense("out", out, torch.bfloat16, (M, w.d), dev)
-    T = X.new_empty((rt, (M + 63) // 64 * 64)) if r > 0 else None
+    T = X.new_empty(rt, (M + 63) // 64 * 64) if r > 0 else None
     if ck is None:
-        ck = Checkpoint.empty(M, k, dev)
+        ck = _new_checkpoint(X, M, k)
     else:
         ck.check(M, k, dev)
     if M == 0:  # empty tensors have no address
@@ -540,8 +546,8 @@ def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, 
             _dense("keep", keep, torch.uint8, (M, k), dev)
             mask = keep.data_ptr()
         new = dY.new_empty if M else dY.new_zeros  # without a token the sums are empty and nothing is launched
-        dA, dB = new((rt, k)), new((d, r))
-    dX = dY.new_empty((M, k)) if need_dx else None
+        dA, dB = new(rt, k), new(d, r)
+    dX = dY.new_empty(M, k) if need_dx else None
     if M == 0:
         return dX, dA, dB
     nws = _lib.qlora_backward_workspace_bytes(M, d, k, rt)
@@ -647,7 +653,7 @@ def _grad_rows(logits: torch.Tensor, out, T: int, V: int, ld: int):
         # a padded head's gradient keeps the padding (as zeros), with rows
         # that start where the logits' rows do
         ldd = ld if ld - V < 256 else V
-        rows = torch.empty((T, ldd), dtype=logits.dtype, device=logits.device)
+        rows = logits.new_empty(T, ldd)
         return (rows if ldd == V else rows.narrow(1, 0, V)), ldd
     if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
         raise ValueError("out has the shape, type and device of the logits")
@@ -780,13 +786,13 @@ def token_scores(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: 
     if not 0 <= top <= 64 or top > V or m > 64:
         raise ValueError("up to 64 tokens a row and 64 alternatives, no more than there are words")
     entropy = torch.empty(T, dtype=torch.float32, device=_on_gpu(logits))
-    logp = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    logp = None if tokens is None else torch.empty_like(tokens, dtype=torch.float32)
     ids = best = stats = None
     if top:
-        ids = torch.empty((T, top), dtype=torch.int32, device=dev)
-        best = torch.empty((T, top), dtype=torch.float32, device=dev)
+        best = entropy.new_empty(T, top)
+        ids = torch.empty_like(best, dtype=torch.int32)
     if save_stats:
-        stats = torch.empty((T, 3), dtype=torch.float32, device=dev)
+        stats = entropy.new_empty(T, 3)
     _run("qlora_token_scores", dev, logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, y, m, int(top),
          float(inv_temperature), _ptr(logp), entropy.data_ptr(), _ptr(ids), _ptr(best), _ptr(stats))
     return (logp, entropy, ids, best, stats) if save_stats else (logp, entropy, ids, best)

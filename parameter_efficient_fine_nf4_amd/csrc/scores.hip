@@ -68,16 +68,53 @@ template <bool FAR>
 __device__ __forceinline__ float exponent1(const Scale& c, float k, float ref, float z) {
   return FAR ? (z - ref) * c.one : fmaf(z, c.one, -k);
 }
+// A thread's N pieces, unpacked in each pass over them, or (up to 32 words) once:
+// for bf16 the second unpacking is a tenth of a row's instructions (4096 x 32000: 52.4
+// us with it, 50.8 without).
+template <typename E, int N, bool KEEP>
+struct Pieces {
+  static constexpr int kPer = Elem<E>::kPer16;
+  u32x4 w[KEEP ? 1 : N];
+  float v[KEEP ? N : 1][kPer];
+  __device__ __forceinline__ explicit Pieces(const u32x4 (&from)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (KEEP)
+        Elem<E>::unpack(from[j], v[j]);
+      else
+        w[j] = from[j];
+    }
+  }
+  template <int PASS>
+  __device__ __forceinline__ void get(int j, float (&f)[kPer]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) f[q] = v[j][q];
+    } else {
+      Elem<E>::unpack(anew<PASS>(w[j]), f);
+    }
+  }
+  __device__ __forceinline__ float max(int j) const {
+    float f[kPer];
+    get<0>(j, f);
+    float mx = f[0];
+#pragma unroll
+    for (int q = 1; q < kPer; ++q) mx = fmaxf(mx, f[q]);
+    return mx;
+  }
+};
+
 // PART: of the first `have` pieces (the others hold no words).
-template <typename E, int N, bool FAR, bool CLAMP, bool PART>
-__device__ __forceinline__ Sums pieces_sums_of(const u32x4 (&w)[N], int have, const Scale& c, float k, float ref) {
+template <typename E, int N, bool FAR, bool CLAMP, bool PART, bool KEEP>
+__device__ __forceinline__ Sums pieces_sums_of(const Pieces<E, N, KEEP>& w, int have, const Scale& c, float k,
+                                               float ref) {
   constexpr int kPer = Elem<E>::kPer16;
   float s[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (PART && j >= have) break;
     float f[kPer];
-    Elem<E>::unpack(anew<1 + PART + 2 * CLAMP>(w[j]), f);
+    w.template get<1 + PART + 2 * CLAMP>(j, f);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const float x = exponent1<FAR>(c, k, ref, f[q]), e = exp2_hw(x);
@@ -87,8 +124,8 @@ __device__ __forceinline__ Sums pieces_sums_of(const u32x4 (&w)[N], int have, co
   }
   return Sums{s[0] + s[1], u[0] + u[1]};
 }
-template <typename E, int N>
-__device__ __forceinline__ Sums pieces_sums(const u32x4 (&w)[N], int have, const Scale& c, float k, float ref,
+template <typename E, int N, bool KEEP>
+__device__ __forceinline__ Sums pieces_sums(const Pieces<E, N, KEEP>& w, int have, const Scale& c, float k, float ref,
                                             bool far) {
   if (far) return pieces_sums_of<E, N, true, true, true>(w, have, c, k, ref);
   Sums o = have == N ? pieces_sums_of<E, N, false, false, false>(w, have, c, k, ref)
@@ -125,18 +162,14 @@ struct OnlineSums {
   }
   // returns the pieces' own maximum
   template <typename E, int N>
-  __device__ __forceinline__ float add(const u32x4 (&w)[N], int have, const Scale& c) {
-    constexpr int kPer = Elem<E>::kPer16;
-    float f[kPer], mx = kNegInf, k, ref;
+  __device__ __forceinline__ float add(const u32x4 (&from)[N], int have, const Scale& c) {
+    const Pieces<E, N, (N * Elem<E>::kPer16 <= 32)> w(from);
+    float mx = kNegInf, k, ref;
     bool far;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      Elem<E>::unpack(anew<0>(w[j]), f);
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) mx = fmaxf(mx, f[q]);
-    }
+    for (int j = 0; j < N; ++j) mx = fmaxf(mx, w.max(j));
     raise(fmaxf(m, mx), c, k, ref, far);
-    const Sums o = pieces_sums<E>(w, have, c, k, ref, far);
+    const Sums o = pieces_sums(w, have, c, k, ref, far);
     sum.s += o.s;
     sum.u += o.u;
     return mx;
@@ -392,7 +425,7 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
   const RowExp x(m, a.c);
   Sums sum;
   if constexpr (N > 0) {
-    sum = pieces_sums<E>(r.w, pieces_there(at, threadIdx.x, T, N), a.c, x.k, m, x.far);
+    sum = pieces_sums(Pieces<E, N, false>(r.w), pieces_there(at, threadIdx.x, T, N), a.c, x.k, m, x.far);
     const Sums l = one_sum(r.last, a.c, x.k, m, x.far);
     sum.s += l.s;
     sum.u += l.u;
@@ -609,18 +642,17 @@ static void scores_kernel(const ScoreArgs& a, hipStream_t st) {
 
 // Threads a row and what each holds, by the row's number of 16-byte pieces.  One
 // wave takes a short row without a barrier.  Up to one row per CU a row's own
-// latency counts: the most threads, with as many loads in flight as 64 registers
-// leave (with more a work-group of 1024 runs at half the speed).  With more rows,
-// 256 or 512 threads: several rows a CU, one of which computes while others load.
-// Measured with 20 alternatives (us):
-//   200 rows, bf16, V = 32000:   1024 x 4 in registers 9.5, 256 in pieces 11.4;
-//   200 rows, bf16, V = 131072:  1024 x 8 in pieces 17.2, x 4 17.4, 512 x 4 18.9,
-//                                1024 x 16 in registers 32; one row 13.3, 14.3,
-//                                15.3, 27.8;
-//   400 rows, bf16, V = 32000:   1024 x 4 in registers 13.3, 256 in pieces 13.2;
+// latency counts: the most threads, with eight pieces each in flight.  With more
+// rows, 256 or 512 threads and four pieces: several rows a CU, one of which
+// computes while others load.  Measured with 20 alternatives (us):
+//   1 row, bf16, V = 131072:     1024 x 8 in pieces 13.3, x 4 14.3, x 12 27, 512 x 4
+//                                15.3, 1024 x 16 in registers 27.8;
+//   200 rows, bf16, V = 32000:   1024 x 4 in registers 9.5, 256 x 4 in pieces 11.4;
+//   200 rows, bf16, V = 131072:  1024 x 8 in pieces 17.2, 512 x 4 18.9;
+//   400 rows, bf16, V = 32000:   1024 x 4 in registers 13.3, 256 x 4 in pieces 13.2;
 //   2048 rows, bf16, V = 32000:  43.7 and 33.3;
-//   4096 rows, bf16, V = 64000:  512 in pieces 115, 256 114 (without alternatives
-//                                93 and 99); V = 131072: 198 and 210.
+//   4096 rows, bf16, V = 64000:  512 x 4 in pieces 97, without alternatives 92, 256 x 4
+//                                100; V = 131072: 188 and 182, 256 x 4 192.
 template <typename E>
 static hipError_t launch_scores_of(const ScoreArgs& a, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;

@@ -233,7 +233,7 @@ struct Best {
   uint16_t part[kList];  // parts with words from the bound on: step * threads + thread
   int parts, count;
   int need;  // of the counting by digits
-  uint64_t prefix;
+  uint32_t prefix;
   int bins[256];
 };
 
@@ -261,61 +261,111 @@ __device__ __forceinline__ void best_piece(Best& b, const u32x4& w, int i0, floa
     }
 }
 
-// Every finite word of the row, by whole work-groups' steps: fn(value, index).
+// Every finite word of the row, a piece a thread at a time: fn(value, index).
 template <typename E, int T, typename F>
-__device__ __forceinline__ void each_word(const E* z, int V, F fn) {
-  for (int i = threadIdx.x; i < V; i += T) {
-    const float f = Elem<E>::get(z + i);
-    if (f >= kLowest) fn(f, i);
+__device__ __forceinline__ void each_word(const E* z, int V, const RowSpan& at, F fn) {
+  constexpr int kPer = Elem<E>::kPer16;
+  for (int i = threadIdx.x; i < at.nv; i += T) {
+    float f[kPer];
+    Elem<E>::unpack(*reinterpret_cast<const u32x4*>(z + at.head + (size_t)i * kPer), f);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (f[q] >= kLowest) fn(f[q], at.head + i * kPer + q);
+  }
+  if (at.rest < V) {
+    const float f = Elem<E>::get(z + at.rest);
+    if (f >= kLowest) fn(f, at.rest);
   }
 }
 
-// The list of a row with too many words from the bound on: the order's digits
-// from the highest down, each counted over the row, until the words from the
-// prefix on fit the list.  Ends after eight digits at the latest: places are
-// distinct, so that n of them are left.
+// The list of a row with too many words from the bound on (equal logits, or a
+// strong few in one group).  The digits of the n-th largest logit's place among
+// the floats, from the highest down, each counted over the row, until the words
+// from there on fit the list.  Where they do not even when the logit is known,
+// there are more words of that one value: those above it are taken, and of its
+// own the first ones by index, in steps of the row that end with enough.  (20
+// alternatives where 3 words of 32000 are left above a mask of bf16's lowest value:
+// 4 rows 34 us, ordinary ones 11; 4096 rows 363 and 51.)
 template <typename E, int T>
-__device__ void best_by_digits(const E* z, int V, int n, Best& b) {
+__device__ void best_by_digits(const E* z, int V, const RowSpan& at, int n, Best& b) {
+  constexpr int kLast = sizeof(E) == 2 ? 16 : 0;  // digits below it follow from those above
   if (threadIdx.x == 0) {
     b.prefix = 0u;
     b.need = n;
   }
-  int shift = 64;
+  int shift = 32;
   do {
     shift -= 8;
     for (int i = threadIdx.x; i < 256; i += T) b.bins[i] = 0;
     __syncthreads();
-    const uint64_t prefix = b.prefix;
+    const uint32_t prefix = b.prefix;
     const int need = b.need;
-    each_word<E, T>(z, V, [&](float f, int i) {
-      const uint64_t p = place_of(f, i);
-      if (shift < 56 && (p ^ prefix) >> (shift + 8) != 0u) return;
+    int digit = 0, run = 0;  // equal digits of a thread are counted at once: rows that come here hold many
+    each_word<E, T>(z, V, at, [&](float f, int) {
+      const uint32_t p = order_of(f);
+      if (shift < 24 && (p ^ prefix) >> (shift + 8) != 0u) return;
       const int d = (int)(p >> shift) & 255;
-      // equal digits of a wave are counted at once: rows that come here hold many
-      const int lead = __builtin_amdgcn_readfirstlane(d);
-      const uint64_t same = __ballot(d == lead);
-      if (d != lead)
-        atomicAdd(&b.bins[d], 1);
-      else if ((int)(threadIdx.x & 63) == (int)__ffsll((long long)same) - 1)
-        atomicAdd(&b.bins[d], (int)__popcll(same));
+      if (d != digit) {
+        if (run != 0) atomicAdd(&b.bins[digit], run);
+        digit = d;
+        run = 0;
+      }
+      ++run;
     });
+    if (run != 0) atomicAdd(&b.bins[digit], run);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int above = 0, d = 255;
-      while (d > 0 && above + b.bins[d] < need) above += b.bins[d--];
-      b.prefix = prefix | (uint64_t)d << shift;
-      b.need = need - above;
-      b.count = n - need + above + b.bins[d];  // words from the new prefix on
+    if (threadIdx.x < 64) {  // four digits a lane, the highest first: the one that holds the need-th word
+      const int top = 255 - 4 * (int)threadIdx.x;
+      int c[4], sum = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        c[q] = b.bins[top - q];
+        sum += c[q];
+      }
+      int upto = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, o, 64);
+        if ((int)threadIdx.x >= o) upto += v;
+      }
+      int above = upto - sum;
+      if (above < need && upto >= need) {
+        int d = top, words = c[0];
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (d == top - q + 1 && above + words < need) {
+            above += words;
+            words = c[q];
+            --d;
+          }
+        b.prefix = prefix | (uint32_t)d << shift;
+        b.need = need - above;
+        b.count = n - need + above + words;  // words from the new prefix on
+      }
     }
     __syncthreads();
-  } while (b.count > kList && shift > 0);
-  const uint64_t from = b.prefix;
+  } while (b.count > kList && shift > kLast);
+  const uint32_t from = b.prefix >> shift;
+  const int need = b.need;
+  const bool ties = b.count > kList;
   __syncthreads();
   if (threadIdx.x == 0) b.count = 0;
   __syncthreads();
-  each_word<E, T>(z, V, [&](float f, int i) {
-    if (place_of(f, i) >= from) best_add(b, f, i);
+  each_word<E, T>(z, V, at, [&](float f, int i) {
+    const uint32_t p = order_of(f) >> shift;
+    if (ties ? p > from : p >= from) best_add(b, f, i);
   });
+  constexpr int S = T < 256 ? T : 256;
+  for (int i0 = 0, found = 0; ties && found < need && i0 < V; i0 += S) {
+    const int i = i0 + (int)threadIdx.x;
+    bool hit = false;
+    if ((int)threadIdx.x < S && i < V) {
+      const float f = Elem<E>::get(z + i);
+      hit = f >= kLowest && order_of(f) >> shift == from;
+      if (hit) best_add(b, f, i);
+    }
+    found += __syncthreads_count(hit);
+  }
   __syncthreads();
 }
 
@@ -505,7 +555,7 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
                       at.head + piece * Elem<E>::kPer16, bound);
     }
     __syncthreads();
-    if (best.parts > kList || best.count > kList) best_by_digits<E, T>(z, a.V, a.n, best);
+    if (best.parts > kList || best.count > kList) best_by_digits<E, T>(z, a.V, at, a.n, best);
   }
   // a word's rank is the number of those before it; four threads count it
   const int count = real ? best.count : 0;

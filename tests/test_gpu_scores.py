@@ -368,3 +368,35 @@ def test_past_2_31_elements(lib):
     assert torch.equal(d[-8:], d[:8]) and torch.equal(d[T // 2 // 8 * 8:][:8], d[:8])
     _check_grad(lib, small, y8, g[:8], gh[:8], out[4][:8].contiguous(), 1.0, BF)
     assert torch.equal(d[:8], lib.token_scores_backward(g[:8], gh[:8], small, y8, out[4][:8].contiguous()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [2048, 4096, 10000, 40000, 140000])
+def test_many_words_of_the_last_value(lib, V, dtype):
+    # the n-th best is one of very many equal words: at the row's end, behind better ones, in one lane's pieces alone, one
+    # step of the type away from as many others, at both signs; and strong words that all lie in one group
+    _case("last value", V, dtype)
+    g = torch.Generator().manual_seed(V)
+    z = (torch.randn(8, V, generator=g) - 8).to(dtype).float()
+    z[0, 3 * V // 4:] = 1.0
+    z[1, 3 * V // 4:] = 1.0
+    z[1, [5, V // 2, V - 1]] = 2.0
+    z[2] = -1.0
+    z[2, V // 2:] = -1.0 - torch.finfo(dtype).eps  # the next value down
+    z[2, ::97] = -0.5
+    z[3, torch.arange(V) // 8 % 64 == 7] = 3.0
+    z[4] = torch.where(torch.arange(V) % 2 == 0, 2.0, 2.0 + 2 * torch.finfo(dtype).eps)
+    lane = torch.nonzero(torch.arange(V) // 8 % 64 == 9)[:, 0]
+    z[5, lane] = torch.linspace(1, 2, len(lane))
+    z[6] = -torch.finfo(dtype).max
+    z[6, V - 30:] = torch.linspace(0, 1, 30)
+    z[7, :V // 2] = 0.0
+    z[7, 1:V // 2:2] = -0.0
+    z = z.to(dtype).to(DEV)
+    for n in (1, 7, 64):
+        _check(lib, z, None, n, 1.0)
+    # as one of many rows, where other threads have them
+    many = z.repeat(40, 1).contiguous()
+    a, b = lib.token_scores(many, top=64), lib.token_scores(z, top=64)
+    for i in (0, 39):
+        assert torch.equal(a[2][8 * i:8 * i + 8], b[2]) and torch.allclose(a[3][8 * i:8 * i + 8], b[3], rtol=0, atol=1e-4)

@@ -710,6 +710,14 @@ __device__ __forceinline__ void tr_reads4(const char* slot, const uint32_t (&off
 #endif
 }
 
+// Strip of a work-group: the eight XCDs, which take work-groups in turn, get a run
+// of neighbouring strips each (whose rows share 128-byte lines), whatever their
+// number.
+__device__ __forceinline__ int strip_of(int block, int nstrips) {
+  const int x = block & 7, per = nstrips >> 3, more = nstrips & 7;
+  return x * per + min(x, more) + (block >> 3);
+}
+
 // One reduction of a launch: out = s Z^T V with V (M x N), r output ranks.
 // Sections: the columns of V fall into sections of dsec columns, and
 // section p reads ranks p*zsec .. p*zsec + r - 1 of Z (zsec = 0, dsec = N:
@@ -793,8 +801,7 @@ __device__ __forceinline__ void tokred_strip(const RedJob& J, int block, int ldz
   const int N = J.N, out_transposed = J.out_transposed, r = J.r;
   uint16_t* __restrict__ out = J.out;
   const int nstrips = (N + SW - 1) / SW;
-  int tm, strip;
-  tile_of(block, 1, nstrips, tm, strip);
+  const int strip = strip_of(block, nstrips);
   const int n0 = strip * SW;
   const int per = ((M + W - 1) / W + kRedStep - 1) / kRedStep * kRedStep;
   const int tb = wave_s * per;
@@ -947,8 +954,7 @@ __device__ __forceinline__ void tokred_strip_ck(const RedJobCk& J, int block, in
   const int g = lane >> 4, sl = lane & 15;
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   const int N = J.N, r = J.r, nstrips = N / (16 * CB);
-  int tm, strip;
-  tile_of(block, 1, nstrips, tm, strip);
+  const int strip = strip_of(block, nstrips);
   const int n0 = strip * 16 * CB;
   const int per = ((M + W - 1) / W + kRedStep - 1) / kRedStep * kRedStep;
   const int tb = wave_s * per;

@@ -37,6 +37,7 @@ struct ScoreArgs {
   int V;
   const int32_t* tokens;  // T x m
   int m, n;
+  int span;  // gradient: columns of a work-group
   float tau;
   Scale c;
   float* logp;     // T x m
@@ -591,7 +592,7 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
 // counted tokens, and B = -tau gH ln 2 / s; a token's own element gets tau
 // sum g_j over its entries on top.
 struct GradOf {
-  float A, B, mean;
+  float A, B, mean, tau;
 };
 template <typename E, bool FAR, bool ENT>
 __device__ __forceinline__ float grad_value(float z, const RowExp& x, const GradOf& g) {
@@ -601,74 +602,142 @@ __device__ __forceinline__ float grad_value(float z, const RowExp& x, const Grad
                        : (sizeof(E) == 2 ? fmaf(z, x.c.one, -x.k) : fmaf(z, x.c.lo, fmaf(z, x.c.hi, -x.k)));
   return exp2_hw(xv) * fmaf(fmaxf(xv, kFloor) - g.mean, g.B, g.A);
 }
-template <typename E, bool FAR, bool ENT>
-__device__ __forceinline__ u32x4 score_grad_piece(const u32x4& w, const RowExp& x, const GradOf& g) {
+// The tokens of a work-group's columns, found by the piece that each lies in: lists
+// of entries by the piece's number, so that a thread puts a token's element in
+// place in the piece that it stores.  (Stored over the pieces afterwards, the
+// elements of 33 tokens a row cost 4096 x 32000 bf16 99 us in place of 79 for one.)
+constexpr uint32_t kNoEntry = ~0u;
+template <int S>
+struct Hits {
+  __attribute__((aligned(16))) uint32_t head[S];
+  struct __attribute__((aligned(16))) Entry {
+    int col;  // of the work-group's columns, -1: none
+    float g;
+    uint32_t next;
+  } of[kMaxScores];
+};
+// A column's piece; a single element's number is that past the pieces of its thread.
+template <typename E>
+__device__ __forceinline__ int piece_of(const RowSpan& at, int col) {
   constexpr int kPer = Elem<E>::kPer16;
-  float f[kPer];
-  Elem<E>::unpack(w, f);
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) f[q] = grad_value<E, FAR, ENT>(f[q], x, g);
-  return Elem<E>::pack(f);
+  if (col < at.head) return at.nv + col;
+  const int i = (col - at.head) / kPer;
+  return i < at.nv ? i : col - at.nv * (kPer - 1);
+}
+// By all threads; a lane of the first wave has an entry, those of one column become
+// one, which takes the sum of their g in their order.
+template <typename E, int T, int S>
+__device__ __forceinline__ void hits_fill(Hits<S>& hits, const RowSpan& at, int col, float g) {
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x; i < S / 4; i += T)
+    reinterpret_cast<u32x4*>(hits.head)[i] = u32x4{kNoEntry, kNoEntry, kNoEntry, kNoEntry};
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    uint32_t next = kNoEntry;
+    if (col >= 0) next = atomicExch(&hits.head[piece_of<E>(at, col) & (S - 1)], (uint32_t)lane);
+    uint64_t todo = __ballot(next != kNoEntry);  // of columns that may be there twice
+    while (todo != 0u) {
+      const int c = __builtin_amdgcn_readlane(col, __ffsll((long long)todo) - 1);
+      const uint64_t same = __ballot(col == c);
+      float sum = 0.0f;
+      for (uint64_t left = same; left != 0u; left &= left - 1u)
+        sum += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), __ffsll((long long)left) - 1));
+      if (col == c) {
+        g = sum;
+        if (lane != __ffsll((long long)same) - 1) col = -1;
+      }
+      todo &= ~same;
+    }
+    hits.of[lane] = {col, g, next};
+  }
+  __syncthreads();
 }
 
-// One row from memory to memory; where out is z, a thread overwrites only what
-// it has read.
-template <typename E, int T, int kBatch, bool FAR, bool ENT, bool STREAM>
-__device__ __forceinline__ void score_row(const E* z, E* out, int V, const RowSpan& at, const RowExp& x,
-                                          const GradOf& g) {
+// d of N elements z of the columns from col on; h: the list of their piece.
+template <typename E, bool FAR, bool ENT, int N, int S>
+__device__ __forceinline__ void grad_values(const float (&z)[N], float (&d)[N], int col, uint32_t h, const Hits<S>& hits,
+                                            const RowExp& x, const GradOf& g) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) d[q] = grad_value<E, FAR, ENT>(z[q], x, g);
+  while (h != kNoEntry) {
+    const auto e = hits.of[h];
+    const int at = e.col - col;
+    if ((uint32_t)at < (uint32_t)N) {
+      float own = z[0];
+#pragma unroll
+      for (int q = 1; q < N; ++q) own = q == at ? z[q] : own;
+      const float v = fmaf(e.g, g.tau, grad_value<float, FAR, ENT>(own, x, g));
+#pragma unroll
+      for (int q = 0; q < N; ++q) d[q] = q == at ? v : d[q];
+    }
+    h = e.next;
+  }
+}
+
+// One row from memory to memory, w being a thread's first pieces; where out is z, a
+// thread overwrites only what it has read.
+template <typename E, int T, int kBatch, bool FAR, bool ENT, bool STREAM, int S>
+__device__ __forceinline__ void score_row(const E* z, E* out, int V, const RowSpan& at, const Hits<S>& hits,
+                                          const RowExp& x, const GradOf& g, u32x4 (&w)[kBatch]) {
   constexpr int kPer = Elem<E>::kPer16;
   for (int i = threadIdx.x; i < at.nv; i += kBatch * T) {
-    u32x4 w[kBatch];
-    load_pieces<E>(z, at, i, T, w);
+    uint32_t h[kBatch];
+    if (i >= T) load_pieces<E>(z, at, i, T, w);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) h[j] = hits.head[(i + j * T) & (S - 1)];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (i + j * T < at.nv)
-        put16<STREAM>(out + at.head + (size_t)(i + j * T) * kPer, score_grad_piece<E, FAR, ENT>(w[j], x, g));
+      if (i + j * T < at.nv) {
+        const int col = at.head + (i + j * T) * kPer;
+        float f[kPer], d[kPer];
+        Elem<E>::unpack(w[j], f);
+        grad_values<E, FAR, ENT>(f, d, col, h[j], hits, x, g);
+        put16<STREAM>(out + col, Elem<E>::pack(d));
+      }
   }
-  if (at.rest < V) Elem<E>::put(out + at.rest, grad_value<E, FAR, ENT>(Elem<E>::get(z + at.rest), x, g));
+  if (at.rest < V) {
+    const float f[1] = {Elem<E>::get(z + at.rest)};
+    float d[1];
+    grad_values<E, FAR, ENT>(f, d, at.rest, hits.head[piece_of<E>(at, at.rest) & (S - 1)], hits, x, g);
+    Elem<E>::put(out + at.rest, d[0]);
+  }
 }
 
-// The rows go from the last to the first, which the forward ended with.  Bound by
+// The rows go from the last to the first, which the forward ended with; a
+// work-group has a span of columns, and the tokens that lie there.  Bound by
 // memory: 4096 rows of 32000 bf16, three tenths uncounted, 33 tokens and an entropy
 // term: 76 us, 446 MB at 5.9 TB/s.
 template <typename E, int T>
 __global__ __launch_bounds__(T) void k_scores_grad(ScoreArgs a) {
   constexpr int B = T == 1024 ? 8 : 4;
+  constexpr int S = T == 64 ? 256 : 1024;
+  __shared__ Hits<S> hits;
   const int lane = threadIdx.x & 63;
   const int64_t t = a.first + gridDim.x - 1 - blockIdx.x;
+  const int c0 = (int)blockIdx.y * a.span;
+  const bool last = blockIdx.y == gridDim.y - 1;
+  const int V = last ? a.V - c0 : a.span, end = last ? (int)a.ldd - c0 : a.span;
   const int token = lane < a.m ? a.tokens[t * a.m + lane] : -1;
   const bool counted = is_counted(token, a.V);
   const float g = counted ? a.dlogp[t * a.m + lane] : 0.0f;
   const bool live = a.m == 0 || __ballot(counted) != 0u;
   const float gh = live && a.dentropy != nullptr ? a.dentropy[t] : 0.0f;
-  E* out = reinterpret_cast<E*>(a.dlogits) + t * a.ldd;
+  E* out = reinterpret_cast<E*>(a.dlogits) + t * a.ldd + c0;
   if (gh == 0.0f && __ballot(g != 0.0f) == 0u) {
-    row_zero<E, T>(out, (int)a.ldd, a.stream);
+    row_zero<E, T>(out, end, a.stream);
     return;
   }
-  const E* z = reinterpret_cast<const E*>(a.logits) + t * a.ld;
-  const float zy = counted ? Elem<E>::get(z + token) : 0.0f;
-  // entries of the same token: the first one takes the sum of all of them
-  float sum = 0.0f;
-  bool first = counted && threadIdx.x < 64;
-  if (threadIdx.x < 64)
-    for (int i = 0; i < a.m; ++i) {
-      const int ti = __builtin_amdgcn_readlane(token, i);
-      const float gi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
-      if (ti == token) {
-        sum += gi;
-        if (i < lane) first = false;
-      }
-    }
+  const E* z = reinterpret_cast<const E*>(a.logits) + t * a.ld + c0;
+  const RowSpan at(z, V);
+  u32x4 w[B];
+  load_pieces<E>(z, at, threadIdx.x, T, w);  // in flight meanwhile
   const float G = wave_sum(g);
   const RowExp x(a.stats[3 * t], a.c);
   const float s = a.stats[3 * t + 1];
-  const GradOf go{-G * a.tau / s, -gh * a.tau * (float)kLn2 / s, a.stats[3 * t + 2]};
-  const RowSpan at(z, a.V);
-  // the tokens' logits are in hand before any of the row is written over
-  __syncthreads();
+  const GradOf go{-G * a.tau / s, -gh * a.tau * (float)kLn2 / s, a.stats[3 * t + 2], a.tau};
+  hits_fill<E, T>(hits, at, counted && is_counted(token - c0, V) ? token - c0 : -1, g);
   auto row = [&](auto far, auto ent, auto stream) {
-    score_row<E, T, B, decltype(far)::value, decltype(ent)::value, decltype(stream)::value>(z, out, a.V, at, x, go);
+    score_row<E, T, B, decltype(far)::value, decltype(ent)::value, decltype(stream)::value>(z, out, V, at, hits, x, go, w);
   };
   const std::true_type yes{};
   const std::false_type no{};
@@ -676,15 +745,7 @@ __global__ __launch_bounds__(T) void k_scores_grad(ScoreArgs a) {
     x.far ? (a.stream ? row(yes, yes, yes) : row(yes, yes, no)) : (a.stream ? row(no, yes, yes) : row(no, yes, no));
   else
     x.far ? (a.stream ? row(yes, no, yes) : row(yes, no, no)) : (a.stream ? row(no, no, yes) : row(no, no, no));
-  for (int i = a.V + (int)threadIdx.x; i < a.ldd; i += T) Elem<E>::put(out + i, 0.0f);
-  // the pieces have left before the tokens' elements are stored over them
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (first) {
-    const float v = x.far ? (gh != 0.0f ? grad_value<E, true, true>(zy, x, go) : grad_value<E, true, false>(zy, x, go))
-                          : (gh != 0.0f ? grad_value<float, false, true>(zy, x, go) : grad_value<float, false, false>(zy, x, go));
-    Elem<E>::put(out + token, fmaf(sum, a.tau, v));
-  }
+  for (int i = V + (int)threadIdx.x; i < end; i += T) Elem<E>::put(out + i, 0.0f);
 }
 
 // ---------------------------------------------------------- launchers ----
@@ -725,31 +786,42 @@ static hipError_t launch_scores_of(const ScoreArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// span: columns of a work-group.
 template <typename E, int T>
-static void scores_grad_kernel(const ScoreArgs& a, hipStream_t st) {
+static void scores_grad_kernel(const ScoreArgs& a, int span, hipStream_t st) {
   ScoreArgs b = a;  // the last rows first, which the forward ended with
-  for (b.first = (a.T - 1) / kRowsALaunch * kRowsALaunch; b.first >= 0; b.first -= kRowsALaunch)
-    QLORA_LAUNCH("scores_grad", st, (k_scores_grad<E, T>), row_grid(b), dim3(T), 0, st, b);
+  while ((a.V - 1) / span > 65534) span *= 2;  // a grid's second dimension
+  b.span = span;
+  const unsigned spans = (unsigned)((a.V - 1) / span + 1);
+  for (b.first = (a.T - 1) / kRowsALaunch * kRowsALaunch; b.first >= 0; b.first -= kRowsALaunch) {
+    const dim3 rows = row_grid(b);
+    QLORA_LAUNCH("scores_grad", st, (k_scores_grad<E, T>), dim3(rows.x, spans), dim3(T), 0, st, b);
+  }
 }
 
+// A gradient past the cache's half is stored in whole rows, where there are two a
+// CU: 2048 x 131072 bf16 197 us, in spans 204.  Any other in spans of four pieces a
+// thread: 4 x 131072 bf16 3.9 us, in whole rows 11.8; 96 x 32000 fp32 5.9 and 7.2; 300 x
+// 50021 fp32 20.3 and 22.5; 2048 x 32000 bf16 41.0 and 41.5 (two pieces a thread 3.5, 5.8,
+// 21.8, 40.8; eight 4.6, 5.8, 20.8, 41.4).
 template <typename E>
 static hipError_t launch_scores_grad_of(const ScoreArgs& a, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.V + Elem<E>::kPer16 - 1) / Elem<E>::kPer16;
   if (pieces <= 64 * 4)
-    scores_grad_kernel<E, 64>(a, st);
-  else if (pieces <= 256 * 4)
-    scores_grad_kernel<E, 256>(a, st);
-  else if (pieces <= 4096 && a.T >= 512)
-    scores_grad_kernel<E, 512>(a, st);
+    scores_grad_kernel<E, 64>(a, a.V, st);
+  else if (!a.stream || a.T < 512)
+    scores_grad_kernel<E, 256>(a, 256 * 4 * Elem<E>::kPer16, st);
+  else if (pieces <= 4096)
+    scores_grad_kernel<E, 512>(a, a.V, st);
   else
-    scores_grad_kernel<E, 1024>(a, st);
+    scores_grad_kernel<E, 1024>(a, a.V, st);
   return hipGetLastError();
 }
 
 hipError_t launch_scores(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* tokens, int m, int n,
                          float tau, float* logp, float* entropy, int32_t* ids, float* top, float* stats,
                          hipStream_t st) {
-  const ScoreArgs a{logits, 0, T, ld, 0, V, tokens, m, n, tau, exp2_scale(tau), logp, entropy, ids, top, stats,
+  const ScoreArgs a{logits, 0, T, ld, 0, V, tokens, m, n, V, tau, exp2_scale(tau), logp, entropy, ids, top, stats,
                     nullptr, nullptr, nullptr, false};
   return f32 ? launch_scores_of<float>(a, st) : launch_scores_of<uint16_t>(a, st);
 }
@@ -757,7 +829,7 @@ hipError_t launch_scores(const void* logits, int f32, int64_t T, int V, int64_t 
 hipError_t launch_scores_grad(const void* logits, int f32, int64_t T, int V, int64_t ld, const int32_t* tokens, int m,
                               float tau, const float* stats, const float* dlogp, const float* dentropy, void* dlogits,
                               int64_t ldd, hipStream_t st) {
-  const ScoreArgs a{logits, 0, T, ld, ldd, V, tokens, m, 0, tau, exp2_scale(tau), nullptr, nullptr, nullptr, nullptr,
+  const ScoreArgs a{logits, 0, T, ld, ldd, V, tokens, m, 0, V, tau, exp2_scale(tau), nullptr, nullptr, nullptr, nullptr,
                     const_cast<float*>(stats), dlogp, dentropy, dlogits, past_cache(T, ldd, f32)};
   return f32 ? launch_scores_grad_of<float>(a, st) : launch_scores_grad_of<uint16_t>(a, st);
 }

@@ -214,6 +214,56 @@ def test_in_place(lib, V, dtype):
     assert lib.token_scores_backward(g, gh, a, y, stats, out=a) is a and torch.equal(a, want)
 
 
+def _crowded(T, V, dtype):
+    """Rows of 64 tokens: one word throughout, neighbours (of them the row's first and last words), words a list's
+    number of pieces apart, both ends and every border between the columns of two work-groups."""
+    per = 16 // torch.finfo(dtype).bits * 8
+    j = torch.arange(64)
+    rows = [torch.full((64,), V // 2), j % V, V - 1 - (j % V), (j // 2 * 1024 * per + 3) % V,
+            torch.where(j % 2 == 0, j // 2 * 1024 * per, j // 2 * 1024 * per - 1) % V,
+            torch.where(j % 3 == 0, V - 1, j % 3 - 1)]
+    return torch.stack([rows[i % len(rows)] for i in range(T)]).to(torch.int32).to(DEV)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V,offset", [(1, 0), (5, 1), (200, 3), (1023, 0), (9001, 1), (40000, 0), (70001, 5)])
+def test_tokens_close_together(lib, V, offset, dtype):
+    _case("crowded", V, offset, dtype)
+    T = 6
+    z, y = _logits(T, V, dtype, 31, offset=offset), _crowded(T, V, dtype)
+    stats = lib.token_scores(z, y, save_stats=True)[4]
+    g, gh = torch.linspace(-1, 2, T * 64).view(T, 64).to(DEV), torch.linspace(1, -1, T).to(DEV)
+    d = _check_grad(lib, z, y, g, gh, stats, 1.0, dtype)
+    a = z.clone()
+    assert torch.equal(lib.token_scores_backward(g, gh, a, y, stats, out=a), d)
+
+
+@pytest.mark.parametrize("V,T", [(33001, 2100), (70001, 1000)])
+def test_tokens_close_together_streamed(lib, V, T):
+    _case("crowded, streamed", V, T)
+    z8, y8 = _logits(6, V, BF, 32), _crowded(6, V, BF)
+    n = -(-T // 6)
+    z, y = z8.repeat(n, 1)[:T].contiguous(), y8.repeat(n, 1)[:T].contiguous()
+    g, gh = torch.ones(T, 64, device=DEV), torch.full((T,), -0.5, device=DEV)
+    stats = lib.token_scores(z, y, save_stats=True)[4]
+    d = lib.token_scores_backward(g, gh, z, y, stats)
+    one = _check_grad(lib, z8, y8, g[:6], gh[:6], stats[:6].contiguous(), 1.0, BF)
+    assert torch.equal(d, one.repeat(n, 1)[:T])
+
+
+def test_the_gradient_of_a_row_of_2_28_words(lib):
+    """Equal logits, whose gradient is known: more columns than the work-groups' usual share of a row reaches."""
+    V = (1 << 28) + 5000
+    _case("one row", V)
+    z, y = torch.zeros(1, V, device=DEV), torch.tensor([[0, V - 1, V - 1]], dtype=torch.int32, device=DEV)
+    _, H, _, _, stats = lib.token_scores(z, y, save_stats=True)
+    assert abs(H.item() - np.log(V)) < 1e-3
+    d = lib.token_scores_backward(torch.tensor([[1.0, 2.0, 4.0]], device=DEV), None, z, y, stats, out=z)[0]
+    assert abs(d[0].item() - 1) < 1e-6 and abs(d[-1].item() - 6) < 1e-6
+    lo, hi = torch.aminmax(d[1:-1])
+    assert abs(lo.item() * V / 7 + 1) < 1e-4 and abs(hi.item() * V / 7 + 1) < 1e-4
+
+
 def test_gradients_past_the_cache_are_streamed(lib):
     _case("streamed")
     T, V, m = 2100, 33001, 2

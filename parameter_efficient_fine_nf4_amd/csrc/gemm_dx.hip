@@ -7,8 +7,8 @@
 // two waves per SIMD, described at the kernel; k_dx covers other shapes.
 //
 // Transposed-dequant GEMM on bf16 MFMA (32x32x16), fp32 accumulation;
-// BM x BN work-group tiles (256 x 256, or 128 x 128 when the grid would not
-// cover the CUs) of 2 x 2 waves, each wave BM/2 x BN/2 outputs.  The
+// BM x BN work-group tiles (256 x 256; 128 x 128, 64 x 128 or 64 x 64 when the grid
+// would not cover the CUs) of 2 x 2 waves, each wave BM/2 x BN/2 outputs.  The
 // contraction runs over d, the weight's row index, while a packed code word
 // holds 8 consecutive columns of one row.  Each K step (64 weight rows x BN
 // columns) is decoded once per work-group: a lane pair (l, l + 32) takes one
@@ -73,7 +73,7 @@ __device__ __forceinline__ int wslot(int r, int c) {
 }
 
 template <int BM, int BN, bool DROP>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_dx(
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 128 ? 1 : 2))) void k_dx(
     const uint16_t* __restrict__ dY, int M, const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ c2, const float* __restrict__ c1, const float* __restrict__ mean,
     int d, int k, int dsec, const uint16_t* __restrict__ U, const uint16_t* __restrict__ At, int rp,
@@ -82,9 +82,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   constexpr int WM = BM / 2, WN = BN / 2;   // 2 x 2 waves
   constexpr int MB = WM / 32, NB = WN / 32;
   constexpr int YCH = BM / 32;              // 1 KB dY fetches per wave per K step
-  constexpr int NP = BN / 128;              // half-block rows decoded per lane per K step
-  constexpr int ROWB = BN * 2;              // bytes per row of a decoded weight tile
-  constexpr int kYBytes = BM * kDxBK * 2, kWBytes = kDxBK * BN * 2;
+  // half-block rows that a lane fetches per K step, and the words (of four) that it
+  // decodes of each: with 64 columns two lanes share a half
+  constexpr int NP = BN >= 128 ? BN / 128 : 1;
+  constexpr int NW = BN >= 128 ? 4 : 2;
+  constexpr int NH = BN >= 128 ? 32 : 16;   // lanes of one half
+  constexpr int ROWB = BN >= 128 ? BN * 2 : 256;  // bytes per row of a decoded weight tile
+  constexpr int kYBytes = BM * kDxBK * 2, kWBytes = kDxBK * ROWB;
   constexpr int kCWave = NP * 1024 + 512;   // per wave: codes, then c2 and c1 words
   constexpr int kCSlot = 4 * kCWave;
   constexpr int kCOff = 2 * kYBytes;
@@ -137,17 +141,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   }
   // Block rows decoded by this wave: G = wave*(BN/4) + j, j < BN/4, is
   // weight row (G % 64) of the step and 64-column block (G / 64) of the
-  // tile.  Pass i of lane l handles j = i*32 + l%32, column half l/32.
+  // tile.  Pass i of lane l handles j = i*32 + l%32, column half l/32 (with
+  // 64 columns j = l%16, column half l/16%2, words 2*(l/32) and the next).
   // The c2/c1 fetch lane l covers j = l % (BN/4).
   int brow[NP], bblk[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const int G = wave * (BN / 4) + i * 32 + l32;
+    const int G = wave * (BN / 4) + i * 32 + lane % NH;
     brow[i] = G % 64;
     bblk[i] = G / 64;
   }
   const int Gc = wave * (BN / 4) + (lane % (BN / 4));
   const int crow = Gc % 64, cblk = Gc / 64;
+  const int chalf = lane / NH & 1;  // column half of a block
   // byte offset of (weight row n, column c) in the codes; block index
   auto code_off = [&](int n, int c) { return (uint32_t)n * (uint32_t)(k >> 1) + (uint32_t)(c >> 1); };
 
@@ -163,7 +169,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       char* cs = smem + kCOff + csl * kCSlot + wave_s * kCWave;
       const int j = i - YCH;
       if (j < NP) {
-        const int n = kc * kDxBK + brow[j], c = c0 + bblk[j] * 64 + half * 32;
+        const int n = kc * kDxBK + brow[j], c = c0 + bblk[j] * 64 + chalf * 32;
         const bool ok = n < d && c < k;
         dma_lds16(rc, code_off(ok ? n : 0, ok ? c : 0), (void*)(cs + j * 1024));
       } else {
@@ -191,8 +197,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       W.v[i] = *reinterpret_cast<const u32x4*>(cs + i * 1024 + lane * 16);
-      W.q2[i] = *reinterpret_cast<const uint32_t*>(cs + NP * 1024 + (i * 32 + l32) * 4);
-      W.q1[i] = *reinterpret_cast<const float*>(cs + NP * 1024 + 256 + (i * 32 + l32) * 4);
+      W.q2[i] = *reinterpret_cast<const uint32_t*>(cs + NP * 1024 + (i * 32 + lane % NH) * 4);
+      W.q1[i] = *reinterpret_cast<const float*>(cs + NP * 1024 + 256 + (i * 32 + lane % NH) * 4);
     }
   };
   Lut lut[NP];
@@ -211,8 +217,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   auto decode_word = [&](const WTile& W, int wd, char* ws) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const u32x4 v = dequant8(W.v[i][wd], lut[i]);
-      const int r = brow[i], c = (bblk[i] * 64 + half * 32 + wd * 8) >> 3;
+      const uint32_t code = NW == 4 ? W.v[i][wd] : (half ? W.v[i][2 + wd] : W.v[i][wd]);
+      const u32x4 v = dequant8(code, lut[i]);
+      const int r = brow[i], c = (bblk[i] * 64 + chalf * 32 + ((NW == 4 ? 0 : half * 2) + wd) * 8) >> 3;
       *reinterpret_cast<u32x4*>(ws + r * ROWB + (wslot(r, c) << 4)) = v;
     }
   };
@@ -283,7 +290,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   read_w(0, W);
   tables(W, 0);
 #pragma unroll
-  for (int wd = 0; wd < 4; ++wd) decode_word(W, wd, wsm);
+  for (int wd = 0; wd < NW; ++wd) decode_word(W, wd, wsm);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCodeLoads) : "memory");
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -305,7 +312,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       if (st < 3) read_ab(ks, st + 1, af[(st + 1) & 1], bf[(st + 1) & 1]);
       __builtin_amdgcn_sched_barrier(0);
       if (st == 0) tables(W, kd);
-      decode_word(W, st, wnext);
+      if (st < NW) decode_word(W, st, wnext);
       if (st < 3) {
 #pragma unroll
         for (int i = st * kPerSub; i < (st + 1) * kPerSub && i < kLoads; ++i) dma_one(i, ky, ysl, kc, csl_far);
@@ -366,11 +373,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   // at a time and stores 16-byte row chunks.
   uint16_t* stage = reinterpret_cast<uint16_t*>(smem) + wave * (WM * 64);
 #pragma unroll
-  for (int pass = 0; pass < NB / 2; ++pass) {
+  for (int pass = 0; pass < (NB + 1) / 2; ++pass) {
+    constexpr int Q = NB < 2 ? 1 : 2;  // 32-column blocks of a pass
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
@@ -381,8 +389,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
           }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < WM / 8; ++i) {
-      const int c = i * 64 + lane, row = c >> 3, ch = c & 7;
+    for (int i = 0; i < WM * Q / 16; ++i) {
+      const int c = i * 64 + lane, row = c / (4 * Q), ch = c % (4 * Q);
       const int m = m0 + wm * WM + row, col = c0 + wn * WN + pass * 64 + ch * 8;
       if (m < M && col < k)
         *reinterpret_cast<u32x4*>(dX + (size_t)m * k + col) = *reinterpret_cast<const u32x4*>(&stage[swz(row, ch)]);
@@ -818,14 +826,27 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
       QLORA_LAUNCH("dx", st, (k_dx8<128, DROP>), dim3((unsigned)(c128 * ((M + 127) / 128))), dim3(64 * kDx8Waves), 0,
                    st, dY, M, w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, dX, t, c256 * 256, c128, keep,
                    dscale, 0, nullptr);
-  } else if (forced == 256 || (forced == 0 && tiles256 >= 256)) {
-    dim3 grid((unsigned)tiles256);
-    QLORA_LAUNCH("dx", st, (k_dx<256, 256, DROP>), grid, dim3(256), 0, st, dY, M, w.codes, w.c2, w.c1, w.mean,
-                 w.d, w.k, w.dsec, U, At, rp, s, dX, t, keep, dscale);
   } else {
-    dim3 grid((unsigned)(((M + 127) / 128) * ((w.k + 127) / 128)));
-    QLORA_LAUNCH("dx", st, (k_dx<128, 128, DROP>), grid, dim3(256), 0, st, dY, M, w.codes, w.c2, w.c1, w.mean,
-                 w.d, w.k, w.dsec, U, At, rp, s, dX, t, keep, dscale);
+    // Other shapes (every tile gives the same bits).  A K step of a work-group takes its time whatever its tile is
+    // (decoding and the steps' chain: 1.0 us at 128 x 128, 0.8 at 64 x 128, 0.65 at 64 x
+    // 64), so where tiles are few, or the last round of them holds few, they are
+    // smaller; work-groups of 64 rows go two to a CU.  500 x 5008 x 448 (M d k): 92 / 77 /
+    // 68 us; 256 x 4112 x 4160: 92 / 79 / 83; 1001 x 1040 x 4160 (264 tiles of 128 x 128) 76 /
+    // 70 / 77; 2000 x 4112 x 1088 (144) 102 / 111 / 130.
+#define QLORA_DX(BM, BN)                                                                                    \
+  QLORA_LAUNCH("dx", st, (k_dx<BM, BN, DROP>),                                                              \
+               dim3((unsigned)(((M + BM - 1) / BM) * ((w.k + BN - 1) / BN))), dim3(256), 0, st, dY, M,      \
+               w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, s, dX, t, keep, dscale)
+    const int last = ((M + 127) / 128) * ((w.k + 127) / 128) % 256;  // 128 x 128 tiles of the last round
+    if (forced == 256 || (forced == 0 && tiles256 >= 256))
+      QLORA_DX(256, 256);
+    else if (forced == 0 && ((M + 63) / 64) * (w.k / 64) <= 128)
+      QLORA_DX(64, 64);
+    else if (forced == 0 && last != 0 && last <= 128)
+      QLORA_DX(64, 128);
+    else
+      QLORA_DX(128, 128);
+#undef QLORA_DX
   }
   return hipGetLastError();
 }

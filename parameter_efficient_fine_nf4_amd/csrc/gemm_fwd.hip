@@ -10,9 +10,9 @@
 //   k_fwd_rich, two waves per SIMD (described at the kernel).
 //
 // k_fwd_rich (M > 64, other shapes): fused NF4-dequant GEMM on bf16 MFMA (32x32x16) with
-//   fp32 accumulation.  Work-group tile BM x 256 (BM = 256, or 128 when the
-//   grid would not cover the CUs), four waves side by side along N (each
-//   wave: all BM rows x 64 output features, BM*64/64 accumulators per lane),
+//   fp32 accumulation.  Work-group tile BM x 128 NB (256 x 256; 128 x 256, 128 x
+//   128 or 64 x 128 when the grid would not cover the CUs), four waves side by
+//   side along N (each wave: all BM rows x 32 NB output features),
 //   K step 64 = one NF4 block per weight row.  Decoding costs about four
 //   VALU operations per weight and each decoded weight feeds BM tokens, so
 //   BM = 256 keeps the decode well under the MFMA time.  X tiles are
@@ -45,8 +45,8 @@ namespace qlora {
 constexpr int kRichBN = 256;
 constexpr int kBK = 64;
 
-template <int BM>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_fwd_rich(const uint16_t* __restrict__ X, int M,
+template <int BM, int NB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 128 ? 1 : 2))) void k_fwd_rich(const uint16_t* __restrict__ X, int M,
                                                  const uint8_t* __restrict__ codes,
                                                  const uint8_t* __restrict__ c2,
                                                  const float* __restrict__ c1,
@@ -55,43 +55,45 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                                                  const uint16_t* __restrict__ B, int r, int rp, int ldr, float s,
                                                  uint16_t* __restrict__ Y, Nf4Table tab) {
   constexpr int MB = BM / 32;        // 32-row MFMA blocks per wave
+  constexpr int BN = 128 * NB;       // output features: 32 NB per wave
   constexpr int XCH = BM / 32;       // 1 KB X loads per wave per K tile
   // One ring slot holds everything a K tile needs: the X tile (BM x 64 bf16,
-  // swizzled), then per wave the packed codes of its 64 weight rows (2 KB)
+  // swizzled), then per wave the packed codes of its 32 NB weight rows (NB KB)
   // and the 32-bit words holding their c2 bytes (256 B) and c1 values
   // (256 B).  Three slots; the epilogue reuses the space for output staging.
   constexpr int kXBytes = BM * kBK * 2;
   constexpr int kCodeOff = kXBytes;
-  constexpr int kC2Off = kCodeOff + 4 * 2048;
+  constexpr int kC2Off = kCodeOff + 4 * NB * 1024;
   constexpr int kC1Off = kC2Off + 4 * 256;
   constexpr int kSlot = kC1Off + 4 * 256;
   constexpr int kRing = 3 * kSlot;
-  constexpr int kStage = 4 * 128 * 64 * 2;
+  constexpr int kStageRows = BM < 128 ? BM : 128;
+  constexpr int kStage = 4 * kStageRows * 64 * 2;
   constexpr int kSmem = kRing > kStage ? kRing : kStage;
   __shared__ __attribute__((aligned(16))) char smem[kSmem];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int half = lane >> 5, l32 = lane & 31;
   int tm, tn;
-  tile_of(blockIdx.x, (M + BM - 1) / BM, (d + kRichBN - 1) / kRichBN, tm, tn);
+  tile_of(blockIdx.x, (M + BM - 1) / BM, (d + BN - 1) / BN, tm, tn);
   const int m0 = tm * BM;
-  const int n0 = tn * kRichBN + wave * 64;
+  const int n0 = tn * BN + wave * (32 * NB);
   const int kblocks = k / kBK;
   // Sections (row blocks of W with their own mean and adapter ranks) never
   // split a tile: the tile's section gives the mean and its columns of T.
-  const int sec = tn * kRichBN / dsec;
+  const int sec = tn * BN / dsec;
   const float mu = mean[sec];
   float qh[8];  // this lane's half of the levels, for build_lut_pair
 #pragma unroll
   for (int i = 0; i < 8; ++i) qh[i] = half ? tab.q[8 + i] : tab.q[i];
 
-  // Weight rows of this lane's two B operands (nb = 0, 1): n0 + nb*32 + l32.
+  // Weight rows of this lane's B operands (nb < NB): n0 + nb*32 + l32.
   // Rows past d read row 0 and are zeroed through their block constant.
-  int nrow[2];
-  bool nval[2];
-  uint32_t cbase[2];  // (clamped row) * kblocks: block index of the row's K tile 0
+  int nrow[NB];
+  bool nval[NB];
+  uint32_t cbase[NB];  // (clamped row) * kblocks: block index of the row's K tile 0
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
+  for (int nb = 0; nb < NB; ++nb) {
     nrow[nb] = n0 + nb * 32 + l32;
     nval[nb] = nrow[nb] < d;
     cbase[nb] = (uint32_t)(nval[nb] ? nrow[nb] : 0) * (uint32_t)kblocks;
@@ -116,10 +118,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int m = min(m0 + r0 + lr, M - 1);
     xoff[j] = (uint32_t)(((size_t)m * k + ((pc ^ swz_f(r0 + lr)) << 3)) * 2);
   }
-  uint32_t coff[2];  // byte offset of this lane's codes of K tile 0, per fetch j
+  uint32_t coff[NB];  // byte offset of this lane's codes of K tile 0, per fetch j
 #pragma unroll
-  for (int j = 0; j < 2; ++j) coff[j] = (uint32_t)(nval[j] ? nrow[j] : 0) * (uint32_t)(k >> 1) + half * 16;
-  const uint32_t dbase = half ? cbase[1] : cbase[0];  // row n0 + lane
+  for (int j = 0; j < NB; ++j) coff[j] = (uint32_t)(nval[j] ? nrow[j] : 0) * (uint32_t)(k >> 1) + half * 16;
+  const uint32_t dbase = half ? cbase[NB - 1] : cbase[0];  // row n0 + lane % (32 NB)
   const uint32_t nblk = (uint32_t)d * (uint32_t)kblocks;
   const BufRsrc rx = make_rsrc(X, (uint64_t)M * k * 2);
   const BufRsrc rc = make_rsrc(codes, (uint64_t)d * k / 2);
@@ -133,12 +135,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     char* slot = smem + sl * kSlot;
     if (i < XCH) {
       dma_lds16(rx, xoff[i] + (uint32_t)kb * (kBK * 2), slot + (wave_s * (BM / 4) + i * 8) * (kBK * 2));
-    } else if (i < XCH + 2) {
+    } else if (i < XCH + NB) {
       const int j = i - XCH;
-      dma_lds16(rc, coff[j] + (uint32_t)kb * 32, slot + kCodeOff + wave_s * 2048 + j * 1024);
+      dma_lds16(rc, coff[j] + (uint32_t)kb * 32, slot + kCodeOff + wave_s * (NB * 1024) + j * 1024);
     } else {
       const uint32_t blk = dbase + (uint32_t)kb;
-      if (i == XCH + 2)
+      if (i == XCH + NB)
         dma_lds4(r2, blk & ~3u, slot + kC2Off + wave_s * 256);
       else
         dma_lds4(r1, (blk >> 8) * 4, slot + kC1Off + wave_s * 256);
@@ -146,43 +148,43 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   };
   auto dma_tile = [&](int kb, int sl) {
 #pragma unroll
-    for (int i = 0; i < XCH + 4; ++i) dma_one(i, kb, sl);
+    for (int i = 0; i < XCH + NB + 2; ++i) dma_one(i, kb, sl);
   };
-  constexpr int kLoads = XCH + 4;  // fetch instructions per wave per K tile
+  constexpr int kLoads = XCH + NB + 2;  // fetch instructions per wave per K tile
   constexpr int kPerSub = (kLoads + 2) / 3;  // issued in each of substeps 0..2
 
   // This lane's codes and block tables of tile kb from ring slot sl.
   struct WTile {
-    u32x4 v[2];
-    uint32_t q2[2];
-    float q1[2];
+    u32x4 v[NB];
+    uint32_t q2[NB];
+    float q1[NB];
   };
   auto read_w = [&](int sl, WTile& W) {
     const char* slot = smem + sl * kSlot;
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      W.v[nb] = *reinterpret_cast<const u32x4*>(slot + kCodeOff + wave_s * 2048 + nb * 1024 + lane * 16);
+    for (int nb = 0; nb < NB; ++nb) {
+      W.v[nb] = *reinterpret_cast<const u32x4*>(slot + kCodeOff + wave_s * (NB * 1024) + nb * 1024 + lane * 16);
       W.q2[nb] = *reinterpret_cast<const uint32_t*>(slot + kC2Off + wave_s * 256 + (nb * 32 + l32) * 4);
       W.q1[nb] = *reinterpret_cast<const float*>(slot + kC1Off + wave_s * 256 + (nb * 32 + l32) * 4);
     }
   };
-  auto tables = [&](const WTile& W, int kb, Lut& a, Lut& b) {
-    float sc[2];
+  auto tables = [&](const WTile& W, int kb, Lut (&t)[NB]) {
+    float sc[NB];
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
+    for (int nb = 0; nb < NB; ++nb) {
       const uint32_t sh = ((cbase[nb] + (uint32_t)kb) & 3u) * 8u;
       const float v = block_scale((W.q2[nb] >> sh) & 0xFFu, W.q1[nb], mu);
       sc[nb] = nval[nb] ? v : 0.0f;
     }
-    a = build_lut_pair(qh, sc[0]);
-    b = build_lut_pair(qh, sc[1]);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) t[nb] = build_lut_pair(qh, sc[nb]);
   };
 
-  f32x16 acc[MB][2];
+  f32x16 acc[MB][NB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0.0f;
 
@@ -219,10 +221,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
   WTile W;
   read_w(0, W);
-  u32x4 wcur0 = W.v[0], wcur1 = W.v[1];
-  Lut t0, t1;
-  tables(W, 0, t0, t1);
-  u32x4 bc0 = dequant8(wcur0[0], t0), bc1 = dequant8(wcur1[0], t1);
+  u32x4 wcur[NB];
+  Lut lut[NB];
+  u32x4 bc[NB];
+  tables(W, 0, lut);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    wcur[nb] = W.v[nb];
+    bc[nb] = dequant8(wcur[nb][0], lut[nb]);
+  }
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   u32x4 afr[2][MB];
@@ -241,7 +248,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       // operand wait then covers only reads issued a substep ago (the
       // compiler waits for all outstanding LDS reads at that point).
       __builtin_amdgcn_sched_barrier(0);
-      acc[0][0] = mfma32(afr[st & 1][0], bc0, acc[0][0]);
+      acc[0][0] = mfma32(afr[st & 1][0], bc[0], acc[0][0]);
       __builtin_amdgcn_sched_barrier(0);
       if (st < 3) {
         read_a(xs, st + 1, afr[(st + 1) & 1]);
@@ -251,31 +258,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       }
       __builtin_amdgcn_sched_barrier(0);
       // decode the next operands (VALU) while this substep's MFMAs run
-      u32x4 bn0, bn1;
-      if (st < 3) {
-        bn0 = dequant8(wcur0[st + 1], t0);
-        bn1 = dequant8(wcur1[st + 1], t1);
-      } else {
-        wcur0 = W.v[0];
-        wcur1 = W.v[1];
-        tables(W, kb + 1, t0, t1);
-        bn0 = dequant8(wcur0[0], t0);
-        bn1 = dequant8(wcur1[0], t1);
+      u32x4 bn[NB];
+      if (st == 3) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) wcur[nb] = W.v[nb];
+        tables(W, kb + 1, lut);
       }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bn[nb] = dequant8(wcur[nb][(st + 1) & 3], lut[nb]);
       if (st < 3) {
 #pragma unroll
         for (int i = st * kPerSub; i < (st + 1) * kPerSub && i < kLoads; ++i) dma_one(i, kf, sl_far);
       }
       // this lane's MFMA k indices: half*32 + st*8 + (0..7) of the block
-      acc[0][1] = mfma32(afr[st & 1][0], bc1, acc[0][1]);
 #pragma unroll
-      for (int mb = 1; mb < MB; ++mb) {
-        acc[mb][0] = mfma32(afr[st & 1][mb], bc0, acc[mb][0]);
-        acc[mb][1] = mfma32(afr[st & 1][mb], bc1, acc[mb][1]);
-      }
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = mb == 0 ? 1 : 0; nb < NB; ++nb) acc[mb][nb] = mfma32(afr[st & 1][mb], bc[nb], acc[mb][nb]);
       constexpr int kDma = kPerSub;
 #pragma unroll
-      for (int i = 0; i < 2 * MB - 1; ++i) {
+      for (int i = 0; i < NB * MB - 1; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
         if (st < 3 && i < kDma) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
@@ -289,8 +291,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
       }
-      bc0 = bn0;
-      bc1 = bn1;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bc[nb] = bn[nb];
     }
     sl_cur = sl_next;
   }
@@ -304,9 +306,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   if (rp > 0) {
     // all operand loads first (B operands are the same for every row block)
     for (int jb = 0; jb < rp; jb += 16) {
-      u32x4 bop[2];
+      u32x4 bop[NB];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
         bop[nb] = u32x4{0u, 0u, 0u, 0u};
         if (nval[nb]) {
 #pragma unroll
@@ -328,14 +330,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) acc[mb][nb] = mfma32(top[mb], bop[nb], acc[mb][nb]);
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma32(top[mb], bop[nb], acc[mb][nb]);
     }
   }
 
-  // Output through LDS, 128 rows at a time: each wave stages its 128 x 64
-  // bf16 sub-tile (16 KB, swizzled like the X tiles) and stores it as
+  // Output through LDS, 128 rows at a time: each wave stages its 128 x 32 NB
+  // bf16 sub-tile (rows of 64, swizzled like the X tiles) and stores it as
   // 16-byte row chunks.
-  uint16_t* stage = reinterpret_cast<uint16_t*>(smem) + wave * (128 * 64);
+  uint16_t* stage = reinterpret_cast<uint16_t*>(smem) + wave * (kStageRows * 64);
 #pragma unroll
   for (int pass = 0; pass < (MB + 3) / 4; ++pass) {
 #pragma unroll
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       const int mb = pass * 4 + q;
       if (mb >= MB) break;
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
@@ -355,8 +357,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     __syncthreads();
     const int rows = (MB - pass * 4) < 4 ? (MB - pass * 4) * 32 : 128;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int c = i * 64 + lane, row = c >> 3, ch = c & 7;
+    for (int i = 0; i < kStageRows * NB / 16; ++i) {
+      const int c = i * 64 + lane, row = c / (4 * NB), ch = c % (4 * NB);
       const int m = m0 + pass * 128 + row, n = n0 + ch * 8;
       if (row < rows && m < M && n < d)
         *reinterpret_cast<u32x4*>(Y + (size_t)m * d + n) = *reinterpret_cast<const u32x4*>(&stage[swz(row, ch)]);
@@ -1909,14 +1911,26 @@ hipError_t launch_forward(const uint16_t* X, int M, const Nf4Dev& w, int nsec, c
       QLORA_LAUNCH("fwd_rich", st, (k_fwd8<128, 2>), grid, dim3(64 * kFwd8Waves), 0, st, X, M, w.codes, w.c2, w.c1,
                    w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t, c256 * kRichBN, c128, 0, nullptr);
     }
-  } else if (rich_bm(M, w.d) == 256) {
-    dim3 grid((unsigned)(ntn * ((M + 255) / 256)));
-    QLORA_LAUNCH("fwd_rich", st, k_fwd_rich<256>, grid, dim3(256), 0, st, X, M, w.codes, w.c2, w.c1,
-                 w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t);
   } else {
-    dim3 grid((unsigned)(ntn * ((M + 127) / 128)));
-    QLORA_LAUNCH("fwd_rich", st, k_fwd_rich<128>, grid, dim3(256), 0, st, X, M, w.codes, w.c2, w.c1,
-                 w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t);
+    // Other shapes (every tile gives the same bits).  A K step of a work-group takes its time whatever its rows are
+    // (decoding: 0.9 us with 64 features a wave, 0.6 with 32), so where tiles are few
+    // they are made smaller, as long as there is one a CU: 1001 x 1040 x 4160 (M d k)
+    // 64 x 128 49 us, 128 x 128 58, 128 x 256 76; 500 x 5008 x 448 128 x 128 14.7, 128 x 256
+    // 19.1; 4000 x 2000 x 2112 128 x 256 56, 64 x 128 76.
+#define QLORA_RICH(BM, NB)                                                                                       \
+  QLORA_LAUNCH("fwd_rich", st, (k_fwd_rich<BM, NB>),                                                             \
+               dim3((unsigned)(((w.d + 128 * NB - 1) / (128 * NB)) * ((M + BM - 1) / BM))), dim3(256), 0, st, X, \
+               M, w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t)
+    const int ntn128 = (w.d + 127) / 128;
+    if (rich_bm(M, w.d) == 256)
+      QLORA_RICH(256, 2);
+    else if (tile_override() == 0 && ntn128 * ((M + 63) / 64) <= 256)
+      QLORA_RICH(64, 1);
+    else if (tile_override() == 0 && ntn128 * ((M + 127) / 128) <= 256)
+      QLORA_RICH(128, 1);
+    else
+      QLORA_RICH(128, 2);
+#undef QLORA_RICH
   }
   return hipGetLastError();
 }

@@ -23,6 +23,8 @@
 // is a buffer-addressed global->LDS load.  The LoRA term s U A is one more
 // MFMA pass in the epilogue, accumulating into the same registers, from U
 // (M x rp) and bf16(s A)^T, zero-padded (k x rp).
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -827,25 +829,28 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
                    st, dY, M, w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, dX, t, c256 * 256, c128, keep,
                    dscale, 0, nullptr);
   } else {
-    // Other shapes (every tile gives the same bits).  A K step of a work-group takes its time whatever its tile is
-    // (decoding and the steps' chain: 1.0 us at 128 x 128, 0.8 at 64 x 128, 0.65 at 64 x
-    // 64), so where tiles are few, or the last round of them holds few, they are
-    // smaller; work-groups of 64 rows go two to a CU.  500 x 5008 x 448 (M d k): 92 / 77 /
-    // 68 us; 256 x 4112 x 4160: 92 / 79 / 83; 1001 x 1040 x 4160 (264 tiles of 128 x 128) 76 /
-    // 70 / 77; 2000 x 4112 x 1088 (144) 102 / 111 / 130.
+    // Other shapes (every tile gives the same bits), as in the forward: a K step costs
+    // a round of work-groups 2.05 us at 256 x 256, 1.05 at 128 x 128, at 64 x 128 0.8 or, two
+    // a CU, 1.1, at 64 x 64 0.65 (up to 128 of them); its start and outputs are 9 us.  M d
+    // k, us in the order of these tiles: 2849 x 7680 x 2880 247 / 374 / 355 / -, 2000 x 4112
+    // x 1088 135 / 76 / 85 / -, 256 x 4112 x 4160 - / 92 / 79 / 83, 500 x 5008 x 448 - / 92 / 77
+    // / 68.
 #define QLORA_DX(BM, BN)                                                                                    \
   QLORA_LAUNCH("dx", st, (k_dx<BM, BN, DROP>),                                                              \
                dim3((unsigned)(((M + BM - 1) / BM) * ((w.k + BN - 1) / BN))), dim3(256), 0, st, dY, M,      \
                w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, s, dX, t, keep, dscale)
-    const int last = ((M + 127) / 128) * ((w.k + 127) / 128) % 256;  // 128 x 128 tiles of the last round
-    if (forced == 256 || (forced == 0 && tiles256 >= 256))
-      QLORA_DX(256, 256);
-    else if (forced == 0 && ((M + 63) / 64) * (w.k / 64) <= 128)
-      QLORA_DX(64, 64);
-    else if (forced == 0 && last != 0 && last <= 128)
-      QLORA_DX(64, 128);
-    else
-      QLORA_DX(128, 128);
+    const int ntn = (w.k + 127) / 128, t64 = (M + 63) / 64;
+    const int64_t ks = (w.d + kDxBK - 1) / kDxBK,
+                  cost[4] = {tile_cost(tiles256, 256, 41 * ks + 180),
+                             tile_cost(ntn * ((M + 127) / 128), 256, 21 * ks + 180),
+                             tile_cost(ntn * t64, 512, 22 * ks + 180, 16 * ks + 180),
+                             t64 * (w.k / 64) <= 128 ? 13 * ks + 180 : INT64_MAX};
+    switch (forced != 0 ? (forced == 256 ? 0 : 1) : (int)(std::min_element(cost, cost + 4) - cost)) {
+      case 0: QLORA_DX(256, 256); break;
+      case 1: QLORA_DX(128, 128); break;
+      case 2: QLORA_DX(64, 128); break;
+      default: QLORA_DX(64, 64); break;
+    }
 #undef QLORA_DX
   }
   return hipGetLastError();

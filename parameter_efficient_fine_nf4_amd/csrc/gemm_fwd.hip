@@ -34,6 +34,8 @@
 //   fixed order, adds s T B^T and rounds to bf16.
 #include <string.h>
 
+#include <algorithm>
+
 #include "checkpoint.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -1912,24 +1914,28 @@ hipError_t launch_forward(const uint16_t* X, int M, const Nf4Dev& w, int nsec, c
                    w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t, c256 * kRichBN, c128, 0, nullptr);
     }
   } else {
-    // Other shapes (every tile gives the same bits).  A K step of a work-group takes its time whatever its rows are
-    // (decoding: 0.9 us with 64 features a wave, 0.6 with 32), so where tiles are few
-    // they are made smaller, as long as there is one a CU: 1001 x 1040 x 4160 (M d k)
-    // 64 x 128 49 us, 128 x 128 58, 128 x 256 76; 500 x 5008 x 448 128 x 128 14.7, 128 x 256
-    // 19.1; 4000 x 2000 x 2112 128 x 256 56, 64 x 128 76.
+    // Other shapes (every tile gives the same bits).  What a K step costs a round of
+    // work-groups, one a CU, hardly depends on how many of its rows are there: 1.6 us
+    // at 256 x 256, 1.15 at 128 x 256, 0.9 at 128 x 128, and at 64 x 128 0.7 or, two a CU,
+    // 1.15; its start and outputs are 8, 5, 4 and 3 us.  The tile with the least of it (M
+    // d k, us in the order of these tiles): 800 x 10960 x 4160 101 / 144 / 158 / 163, 4000 x
+    // 2000 x 2112 56 / 46 / 69 / 76, 500 x 5008 x 448 - / 19.1 / 14.7 / 15.2, 1001 x 1040 x 4160
+    // - / 76 / 58 / 49.
 #define QLORA_RICH(BM, NB)                                                                                       \
   QLORA_LAUNCH("fwd_rich", st, (k_fwd_rich<BM, NB>),                                                             \
                dim3((unsigned)(((w.d + 128 * NB - 1) / (128 * NB)) * ((M + BM - 1) / BM))), dim3(256), 0, st, X, \
                M, w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, T, B, r, rp, ldr, s, Y, t)
     const int ntn128 = (w.d + 127) / 128;
-    if (rich_bm(M, w.d) == 256)
-      QLORA_RICH(256, 2);
-    else if (tile_override() == 0 && ntn128 * ((M + 63) / 64) <= 256)
-      QLORA_RICH(64, 1);
-    else if (tile_override() == 0 && ntn128 * ((M + 127) / 128) <= 256)
-      QLORA_RICH(128, 1);
-    else
-      QLORA_RICH(128, 2);
+    const int64_t ks = w.k / kBK, cost[4] = {tile_cost(ntn * ((M + 255) / 256), 256, 32 * ks + 160),
+                                             tile_cost(ntn * ((M + 127) / 128), 256, 23 * ks + 100),
+                                             tile_cost(ntn128 * ((M + 127) / 128), 256, 18 * ks + 80),
+                                             tile_cost(ntn128 * ((M + 63) / 64), 512, 23 * ks + 60, 14 * ks + 60)};
+    switch (tile_override() != 0 ? (tile_override() == 256 ? 0 : 1) : (int)(std::min_element(cost, cost + 4) - cost)) {
+      case 0: QLORA_RICH(256, 2); break;
+      case 1: QLORA_RICH(128, 2); break;
+      case 2: QLORA_RICH(128, 1); break;
+      default: QLORA_RICH(64, 1); break;
+    }
 #undef QLORA_RICH
   }
   return hipGetLastError();

@@ -221,6 +221,13 @@ inline int tile_override() {
   return (v == 128 || v == 256) ? v : 0;
 }
 
+// Time of t work-groups, n at a time, of what a round of them takes; `few`, if
+// given, is a round's of no more than half as many.
+inline int64_t tile_cost(int t, int n, int64_t round, int64_t few = 0) {
+  const bool half = few != 0 && t % n != 0 && t % n <= n / 2;
+  return half ? t / n * round + few : (t + n - 1) / n * round;
+}
+
 // Row stride (elements) of the transposed rank-r activations (T^T, U^T).
 inline int tsave_ld(int M) { return (int)align_up(M, 64); }
 

@@ -343,30 +343,49 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
   // LoRA term: acc += U_tile . (s A)_tile^T, K = rp (At holds bf16(s A)^T),
   // accumulated straight into the MFMA accumulators.
   if (rp > 0) {
-    const BufRsrc rk = make_rsrc(keep, DROP ? (uint64_t)M * k : 0);
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    auto load_u = [&](int mb, int jb) {
       const int m = m0 + wm * WM + mb * 32 + l32;
+      return m < M ? *reinterpret_cast<const u32x4*>(U + (size_t)m * rp + jb + half * 8) : u32x4{0u, 0u, 0u, 0u};
+    };
+    auto load_at = [&](int nb, int jb) {
+      const int c = c0 + wn * WN + nb * 32 + l32;
+      return c < k ? *reinterpret_cast<const u32x4*>(At + (size_t)c * rp + jb + half * 8) : u32x4{0u, 0u, 0u, 0u};
+    };
+    if constexpr (DROP) {  // masked apart from the rest, a block at a time
+      const BufRsrc rk = make_rsrc(keep, (uint64_t)M * k);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int c = c0 + wn * WN + nb * 32 + l32;
-        f32x16 t;
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) t[e] = 0.0f;
-        for (int jb = 0; jb < rp; jb += 16) {
-          u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
-          if (m < M) a = *reinterpret_cast<const u32x4*>(U + (size_t)m * rp + jb + half * 8);
-          if (c < k) b = *reinterpret_cast<const u32x4*>(At + (size_t)c * rp + jb + half * 8);
-          if (DROP)
-            t = mfma32(a, b, t);
-          else
-            acc[mb][nb] = mfma32(a, b, acc[mb][nb]);
-        }
-        if (DROP) {
-          drop_block(t, rk, m0 + wm * WM + mb * 32, c, M, k, half, dscale);
+        for (int nb = 0; nb < NB; ++nb) {
+          f32x16 t;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] = 0.0f;
+          for (int jb = 0; jb < rp; jb += 16) t = mfma32(load_u(mb, jb), load_at(nb, jb), t);
+          drop_block(t, rk, m0 + wm * WM + mb * 32, c0 + wn * WN + nb * 32 + l32, M, k, half, dscale);
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[mb][nb][e] += t[e];
         }
+    } else {  // the next 16 ranks in flight
+      u32x4 a[MB], b[NB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) a[mb] = load_u(mb, 0);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) b[nb] = load_at(nb, 0);
+      for (int jb = 0; jb < rp; jb += 16) {
+        const int jn = jb + 16 < rp ? jb + 16 : jb;
+        u32x4 an[MB], bn[NB];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) an[mb] = load_u(mb, jn);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) bn[nb] = load_at(nb, jn);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma32(a[mb], b[nb], acc[mb][nb]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) a[mb] = an[mb];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) b[nb] = bn[nb];
       }
     }
   }

@@ -312,7 +312,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         bop[nb] = u32x4{0u, 0u, 0u, 0u};
-        if (nval[nb]) {
+        if ((r & 7) == 0) {  // eight ranks in a load
+          if (nval[nb] && jb + half * 8 < r) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(B + (size_t)nrow[nb] * r + jb + half * 8);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) bop[nb][p] = pack_bf16x2(s * bf16_lo(v[p]), s * bf16_hi(v[p]));
+          }
+        } else if (nval[nb]) {
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const int j = jb + half * 8 + 2 * p;

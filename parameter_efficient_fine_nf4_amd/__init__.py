@@ -537,6 +537,8 @@ def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, 
     rt = r * w.nsec
     codes = absmax = mask = dA = dB = T = None
     if r > 0:
+        if ck is None:
+            raise ValueError("an adapter's gradients need the checkpoint")
         ck.check(M, k, dev)
         codes, absmax, T = ck.codes.data_ptr(), ck.absmax.data_ptr(), T_saved
         if T is None or T.dtype is not torch.bfloat16 or T.numel() < rt * ((M + 63) // 64 * 64) \

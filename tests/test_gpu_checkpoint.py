@@ -220,6 +220,7 @@ def test_refusals_on_the_gpu(lib):
     w, A, B, X, dY = _layer(lib, 64, 128, 4, 3, 1, 8)
     Y, T, ck = lib.forward_checkpoint(X, w, A, B, 8.0)
     bad = [lambda: lib.backward_checkpoint(dY, ck, w, A, B, 8.0),                        # no T
+           lambda: lib.backward_checkpoint(dY, None, w, A, B, 8.0, T),
            lambda: lib.backward_checkpoint(dY, ck, w, A, B, 8.0, T[:, :3]),
            lambda: lib.backward_checkpoint(dY[:2], ck, w, A, B, 8.0, T),
            lambda: lib.backward_checkpoint(dY, ck, w, A[:, :64], B, 8.0, T),

@@ -450,3 +450,23 @@ def test_many_words_of_the_last_value(lib, V, dtype):
     a, b = lib.token_scores(many, top=64), lib.token_scores(z, top=64)
     for i in (0, 39):
         assert torch.equal(a[2][8 * i:8 * i + 8], b[2]) and torch.allclose(a[3][8 * i:8 * i + 8], b[3], rtol=0, atol=1e-4)
+
+
+def test_two_streams_at_once(lib):
+    _case("two streams")
+    sets = [(_logits(64, 40001, BF, 41), _tokens(64, 40001, 33, 41)), (_logits(64, 33000, F32, 42), _tokens(64, 33000, 2, 42))]
+
+    def call(z, y):
+        out = lib.token_scores(z, y, top=20, save_stats=True)
+        return *out, lib.token_scores_backward(torch.ones_like(out[0]), torch.full_like(out[1], -0.5), z, y, out[4])
+
+    want = [call(*s) for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(call(*s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))

@@ -48,16 +48,35 @@ __device__ __forceinline__ void drop_block(f32x16& t, const BufRsrc& rk, int row
   for (int e = 0; e < 16; ++e) t[e] *= kv[e] ? dscale : 0.0f;
 }
 
-// Mean of the section holding weight rows kc*64 .. kc*64 + 63 (sections of
-// dsec rows, dsec a multiple of 64, at most kMaxSections of them), from the
-// means held in registers.
-__device__ __forceinline__ float section_mean(const float (&mus)[kMaxSections], int kc, int dsec) {
-  const int sec = kc * kDxBK / dsec;
-  float m = mus[0];
-#pragma unroll
-  for (int i = 1; i < kMaxSections; ++i) m = sec == i ? mus[i] : m;
-  return m;
-}
+// Means of the sections of weight rows (dsec rows each, a multiple of 64).  The
+// compiler is kept from seeing the choice as one between elements of an array, of
+// which it makes an indexed one, in scratch memory (whose load waits for every
+// fetch in flight) or in LDS (whose place it works out from the dispatch packet, in
+// host memory: 10 us of a launch).
+struct SectionMeans {
+  float m0, m1, m2, m3;
+  uint32_t dsec;
+  __device__ __forceinline__ SectionMeans(const float* __restrict__ mean, int d, int dsec_) : dsec((uint32_t)dsec_) {
+    static_assert(kMaxSections == 4, "one member each");
+    const int last = d / dsec_ - 1;
+    m0 = mean[0];
+    m1 = mean[min(1, last)];
+    m2 = mean[min(2, last)];
+    m3 = mean[min(3, last)];
+  }
+  // of weight rows kc*64 .. kc*64 + 63; past the last section (3 dsec may be past 32
+  // bits then) the last one's
+  __device__ __forceinline__ float of(int kc) const {
+    const uint32_t n = (uint32_t)kc * kDxBK;
+    float a = m0, b = m1, c = m2, e = m3;
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm("" : "+s"(a), "+s"(b), "+s"(c), "+s"(e));
+#endif
+    b = n >= dsec ? b : a;
+    c = n >= 2 * dsec ? c : b;
+    return n >= 3 * dsec ? e : c;
+  }
+};
 
 // Placement of the 16-byte piece c (8 columns) of decoded weight row r inside
 // its row.  LDS serves a 16-byte store to eight lanes at a time over 128
@@ -115,9 +134,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
   const int kblocks = k / 64;
   // The contraction runs over all weight rows, so a K step's mean is that
   // of its section.
-  float mus[kMaxSections];
-#pragma unroll
-  for (int i = 0; i < kMaxSections; ++i) mus[i] = mean[min(i, d / dsec - 1)];
+  const SectionMeans means(mean, d, dsec);
   float qh[8];  // this lane's half of the levels, for build_lut_pair
 #pragma unroll
   for (int i = 0; i < 8; ++i) qh[i] = half ? tab.q[8 + i] : tab.q[i];
@@ -210,7 +227,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
       const int n = kc * kDxBK + brow[i], c = c0 + bblk[i] * 64;
       const bool ok = n < d && c < k;
       const uint32_t blk = (uint32_t)(ok ? n : 0) * (uint32_t)kblocks + (uint32_t)((ok ? c : 0) >> 6);
-      const float v = block_scale((W.q2[i] >> ((blk & 3u) * 8u)) & 0xFFu, W.q1[i], section_mean(mus, kc, dsec));
+      const float v = block_scale((W.q2[i] >> ((blk & 3u) * 8u)) & 0xFFu, W.q1[i], means.of(kc));
       lut[i] = build_lut_pair(qh, ok ? v : 0.0f);
     }
   };
@@ -470,9 +487,7 @@ __global__ __launch_bounds__(64 * kDx8Waves) __attribute__((amdgpu_waves_per_eu(
   const int kbase = sps > 0 ? split * sps : 0;
   const int ksteps = sps > 0 ? min(sps, d / kDxBK - kbase) : d / kDxBK;
   const int kblocks = k / 64;
-  float mus[kMaxSections];  // means of the sections of weight rows
-#pragma unroll
-  for (int i = 0; i < kMaxSections; ++i) mus[i] = mean[min(i, d / dsec - 1)];
+  const SectionMeans means(mean, d, dsec);
   float qh[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) qh[i] = half ? tab.q[8 + i] : tab.q[i];
@@ -539,7 +554,7 @@ __global__ __launch_bounds__(64 * kDx8Waves) __attribute__((amdgpu_waves_per_eu(
   };
   Lut lut;
   auto tables = [&](const WTile& W, int kc) {
-    lut = build_lut_pair(qh, block_scale((W.q2 >> (wblk * 8)) & 0xFFu, W.q1, section_mean(mus, kbase + kc, dsec)));
+    lut = build_lut_pair(qh, block_scale((W.q2 >> (wblk * 8)) & 0xFFu, W.q1, means.of(kbase + kc)));
   };
   uint32_t doff[4];
 #pragma unroll

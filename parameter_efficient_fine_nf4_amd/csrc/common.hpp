@@ -28,6 +28,7 @@ typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;  // 16 bytes at element alignment
 
 constexpr int kBlock = 64;    // weights per NF4 block constant
 constexpr int kGroup = 256;   // block constants per second-level scale

@@ -312,12 +312,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         bop[nb] = u32x4{0u, 0u, 0u, 0u};
-        if ((r & 7) == 0) {  // eight ranks in a load
-          if (nval[nb] && jb + half * 8 < r) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(B + (size_t)nrow[nb] * r + jb + half * 8);
+        if (nval[nb] && jb + half * 8 + 8 <= r) {  // eight ranks in a load, wherever the row starts
+          const u32x4 v = *reinterpret_cast<const u32x4_any*>(B + (size_t)nrow[nb] * r + jb + half * 8);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) bop[nb][p] = pack_bf16x2(s * bf16_lo(v[p]), s * bf16_hi(v[p]));
-          }
+          for (int p = 0; p < 4; ++p) bop[nb][p] = pack_bf16x2(s * bf16_lo(v[p]), s * bf16_hi(v[p]));
         } else if (nval[nb]) {
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -1601,8 +1599,22 @@ __device__ __forceinline__ void decode_finish(const float* __restrict__ part, in
       }
     }
   } else {
+    // eight ranks per load wherever the row starts, the last ones singly (rank by
+    // rank: 26 tokens, 9056 x 320, r = 50: 47 us a call, so 15)
 #pragma unroll
-    for (int j = 0; j < kMaxRank; ++j) bv[j] = (lora && j < r) ? bf16_to_f32(Bn[j]) : 0.0f;
+    for (int q = 0; q < kMaxRank / 8; ++q) {
+      if (lora && 8 * q + 8 <= r) {
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(Bn + 8 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          bv[8 * q + 2 * e] = bf16_lo(w[e]);
+          bv[8 * q + 2 * e + 1] = bf16_hi(w[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bv[8 * q + e] = (lora && 8 * q + e < r) ? bf16_to_f32(Bn[8 * q + e]) : 0.0f;
+      }
+    }
   }
   float y = 0.0f, t = 0.0f;
 #pragma unroll

@@ -11,9 +11,6 @@
 
 namespace qlora {
 
-// 16 bytes at element alignment.
-typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr double kLn2 = 0.69314718055994530942;
 constexpr float kNegInf = -__builtin_inff();

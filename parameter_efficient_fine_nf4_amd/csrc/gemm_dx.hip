@@ -865,7 +865,8 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
   } else {
     // Other shapes (every tile gives the same bits), as in the forward: a K step costs
     // a round of work-groups 2.05 us at 256 x 256, 1.05 at 128 x 128, at 64 x 128 0.8 or, two
-    // a CU, 1.15, at 64 x 64 0.65 or 0.95; its start and outputs 10, 4, 4 and 4 us.  M d k,
+    // a CU, 1.15, at 64 x 64 0.65 or 0.95; its start and outputs 10 (under dropout, whose
+    // masked term does not fit its registers, 60), 4, 4 and 4 us.  M d k,
     // us in the order of these tiles: 2849 x 7680 x 2880 251 / 358 / 329 / 379, 2000 x 4112
     // x 1088 135 / 69 / 74 / 94, 1001 x 1040 x 4160 46 / 42 / 37 / 42, 129 x 1040 x 4160 44 / 22
     // / 17 / 13.5.
@@ -875,7 +876,7 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
                w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, s, dX, t, keep, dscale)
     const int ntn = (w.k + 127) / 128, t64 = (M + 63) / 64;
     const int64_t ks = (w.d + kDxBK - 1) / kDxBK,
-                  cost[4] = {tile_cost(tiles256, 256, 41 * ks + 200),
+                  cost[4] = {tile_cost(tiles256, 256, 41 * ks + (DROP ? 1200 : 200)),
                              tile_cost(ntn * ((M + 127) / 128), 256, 21 * ks + 80),
                              tile_cost(ntn * t64, 512, 23 * ks + 100, 16 * ks + 80),
                              tile_cost(t64 * (w.k / 64), 512, 19 * ks + 80, 13 * ks + 70)};

@@ -17,9 +17,9 @@
 // B operands are then read with gfx950's transposing LDS read
 // (ds_read_b64_tr_b16: within each 16-lane group, lane i receives element
 // i % 4 of the 8-byte loads of lanes 4r + i / 4, r = 0..3), which turns four
-// rows x 16 columns into 16 lanes x four rows.  dY tiles (2 slots), decoded
-// weight tiles (2 slots) and packed codes with their block constants (3
-// slots, fetched three K steps ahead) live in swizzled LDS; every fetch
+// rows x 16 columns into 16 lanes x four rows.  dY tiles (2 or 3 slots), decoded
+// weight tiles (2 slots) and packed codes with their block constants
+// (a slot more, fetched as many K steps ahead) live in swizzled LDS; every fetch
 // is a buffer-addressed global->LDS load.  The LoRA term s U A is one more
 // MFMA pass in the epilogue, accumulating into the same registers, from U
 // (M x rp) and bf16(s A)^T, zero-padded (k x rp).
@@ -112,8 +112,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
   constexpr int kYBytes = BM * kDxBK * 2, kWBytes = kDxBK * ROWB;
   constexpr int kCWave = NP * 1024 + 512;   // per wave: codes, then c2 and c1 words
   constexpr int kCSlot = 4 * kCWave;
-  constexpr int kCOff = 2 * kYBytes;
-  constexpr int kSmem = kCOff + 3 * kCSlot;
+  // ring slots of dY and of the codes: one step's fetches fill a slot while YS - 1 are
+  // in flight (three of dY at 64 x 64: 300 x 9984 x 384 112 -> 84 us; 129 x 1040 x 4160
+  // 13.7 and 14.0; two a CU still fit)
+  constexpr int YS = BN == 64 ? 3 : 2, CS = YS + 1;
+  constexpr int kCOff = YS * kYBytes;
+  constexpr int kSmem = kCOff + CS * kCSlot;
   constexpr int kStage = 4 * WM * 64 * 2;
   static_assert(kStage <= kSmem, "output staging must fit");
   static_assert(kSmem + 2 * kWBytes <= 160 * 1024, "LDS");
@@ -265,8 +269,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
         boff[nb][q] = (uint32_t)(r * ROWB + (wslot(r, col >> 3) << 4) + (col & 7) * 2);
       }
   }
+  int ycur = 0;  // dY slot of the current step
   auto read_ab = [&](int ks, int st, u32x4 (&af)[MB], u32x4 (&bf)[NB]) {
-    const char* ys = smem + (ks & 1) * kYBytes;
+    const char* ys = smem + ycur * kYBytes;
     const char* ws = wsm + (ks & 1) * kWBytes + st * 16 * ROWB;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -287,12 +292,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
 
   // Pipeline.  K step ks multiplies dY tile ks by decoded tile ks while it
-  // (a) fetches dY tile ks+1 and the codes of step ks+3 (clamped to the last
-  // step, so every step issues kLoads fetches), spread between its MFMAs,
-  // and (b) decodes step ks+1 from codes fetched two steps earlier into the
+  // (a) fetches dY tile ks+YS-1 and the codes of step ks+YS+1 (clamped to the
+  // last step, so every step issues kLoads fetches), spread between its MFMAs,
+  // and (b) decodes step ks+1 from codes fetched YS steps earlier into the
   // other decoded-weight slot.  At the end of the step each wave waits until
-  // only its code fetches of this step are outstanding (its dY share of
-  // ks+1 and its codes of ks+2 have landed) and its LDS traffic is done;
+  // only its code fetches of this step (YS = 2; with YS = 3 all of this step's)
+  // are outstanding -- its dY share of ks+1 and its codes of ks+2 have landed --
+  // and its LDS traffic is done;
   // the barrier then publishes dY tile ks+1 and decoded tile ks+1 and frees
   // the slots of step ks.
   const auto clampk = [&](int x) { return x < ksteps ? x : ksteps - 1; };
@@ -304,23 +310,31 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
   for (int i = YCH; i < kLoads; ++i) dma_one(i, 0, 0, clampk(1), 1);   // codes of step 1
 #pragma unroll
   for (int i = YCH; i < kLoads; ++i) dma_one(i, 0, 0, clampk(2), 2);   // codes of step 2
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kCodeLoads) : "memory");
+#pragma unroll
+  for (int y = 1; y < YS - 1; ++y) {                                   // dY tile y, codes of step y + 2
+#pragma unroll
+    for (int i = 0; i < YCH; ++i) dma_one(i, clampk(y), y, 0, 0);
+#pragma unroll
+    for (int i = YCH; i < kLoads; ++i) dma_one(i, 0, 0, clampk(y + 2), y + 2);
+  }
+  constexpr int kAhead = (YS - 2) * kLoads;
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kCodeLoads + kAhead) : "memory");
   WTile W;
   read_w(0, W);
   tables(W, 0);
 #pragma unroll
   for (int wd = 0; wd < NW; ++wd) decode_word(W, wd, wsm);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCodeLoads) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCodeLoads + kAhead) : "memory");
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 
   constexpr int kPerSub = (kLoads + 2) / 3;
-  int csl_next = 1;  // code slot of step ks+1 (ring of three)
+  int csl_next = 1;  // code slot of step ks+1
   for (int ks = 0; ks < ksteps; ++ks) {
-    const int ky = clampk(ks + 1), kc = clampk(ks + 3), kd = clampk(ks + 1);
-    const int ysl = (ks + 1) & 1;
-    const int csl_far = csl_next == 0 ? 2 : csl_next - 1;  // slot of step ks (free)
+    const int ky = clampk(ks + YS - 1), kc = clampk(ks + CS), kd = clampk(ks + 1);
+    const int ysl = ycur == 0 ? YS - 1 : ycur - 1;
+    const int csl_far = csl_next == 0 ? CS - 1 : csl_next - 1;  // slot of step ks (free)
     char* wnext = wsm + ((ks + 1) & 1) * kWBytes;
     u32x4 af[2][MB], bf[2][NB];
     read_ab(ks, 0, af[0], bf[0]);
@@ -348,11 +362,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCodeLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(YS == 2 ? kCodeLoads : (YS - 2) * kLoads) : "memory");
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    csl_next = csl_next == 2 ? 0 : csl_next + 1;
+    ycur = ycur == YS - 1 ? 0 : ycur + 1;
+    csl_next = csl_next == CS - 1 ? 0 : csl_next + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();

@@ -145,10 +145,11 @@ struct OnlineSums {
   float m = kNegInf;
   double K = 0.0;
   Sums sum{0.0f, 0.0f};
-  // the sums so far, relative to another K
+  // the sums so far, relative to another K; of masked words alone they are 0 to any, or
+  // a NaN that was among them
   __device__ __forceinline__ Sums at(double to) const {
     const float d = fmaxf((float)(K - to), kFloor), f = exp2_hw(d);
-    return m == kNegInf ? Sums{0.0f, 0.0f} : Sums{sum.s * f, f * fmaf(d, sum.s, sum.u)};
+    return m == kNegInf ? sum : Sums{sum.s * f, f * fmaf(d, sum.s, sum.u)};
   }
   // raises the maximum; k, ref and far of the terms to come
   __device__ __forceinline__ void raise(float mx, const Scale& c, float& k, float& ref, bool& far) {

@@ -541,9 +541,10 @@ def backward_checkpoint(dY: torch.Tensor, ck: Checkpoint, w: NF4Weight, A=None, 
             raise ValueError("an adapter's gradients need the checkpoint")
         ck.check(M, k, dev)
         codes, absmax, T = ck.codes.data_ptr(), ck.absmax.data_ptr(), T_saved
-        if T is None or T.dtype is not torch.bfloat16 or T.numel() < rt * ((M + 63) // 64 * 64) \
-                or not T.is_contiguous() or T.device != dev:
-            raise ValueError("T_saved is the T that the forward returned")
+        ldt = (M + 63) // 64 * 64  # a T of another M has other rows: ranks would be read from wrong places
+        if T is None or T.dtype is not torch.bfloat16 or not T.is_contiguous() or T.device != dev \
+                or M > 0 and T.shape != (rt, ldt) and T.shape != (rt * ldt,):
+            raise ValueError(f"T_saved is the T that the forward returned: {rt} x {ldt}, torch.bfloat16, on {dev}")
         if keep is not None:
             _dense("keep", keep, torch.uint8, (M, k), dev)
             mask = keep.data_ptr()

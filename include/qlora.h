@@ -556,7 +556,9 @@ int qlora_policy_loss(const void *logits, int32_t dtype, int64_t T, int64_t V, i
  *   entropy  device, T fp32, written.
  *   top_ids, top_logp   device, T x n int32 and fp32, written (NULL if n == 0).
  *   stats    device, T x 3 fp32, written (may be NULL in the forward): what
- *            the backward needs of each row.
+ *            the backward needs of each row, for the forward's tokens or
+ *            others.  A row that was not read has none: its gradient is NaN
+ *            if it is asked for with a token that counts.
  *   dlogp    device, T x m fp32 (not read where a token does not count).
  *   dentropy device, T fp32, or NULL: the loss has no entropy term.
  *   dlogits, ldd   as in qlora_token_logprobs_backward: whole rows, may be the

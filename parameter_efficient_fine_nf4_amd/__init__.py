@@ -809,7 +809,9 @@ def token_scores_backward(dlogp: torch.Tensor | None, dentropy: torch.Tensor | N
     (fp32 [T], None for a loss without it).  ``out`` as in
     ``token_logprobs_backward`` (it may be the logits).  A loss on the top
     alternatives gives their ids as tokens: an id of -1 does not count, and
-    one that is there twice gets both gradients."""
+    one that is there twice gets both gradients.  A row of which the forward
+    read nothing has no statistics: a token that counts there makes its
+    gradient NaN."""
     T, V, ld = _rows(logits)
     dev = logits.device
     y, m, _ = _tokens(tokens, T, dev)

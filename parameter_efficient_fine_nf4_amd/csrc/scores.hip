@@ -416,9 +416,9 @@ __global__ __launch_bounds__(T) void k_scores(ScoreArgs a) {
     }
     if (threadIdx.x == 0) {
       a.entropy[t] = 0.0f;
-      if (a.stats != nullptr) {
-        a.stats[3 * t] = 0.0f;
-        a.stats[3 * t + 1] = 1.0f;
+      if (a.stats != nullptr) {  // none: with these a gradient of other tokens is 0 / 0
+        a.stats[3 * t] = -kNegInf;
+        a.stats[3 * t + 1] = 0.0f;
         a.stats[3 * t + 2] = 0.0f;
       }
     }

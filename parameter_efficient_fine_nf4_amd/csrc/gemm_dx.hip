@@ -23,8 +23,6 @@
 // is a buffer-addressed global->LDS load.  The LoRA term s U A is one more
 // MFMA pass in the epilogue, accumulating into the same registers, from U
 // (M x rp) and bf16(s A)^T, zero-padded (k x rp).
-#include <algorithm>
-
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -895,7 +893,7 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
                              tile_cost(ntn * ((M + 127) / 128), 256, 21 * ks + 80),
                              tile_cost(ntn * t64, 512, 23 * ks + 100, 16 * ks + 80),
                              tile_cost(t64 * (w.k / 64), 512, 19 * ks + 80, 13 * ks + 70)};
-    switch (forced != 0 ? (forced == 256 ? 0 : 1) : (int)(std::min_element(cost, cost + 4) - cost)) {
+    switch (tile_choice<4>({{256, 256}, {128, 128}, {64, 128}, {64, 64}}, cost)) {
       case 0: QLORA_DX(256, 256); break;
       case 1: QLORA_DX(128, 128); break;
       case 2: QLORA_DX(64, 128); break;

@@ -34,8 +34,6 @@
 //   fixed order, adds s T B^T and rounds to bf16.
 #include <string.h>
 
-#include <algorithm>
-
 #include "checkpoint.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -1948,7 +1946,7 @@ hipError_t launch_forward(const uint16_t* X, int M, const Nf4Dev& w, int nsec, c
                                              tile_cost(ntn * ((M + 127) / 128), 256, 23 * ks + 100),
                                              tile_cost(ntn128 * ((M + 127) / 128), 256, 18 * ks + 80),
                                              tile_cost(ntn128 * ((M + 63) / 64), 512, 23 * ks + 60, 14 * ks + 60)};
-    switch (tile_override() != 0 ? (tile_override() == 256 ? 0 : 1) : (int)(std::min_element(cost, cost + 4) - cost)) {
+    switch (tile_choice<4>({{256, 256}, {128, 256}, {128, 128}, {64, 128}}, cost)) {
       case 0: QLORA_RICH(256, 2); break;
       case 1: QLORA_RICH(128, 2); break;
       case 2: QLORA_RICH(128, 1); break;

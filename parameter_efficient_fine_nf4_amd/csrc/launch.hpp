@@ -7,6 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 #include <stdlib.h>
+#include <string.h>
+
+#include <algorithm>
 
 #include "common.hpp"
 
@@ -212,20 +215,37 @@ hipError_t launch_muon(uint16_t* P, float* W, const uint16_t* G, float* m, int64
                        float lr, float momentum, int nesterov, float wd, float scale, float eps, const MuonCoef& co,
                        void* ws, hipStream_t st);
 
-// Tile height forced through the environment (QLORA_TILE=128 or 256) for
-// tests of each variant on small shapes; 0 = choose by shape.
-inline int tile_override() {
+// Tile forced through the environment for tests of each variant on small shapes:
+// QLORA_TILE=128 or 256 its height, QLORA_TILE=64x128 its rows and columns where a
+// kernel has that one; 0 = choose by shape.
+struct Tile {
+  int rows, cols;
+};
+inline Tile tile_forced() {
   const char* e = getenv("QLORA_TILE");
-  if (e == nullptr) return 0;
+  if (e == nullptr) return {0, 0};
   const int v = atoi(e);
-  return (v == 128 || v == 256) ? v : 0;
+  if (v != 64 && v != 128 && v != 256) return {0, 0};
+  const char* x = strchr(e, 'x');
+  return {v, x != nullptr ? atoi(x + 1) : 0};
 }
+inline int tile_override() { return tile_forced().rows; }
 
 // Time of t work-groups, n at a time, of what a round of them takes; `few`, if
 // given, is a round's of no more than half as many.
 inline int64_t tile_cost(int t, int n, int64_t round, int64_t few = 0) {
   const bool half = few != 0 && t % n != 0 && t % n <= n / 2;
   return half ? t / n * round + few : (t + n - 1) / n * round;
+}
+
+// Which of a kernel's tiles: the forced one if it is there, else the one of the
+// least cost.
+template <int N>
+inline int tile_choice(const Tile (&tiles)[N], const int64_t (&cost)[N]) {
+  const Tile f = tile_forced();
+  for (int i = 0; i < N; ++i)
+    if (f.rows == tiles[i].rows && (f.cols == 0 || f.cols == tiles[i].cols)) return i;
+  return (int)(std::min_element(cost, cost + N) - cost);
 }
 
 // Row stride (elements) of the transposed rank-r activations (T^T, U^T).

@@ -652,7 +652,11 @@ static int backward_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const
     // launch writes bf16(s A)^T for the dX epilogue.  B is read as stored
     // when r is a multiple of 8, else from a transposed copy.  With
     // sections, U's ranks of section p sum over that section's columns of
-    // dY only.
+    // dY only.  U, a sum in fp32, is rounded to bf16 as an operand of the matrix units
+    // (dX's s U A, dA's s U^T X), as T is by the forward: 2^-8 of it at most, 0.0017 in
+    // the mean square, beside the same of the gradient's own rounding (dA and dB of a
+    // step: 0.0024 from their formula in 64 bits in place of 0.0017).  Operands of more
+    // bits would take the products twice.
     if (r % 8 == 0) {
       e = launch_lora_proj(dY, (int)M, (int)d, B, true, rt, nsec, w.U, w.Ut, ldt, w.proj, A, (int)k, s, w.At, st);
     } else {

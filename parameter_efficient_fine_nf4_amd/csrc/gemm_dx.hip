@@ -62,8 +62,8 @@ struct SectionMeans {
     m2 = mean[min(2, last)];
     m3 = mean[min(3, last)];
   }
-  // of weight rows kc*64 .. kc*64 + 63; past the last section (3 dsec may be past 32
-  // bits then) the last one's
+  // of weight rows kc*64 .. kc*64 + 63; past the last section the last one's (k >= 64
+  // and d k < 2^31: no row's number, and no multiple of dsec here, leaves 27 bits)
   __device__ __forceinline__ float of(int kc) const {
     const uint32_t n = (uint32_t)kc * kDxBK;
     float a = m0, b = m1, c = m2, e = m3;
@@ -111,8 +111,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, BM >= 12
   constexpr int kCWave = NP * 1024 + 512;   // per wave: codes, then c2 and c1 words
   constexpr int kCSlot = 4 * kCWave;
   // ring slots of dY and of the codes: one step's fetches fill a slot while YS - 1 are
-  // in flight (three of dY at 64 x 64: 300 x 9984 x 384 112 -> 84 us; 129 x 1040 x 4160
-  // 13.7 and 14.0; two a CU still fit)
+  // in flight (three of dY at 64 x 64: 300 x 9984 x 384 112 -> 83 us, but 3 x 9984 x 384 83
+  // -> 87; 129 x 1040 x 4160 13.7 and 14.0; two a CU still fit)
   constexpr int YS = BN == 64 ? 3 : 2, CS = YS + 1;
   constexpr int kCOff = YS * kYBytes;
   constexpr int kSmem = kCOff + CS * kCSlot;
@@ -876,13 +876,16 @@ static hipError_t launch_dx_t(const uint16_t* dY, int M, const Nf4Dev& w, const 
                    st, dY, M, w.codes, w.c2, w.c1, w.mean, w.d, w.k, w.dsec, U, At, rp, dX, t, c256 * 256, c128, keep,
                    dscale, 0, nullptr);
   } else {
-    // Other shapes (every tile gives the same bits), as in the forward: a K step costs
-    // a round of work-groups 2.05 us at 256 x 256, 1.05 at 128 x 128, at 64 x 128 0.8 or, two
-    // a CU, 1.15, at 64 x 64 0.65 or 0.95; its start and outputs 10 (under dropout, whose
-    // masked term does not fit its registers, 60), 4, 4 and 4 us.  M d k,
-    // us in the order of these tiles: 2849 x 7680 x 2880 251 / 358 / 329 / 379, 2000 x 4112
-    // x 1088 135 / 69 / 74 / 94, 1001 x 1040 x 4160 46 / 42 / 37 / 42, 129 x 1040 x 4160 44 / 22
-    // / 17 / 13.5.
+    // Other shapes (every tile gives the same bits), as in the forward: a K step is
+    // reckoned to cost a round of work-groups 2.05 us at 256 x 256, 1.05 at 128 x 128, at 64
+    // x 128 0.8 or, two a CU, 1.15, at 64 x 64 0.65 or 0.95; its start and outputs 10 (under
+    // dropout, whose masked term does not fit its registers, 60), 4, 4 and 4 us.  M d k, us
+    // in the order of these tiles, without an adapter: 2849 x 7680 x 2880 235 / 352 / 300 /
+    // 345, 2000 x 4112 x 1088 130 / 66 / 70 / 80, 1001 x 1040 x 4160 42 / 40 / 35 / 39, 129 x
+    // 1040 x 4160 41 / 20.5 / 16.5 / 13.4, 20000 x 9984 x 64 302 / 190 / 174 / 120.  64 x 64
+    // takes less than it is reckoned (0.52 and 0.72 us a step since it has three slots of
+    // dY; its entry is of two): with 257 to 512 of its tiles it is passed over where it would
+    // be the best, by 8 % at the most (4000 x 9984 x 320: 122 against 113 us).
 #define QLORA_DX(BM, BN)                                                                                    \
   QLORA_LAUNCH("dx", st, (k_dx<BM, BN, DROP>),                                                              \
                dim3((unsigned)(((M + BM - 1) / BM) * ((w.k + BN - 1) / BN))), dim3(256), 0, st, dY, M,      \

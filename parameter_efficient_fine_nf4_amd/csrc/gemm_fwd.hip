@@ -1931,12 +1931,13 @@ hipError_t launch_forward(const uint16_t* X, int M, const Nf4Dev& w, int nsec, c
     }
   } else {
     // Other shapes (every tile gives the same bits).  What a K step costs a round of
-    // work-groups, one a CU, hardly depends on how many of its rows are there: 1.6 us
-    // at 256 x 256, 1.15 at 128 x 256, 0.9 at 128 x 128, and at 64 x 128 0.7 or, two a CU,
-    // 1.15; its start and outputs are 8, 5, 4 and 3 us.  The tile with the least of it (M
-    // d k, us in the order of these tiles): 800 x 10960 x 4160 101 / 144 / 158 / 163, 4000 x
-    // 2000 x 2112 56 / 46 / 69 / 76, 500 x 5008 x 448 - / 19.1 / 14.7 / 15.2, 1001 x 1040 x 4160
-    // - / 76 / 58 / 49.
+    // work-groups, one a CU, hardly depends on how many of its rows are there.  It is
+    // reckoned, for CUs that all have one, at 1.6 us at 256 x 256, 1.15 at 128 x 256, 0.9 at
+    // 128 x 128, and at 64 x 128 at 0.7 or, two a CU, 1.15; its start and outputs at 8, 5, 4
+    // and 3 us (of few work-groups each step takes some 0.8 of that).  The tile with the
+    // least of it (M d k, us in the order of these tiles, without an adapter): 800 x 10960
+    // x 4160 99 / 141 / 139 / 144, 4000 x 2000 x 2112 55 / 44 / 54 / 59, 500 x 5008 x 448 19.1 /
+    // 13.4 / 9.9 / 10.2, 1001 x 1040 x 4160 91 / 65 / 47 / 38.4.
 #define QLORA_RICH(BM, NB)                                                                                       \
   QLORA_LAUNCH("fwd_rich", st, (k_fwd_rich<BM, NB>),                                                             \
                dim3((unsigned)(((w.d + 128 * NB - 1) / (128 * NB)) * ((M + BM - 1) / BM))), dim3(256), 0, st, X, \

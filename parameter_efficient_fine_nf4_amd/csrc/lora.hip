@@ -1058,10 +1058,12 @@ __device__ __forceinline__ void tokred_strip_ck(const RedJobCk& J, int block, in
 // and of dB the sections' columns of dY.  (As launches of their own, with few
 // strips each: 5569 tokens, 3 sections of 256 x 64 at r = 48: 78 us; in one 27.)
 // 4096 tokens, 4096 x 4096, r = 16: 14.5 us, 53 MB at 3.6 TB/s; 8192 x 22016, r = 64: 71
-// us, 181 MB at 2.5 TB/s.  Bound by the requests that the strips' short pieces of rows
-// make of the L2 (the address units are busy 60 % of the time); deeper rings, and
-// ranges of tokens whose work-groups share Z in LDS, took as long or longer (24 and
-// 27.5 us with U's projection).
+// us, 181 MB at 2.5 TB/s.  Of the cycles in which the CUs have waves, the address units
+// are busy in 84 % (92 % at the larger) and two thirds of that wait for the L1, with
+// 1.6 (6.2) million requests of the L2, three quarters of which hit there: bound by the
+// short pieces of rows that the strips read.  Deeper rings, and ranges of tokens whose
+// work-groups share Z in LDS, took as long or longer (24 and 27.5 us with U's
+// projection).
 struct RedCk {
   const uint16_t* Ut;      // nsec r x ldz
   const uint8_t* codes;    // M x k
